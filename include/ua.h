@@ -72,13 +72,20 @@ typedef enum {
   UA_ERR_UNSUPPORTED = 2,  /* a valid combination this build has no kernel for */
   UA_ERR_CUDA = 3,         /* a CUDA runtime call failed (launch, allocation, query) */
   UA_ERR_WORKSPACE = 4,    /* the caller's workspace is smaller than ua_plan() asks */
-  UA_ERR_DEVICE_CHECK = 5, /* a kernel saw a block id outside [0, num_blocks) */
+  UA_ERR_DEVICE_CHECK = 5, /* a kernel saw a block id outside [0, num_blocks), or ua_append_kv a
+                              position outside the rotation table */
   UA_ERR_TIMEOUT = 6,      /* a kernel gave up waiting on its own copy pipeline */
   UA_ERR_SCRATCH_LIMIT = 7 /* ua_unified_attention_noalloc: the call needs more scratch than
                               its fixed UA_NOALLOC_SCRATCH_BYTES */
 } ua_status_t;
 
-typedef enum { UA_DT_F16 = 0, UA_DT_BF16 = 1, UA_DT_F8E4M3 = 2, UA_DT_F32 = 3 } ua_dtype_t;
+typedef enum {
+  UA_DT_F16 = 0,
+  UA_DT_BF16 = 1,
+  UA_DT_F8E4M3 = 2,
+  UA_DT_F32 = 3,
+  UA_DT_I8 = 4 /* caches only: signed codes -127 .. 127 with a scale per block and kv-head */
+} ua_dtype_t;
 
 typedef enum {
   UA_BACKEND_AUTO = 0,  /* dispatcher picks from grid fill and key-walk length */
@@ -221,6 +228,91 @@ int ua_unified_attention_noalloc(const void* q, const void* k_cache, const void*
                                  const float* alibi_slopes, const float* qq_bias,
                                  const float* sinks, int kv_dtype, const float* kv_scale,
                                  int backend, void* stream, const ua_shape_t* shape);
+
+/*
+ * One ua_append_kv call: what to write, where, and how it is rotated.  Sizes are host ints;
+ * tensors are device memory.  Strides are in elements.
+ */
+typedef struct {
+  const void* k;       /* [total_q, num_kv_heads, head_dim] of `dtype`, strides k_stride */
+  const void* v;       /* likewise, v_stride */
+  const void* q;       /* [total_q, num_q_heads, head_dim] to rotate, or NULL */
+  void* q_out;         /* the rotated queries, q_out_stride (may be q itself) */
+  void* k_cache;       /* [num_blocks, block_size, num_kv_heads, head_dim] kv_dtype, contiguous */
+  void* v_cache;
+  const int32_t* cu_seqlens_q;  /* [num_seqs + 1] */
+  const int32_t* seq_lens_k;    /* [num_seqs]: lengths with the new tokens */
+  const int32_t* block_table;   /* [num_seqs, max_blocks_per_seq] */
+  const float* cos_sin;         /* [max_position, rot_dim]: a row's rot_dim / 2 cosines, then its
+                                   sines; 16-byte aligned; NULL: no rotation (rot_dim 0) */
+  const int32_t* positions;     /* [n_axes][total_q], or NULL: a token's place in the cache */
+  const float* kv_scale;        /* e4m3 cache, per tensor: {k_scale, v_scale} */
+  float* k_scale_tok;           /* e4m3 cache, per token: written at (block, slot, kv-head) */
+  float* v_scale_tok;
+  float* k_scale_blk;           /* e4m3 or int8 cache, per block: updated at (block, kv-head) */
+  float* v_scale_blk;
+  int64_t q_stride[2];          /* token, head: multiples of 8; the head dim has stride 1 */
+  int64_t k_stride[2];
+  int64_t v_stride[2];
+  int64_t q_out_stride[2];
+  int64_t k_scale_tok_stride[3];
+  int64_t v_scale_tok_stride[3];
+  int64_t k_scale_blk_stride[2];
+  int64_t v_scale_blk_stride[2];
+  int64_t positions_stride;     /* from one axis' positions to the next's */
+  int32_t num_seqs;
+  int32_t total_q;
+  int32_t max_seqlen_q;         /* >= every q_len */
+  int32_t max_blocks_per_seq;
+  int32_t num_blocks;
+  int32_t block_size;
+  int32_t num_q_heads;          /* 0 without q */
+  int32_t num_kv_heads;
+  int32_t head_dim;             /* 64, 128 or 256 */
+  int32_t dtype;                /* of q, k, v and q_out: F16 or BF16 */
+  int32_t kv_dtype;             /* of the caches: `dtype`, F8E4M3 or I8 */
+  int32_t rot_dim;              /* rotated elements at a head's front: a multiple of 16, 0 .. head_dim */
+  int32_t max_position;         /* rows of cos_sin */
+  int32_t interleaved;          /* pairs: 0: (f, f + rot_dim / 2); 1: (2 f, 2 f + 1) */
+  int32_t n_axes;               /* 1 .. 4 (1 without positions) */
+  const uint8_t* axis_of;       /* n_axes > 1: host array [rot_dim / 2], the axis of each frequency */
+} ua_append_t;
+
+/*
+ * ua_append_kv -- appends the batch's new keys and values to the paged cache, the keys rotated
+ * by their position on the way, and rotates the queries beside them, in one launch.  (The
+ * pages describe the cache that ua_unified_attention reads; this call writes it.)
+ *
+ * Token i of sequence b goes to cache position seq_lens_k[b] - q_len + i; its slot follows
+ * from the block table, as ua_unified_attention reads it.  With cos_sin, pair f = 0 ..
+ * rot_dim / 2 - 1 of each q and k head turns by the angle in row positions[axis_of[f]][token]
+ * (or, without positions, the cache position):
+ *   a' = a cos - b sin,  b' = b cos + a sin      fp32, every product and sum rounded on its own
+ * and elements from rot_dim on pass through.  What is stored, with x the fp32 value:
+ *   16-bit cache        x rounded once
+ *   e4m3, kv_scale      rne(x * (1 / scale)), saturating at 448
+ *   e4m3, *_scale_tok   scale = amax * (1 / 448) of the token's head, within [2^-40, 2^40];
+ *                       written beside the codes
+ *   *_scale_blk         one scale for each block and kv-head, qmax 448 (e4m3) or 127 (int8):
+ *                       s = amax over the block's new tokens * (1 / qmax), within [2^-40,
+ *                       2^40], or the block's present scale if it holds tokens of the sequence
+ *                       already and that is larger.  New codes are rne(x * (1 / s)); codes
+ *                       held already become rne(code * (present / s)) when s grew.
+ * Slots past the new tokens, and blocks that no new token reaches, keep what they hold (a
+ * block's slots past kv_len too).  Values must be finite where a scale is computed.  A block
+ * reached by two sequences of one call, or twice by one, is the caller's error.
+ *
+ * A token whose cache position is negative (kv_len < q_len) is skipped, as are rows of k, v
+ * and q past cu_seqlens_q[num_seqs].  A block id outside [0, num_blocks) or past the table's
+ * row is not written; a position outside [0, max_position) skips its token, queries included;
+ * both raise UA_ERR_DEVICE_CHECK in the device status word.
+ *
+ * Asynchronous on `stream`, capturable, no workspace, no allocation.  Returns UA_OK or
+ * UA_ERR_INVALID_ARG (a missing or misaligned pointer, a size, stride or enum value that is
+ * not accepted, scales that do not fit the cache's type), UA_ERR_UNSUPPORTED (a 16-bit cache
+ * of another type than k and v), UA_ERR_CUDA.
+ */
+int ua_append_kv(const ua_append_t* call, void* stream);
 
 /*
  * ua_plan -- the dispatcher's decision for a call with these sizes, without touching

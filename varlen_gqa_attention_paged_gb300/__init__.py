@@ -2,7 +2,8 @@
 
 Python binding of the C ABI in ``include/ua.h``: it only turns torch tensors into
 device pointers, the current CUDA stream and host-side sizes, and calls
-``ua_unified_attention`` in ``libua.so``.  Every step of the computation runs in the
+``ua_append_kv`` (new keys and values into the paged cache, rotated by position) and
+``ua_unified_attention`` (attention over it) in ``libua.so``.  Every step of the computation runs in the
 library's CUDA kernels; without the built library this module raises.
 """
 from __future__ import annotations
@@ -14,14 +15,15 @@ import torch
 
 from . import _lib
 from ._lib import (UA_BACKEND_2D, UA_BACKEND_AUTO, UA_BACKEND_SPLIT, UA_DT_BF16, UA_DT_F8E4M3,
-                   UA_DT_F16, UA_DT_F32, UA_PATH_2D, UA_PATH_SPLIT)
+                   UA_DT_F16, UA_DT_F32, UA_DT_I8, UA_PATH_2D, UA_PATH_SPLIT)
 
-__all__ = ["unified_attention", "prepare", "PreparedAttention", "plan", "device_status",
-           "device_status_reset", "UaError", "BACKENDS", "library_path"]
+__all__ = ["unified_attention", "prepare", "PreparedAttention", "append_kv", "prepare_append",
+           "PreparedAppend", "rope_table", "plan", "device_status", "device_status_reset", "UaError", "BACKENDS", "library_path"]
 
 BACKENDS = {"auto": UA_BACKEND_AUTO, "2d": UA_BACKEND_2D, "split": UA_BACKEND_SPLIT}
 _DTYPES = {torch.float16: UA_DT_F16, torch.bfloat16: UA_DT_BF16,
-           torch.float8_e4m3fn: UA_DT_F8E4M3, torch.float32: UA_DT_F32}
+           torch.float8_e4m3fn: UA_DT_F8E4M3, torch.float32: UA_DT_F32,
+           torch.int8: UA_DT_I8}
 
 
 class UaError(RuntimeError):
@@ -214,6 +216,244 @@ def prepare(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *, max_s
     prep._static = (k_cache, v_cache, alibi_slopes, qq_bias, sinks, kv_scale, k_scale_tok,
                     v_scale_tok, workspace)
     return prep
+
+
+def rope_table(max_position: int, rot_dim: int, *, base: float = 10000.0, inv_freq=None,
+               device="cuda") -> torch.Tensor:
+    """The rotation table of :func:`append_kv`: float32 [max_position, rot_dim], row p the
+    cosines of p * f for the rot_dim / 2 frequencies f, then the sines.  f is
+    base^(-2 i / rot_dim), or ``inv_freq`` (rot_dim / 2 values, for scaled variants).  The
+    angles are taken in 64 bits: fp32 products are off by whole radians at far positions."""
+    if rot_dim <= 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be a positive even number")
+    if inv_freq is None:
+        i = torch.arange(rot_dim // 2, dtype=torch.float64, device=device)
+        inv_freq = base ** (-2.0 * i / rot_dim)
+    else:
+        inv_freq = torch.as_tensor(inv_freq, dtype=torch.float64, device=device)
+        if tuple(inv_freq.shape) != (rot_dim // 2,):
+            raise ValueError("inv_freq must hold rot_dim / 2 frequencies")
+    a = torch.arange(max_position, dtype=torch.float64, device=device)[:, None] * inv_freq
+    return torch.cat([torch.cos(a), torch.sin(a)], dim=1).to(torch.float32)
+
+
+def _rows3(name, t, total_q, d, dtype, device):
+    if t.dim() != 3 or t.shape[0] != total_q or t.shape[2] != d:
+        raise ValueError(f"{name} must be [total_q, heads, head_dim]")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must have k's dtype and device")
+    if t.stride(2) != 1 or t.stride(0) % 8 or t.stride(1) % 8:
+        raise ValueError(f"{name}: the head dim must be contiguous, the other strides "
+                         "multiples of 8 elements")
+
+
+def _append_call(k, v, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, max_seqlen_q,
+                 q, q_out, cos_sin, positions, axis_of, interleaved, kv_scale, k_scale_tok,
+                 v_scale_tok, k_scale_blk, v_scale_blk):
+    """Checks the tensors of an append_kv call; returns its UaAppend and what it points at."""
+    if k.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("k must be [total_q, H_kv, D] and k_cache [blocks, block_size, H_kv, D]")
+    total_q, hkv, d = k.shape
+    num_blocks, block_size = k_cache.shape[:2]
+    dev = k.device
+    if not k.is_cuda:
+        raise ValueError("k must be a CUDA tensor")
+    if v_cache.shape != k_cache.shape or tuple(k_cache.shape[2:]) != (hkv, d):
+        raise ValueError("k, k_cache and v_cache disagree on shape")
+    if v.shape != k.shape:
+        raise ValueError("k and v disagree on shape")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not t.is_contiguous() or t.dtype != k_cache.dtype or t.device != dev:
+            raise ValueError(f"{name} must be contiguous, on k's device, of the caches' dtype")
+    for name, t in (("cu_seqlens_q", cu_seqlens_q), ("seq_lens_k", seq_lens_k),
+                    ("block_table", block_table)):
+        if t.dtype != torch.int32 or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{name} must be a contiguous int32 tensor on k's device")
+    num_seqs = cu_seqlens_q.numel() - 1
+    if num_seqs < 0 or seq_lens_k.numel() != num_seqs or block_table.dim() != 2 or \
+            block_table.shape[0] != num_seqs:
+        raise ValueError("cu_seqlens_q [S + 1], seq_lens_k [S] and block_table [S, blocks] "
+                         "disagree on the number of sequences")
+    _rows3("k", k, total_q, d, k.dtype, dev)
+    _rows3("v", v, total_q, d, k.dtype, dev)
+    a = _lib.UaAppend()
+    if q is not None:
+        _rows3("q", q, total_q, d, k.dtype, dev)
+        if q_out is None:
+            q_out = torch.empty(tuple(q.shape), dtype=q.dtype, device=dev)
+        _rows3("q_out", q_out, total_q, d, k.dtype, dev)
+        if q_out.shape != q.shape:
+            raise ValueError("q and q_out disagree on shape")
+        a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
+        a.q_stride = (ctypes.c_int64 * 2)(*q.stride()[:2])
+        a.q_out_stride = (ctypes.c_int64 * 2)(*q_out.stride()[:2])
+        a.num_q_heads = q.shape[1]
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    a.k, a.v = k.data_ptr(), v.data_ptr()
+    a.k_stride = (ctypes.c_int64 * 2)(*k.stride()[:2])
+    a.v_stride = (ctypes.c_int64 * 2)(*v.stride()[:2])
+    a.k_cache, a.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
+    a.cu_seqlens_q, a.seq_lens_k = cu_seqlens_q.data_ptr(), seq_lens_k.data_ptr()
+    a.block_table = block_table.data_ptr()
+    axes = None
+    a.n_axes = 1
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.device != dev or \
+                not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous float32 [max_position, rot_dim] tensor "
+                             "on k's device (see rope_table)")
+        a.cos_sin = cos_sin.data_ptr()
+        a.max_position, a.rot_dim = cos_sin.shape
+        if a.rot_dim % 16 or not 0 < a.rot_dim <= d:
+            raise ValueError("rot_dim must be a multiple of 16 within 16 .. head_dim")
+    elif positions is not None or axis_of is not None:
+        raise ValueError("positions and axis_of need cos_sin")
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.device != dev or \
+                positions.dim() not in (1, 2) or positions.shape[-1] != total_q or \
+                (positions.numel() and positions.stride(-1) != 1):
+            raise ValueError("positions must be int32 [total_q] or [axes, total_q] on k's device")
+        if positions.dim() == 2:
+            a.n_axes = positions.shape[0]
+            a.positions_stride = positions.stride(0)
+        a.positions = positions.data_ptr()
+    if axis_of is not None:
+        axes = bytes(axis_of)
+        if len(axes) != a.rot_dim // 2 or (axes and max(axes) >= a.n_axes):
+            raise ValueError("axis_of names an axis of positions for each of the rot_dim / 2 "
+                             "frequencies")
+    elif a.n_axes > 1:
+        raise ValueError("positions of several axes need axis_of")
+    if axes is not None:
+        axes = ctypes.create_string_buffer(axes, len(axes))
+        a.axis_of = ctypes.addressof(axes)
+    if kv_scale is not None:
+        if kv_scale.dtype != torch.float32 or kv_scale.device != dev or kv_scale.numel() != 2 or \
+                not kv_scale.is_contiguous():
+            raise ValueError("kv_scale must be float32 [2] on k's device")
+        a.kv_scale = kv_scale.data_ptr()
+    for form, ks, vs, shape in (("tok", k_scale_tok, v_scale_tok, (num_blocks, block_size, hkv)),
+                                ("blk", k_scale_blk, v_scale_blk, (num_blocks, hkv))):
+        if (ks is None) != (vs is None):
+            raise ValueError(f"give both k_scale_{form} and v_scale_{form}, or neither")
+        if ks is None:
+            continue
+        for n, t in (("k", ks), ("v", vs)):
+            if t.dtype != torch.float32 or t.device != dev or tuple(t.shape) != shape:
+                raise ValueError(f"{n}_scale_{form} must be float32 {list(shape)} on k's device")
+            setattr(a, f"{n}_scale_{form}", t.data_ptr())
+            setattr(a, f"{n}_scale_{form}_stride",
+                    (ctypes.c_int64 * len(shape))(*t.stride()))
+    a.num_seqs, a.total_q, a.max_seqlen_q = num_seqs, total_q, int(max_seqlen_q)
+    a.max_blocks_per_seq, a.num_blocks, a.block_size = block_table.shape[1], num_blocks, block_size
+    a.num_kv_heads, a.head_dim = hkv, d
+    a.dtype, a.kv_dtype = _dtype_code(k), _dtype_code(k_cache)
+    a.interleaved = 1 if interleaved else 0
+    keep = dict(k=k, v=v, q=q, q_out=q_out, cu_seqlens_q=cu_seqlens_q, seq_lens_k=seq_lens_k,
+                block_table=block_table, positions=positions)
+    static = (k_cache, v_cache, cos_sin, axes, kv_scale, k_scale_tok, v_scale_tok, k_scale_blk,
+              v_scale_blk)
+    return a, keep, static
+
+
+class PreparedAppend:
+    """``append_kv`` with its checks made and its sizes marshalled once, for a loop that calls
+    it with the same shapes (a decode loop, a captured step).
+
+    Built by :func:`prepare_append`.  Calling it passes the step's tensors -- ``k``, ``v``,
+    ``q``, ``q_out``, ``cu_seqlens_q``, ``seq_lens_k``, ``block_table``, ``positions`` -- each
+    of the prepared one's shape, strides, dtype and device (checked); any left out keeps the
+    prepared tensor.  The caches, the table and the scales stay as prepared.  Returns ``q_out``.
+    """
+
+    def __init__(self, lib, call, keep, static, stream):
+        self._lib = lib
+        self._call = call
+        self._ref = ctypes.byref(call)
+        self._keep = keep
+        self._static = static
+        self._meta = {n: (t.shape, t.stride(), t.dtype, t.device)
+                      for n, t in keep.items() if t is not None}
+        self._device = keep["k"].device
+        self._stream = stream
+
+    def __call__(self, k=None, v=None, q=None, q_out=None, cu_seqlens_q=None, seq_lens_k=None,
+                 block_table=None, positions=None, stream=None):
+        keep, call = self._keep, self._call
+        for name, t in (("k", k), ("v", v), ("q", q), ("q_out", q_out),
+                        ("cu_seqlens_q", cu_seqlens_q), ("seq_lens_k", seq_lens_k),
+                        ("block_table", block_table), ("positions", positions)):
+            if t is None or t is keep[name]:
+                continue
+            if (t.shape, t.stride(), t.dtype, t.device) != self._meta.get(name):
+                raise ValueError(f"{name}: shape, strides, dtype or device differs from the "
+                                 "prepared call")
+            setattr(call, name, t.data_ptr())
+            keep[name] = t
+        if stream is None:
+            stream = self._stream
+        with torch.cuda.device(self._device):
+            rc = self._lib.ua_append_kv(self._ref, stream.cuda_stream)
+        if rc != 0:
+            raise UaError(rc, "ua_append_kv")
+        return keep["q_out"]
+
+
+def prepare_append(k, v, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *,
+                   max_seqlen_q: int, q=None, q_out=None, cos_sin=None, positions=None,
+                   axis_of=None, interleaved: bool = False, kv_scale=None, k_scale_tok=None,
+                   v_scale_tok=None, k_scale_blk=None, v_scale_blk=None,
+                   stream=None) -> PreparedAppend:
+    """Check and marshal an ``append_kv`` call once (same arguments); the returned
+    :class:`PreparedAppend` makes the call with new per-step tensors."""
+    lib = _lib.load()
+    call, keep, static = _append_call(
+        k, v, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, max_seqlen_q, q, q_out,
+        cos_sin, positions, axis_of, interleaved, kv_scale, k_scale_tok, v_scale_tok,
+        k_scale_blk, v_scale_blk)
+    if stream is None:
+        stream = torch.cuda.current_stream(k.device)
+    return PreparedAppend(lib, call, keep, static, stream)
+
+
+def append_kv(k, v, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *,
+              max_seqlen_q: int, q=None, q_out=None, cos_sin=None, positions=None, axis_of=None,
+              interleaved: bool = False, kv_scale=None, k_scale_tok=None, v_scale_tok=None,
+              k_scale_blk=None, v_scale_blk=None, stream=None):
+    """Append new keys and values to the paged cache, rotating keys (and queries) by position.
+
+    k, v [total_q, H_kv, D] f16/bf16 (any token and head strides that are multiples of 8, so
+    slices of a fused projection go in as they are); token i of sequence b is written at cache
+    position seq_lens_k[b] - q_len + i through the block table, with the caches, cu_seqlens_q,
+    seq_lens_k (lengths with the new tokens) and block_table of :func:`unified_attention`.
+
+    Rotation: ``cos_sin`` float32 [max_position, rot_dim] (:func:`rope_table`) turns the first
+    rot_dim elements of every k and q head; pairs are (f, f + rot_dim / 2), or with
+    ``interleaved`` (2f, 2f + 1).  A token's angle is taken at its cache position, or at
+    ``positions`` int32 [total_q], or, with several axes (time, height, width), at positions
+    [axes, total_q] with ``axis_of``: the axis of each of the rot_dim / 2 frequencies, e.g.
+    [0] * 16 + [1] * 24 + [2] * 24.  ``q`` [total_q, H_q, D] is rotated into ``q_out`` (new
+    unless given; may be q itself), which is returned.
+
+    Scales of an 8-bit cache, one form: ``kv_scale`` float32 [2] (e4m3, per tensor, read);
+    k_scale_tok / v_scale_tok float32 [blocks, block_size, H_kv] (e4m3, per token, written);
+    k_scale_blk / v_scale_blk float32 [blocks, H_kv] (e4m3 or int8, one for each block and
+    head, updated: a block's scale grows with its tokens, and the codes it holds are rounded
+    again when it does).  include/ua.h has the arithmetic and what is left unwritten.
+    """
+    lib = _lib.load()
+    call, keep, _static = _append_call(
+        k, v, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, max_seqlen_q, q, q_out,
+        cos_sin, positions, axis_of, interleaved, kv_scale, k_scale_tok, v_scale_tok,
+        k_scale_blk, v_scale_blk)
+    if stream is None:
+        stream = torch.cuda.current_stream(k.device)
+    with torch.cuda.device(k.device):
+        rc = lib.ua_append_kv(ctypes.byref(call), ctypes.c_void_p(stream.cuda_stream))
+    if rc != 0:
+        raise UaError(rc, "ua_append_kv")
+    return keep["q_out"]
 
 
 def plan(*, num_seqs, total_q, max_seqlen_q, max_seqlen_k, block_size, num_q_heads,

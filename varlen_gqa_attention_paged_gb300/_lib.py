@@ -12,15 +12,16 @@ UA_OK, UA_ERR_INVALID_ARG, UA_ERR_UNSUPPORTED, UA_ERR_CUDA = 0, 1, 2, 3
 UA_ERR_WORKSPACE, UA_ERR_DEVICE_CHECK, UA_ERR_TIMEOUT, UA_ERR_SCRATCH_LIMIT = 4, 5, 6, 7
 UA_NOALLOC_SCRATCH_BYTES = 16 << 20
 # ua_dtype_t
-UA_DT_F16, UA_DT_BF16, UA_DT_F8E4M3, UA_DT_F32 = 0, 1, 2, 3
+UA_DT_F16, UA_DT_BF16, UA_DT_F8E4M3, UA_DT_F32, UA_DT_I8 = 0, 1, 2, 3, 4
 # ua_backend_t
 UA_BACKEND_AUTO, UA_BACKEND_2D, UA_BACKEND_SPLIT = 0, 1, 2
 # ua_path_t
 UA_PATH_2D, UA_PATH_SPLIT = 1, 2
 
 # every symbol include/ua.h declares
-EXPORTS = ("ua_unified_attention", "ua_unified_attention_noalloc", "ua_plan", "ua_workspace_bytes", "ua_device_status",
-           "ua_device_status_reset", "ua_status_string", "ua_version")
+EXPORTS = ("ua_unified_attention", "ua_unified_attention_noalloc", "ua_append_kv", "ua_plan",
+           "ua_workspace_bytes", "ua_device_status", "ua_device_status_reset",
+           "ua_status_string", "ua_version")
 
 
 class UaShape(ctypes.Structure):
@@ -43,6 +44,23 @@ class UaShape(ctypes.Structure):
         ("k_scale_stride", ctypes.c_int64 * 3),
         ("v_scale_stride", ctypes.c_int64 * 3),
     ]
+
+
+class UaAppend(ctypes.Structure):
+    _fields_ = (
+        [(n, ctypes.c_void_p) for n in (
+            "k", "v", "q", "q_out", "k_cache", "v_cache", "cu_seqlens_q", "seq_lens_k",
+            "block_table", "cos_sin", "positions", "kv_scale", "k_scale_tok", "v_scale_tok",
+            "k_scale_blk", "v_scale_blk")] +
+        [(n, ctypes.c_int64 * 2) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride")] +
+        [(n, ctypes.c_int64 * 3) for n in ("k_scale_tok_stride", "v_scale_tok_stride")] +
+        [(n, ctypes.c_int64 * 2) for n in ("k_scale_blk_stride", "v_scale_blk_stride")] +
+        [("positions_stride", ctypes.c_int64)] +
+        [(n, ctypes.c_int32) for n in (
+            "num_seqs", "total_q", "max_seqlen_q", "max_blocks_per_seq", "num_blocks",
+            "block_size", "num_q_heads", "num_kv_heads", "head_dim", "dtype", "kv_dtype",
+            "rot_dim", "max_position", "interleaved", "n_axes")] +
+        [("axis_of", ctypes.c_void_p)])
 
 
 class UaPlan(ctypes.Structure):
@@ -84,6 +102,8 @@ def load():
         lib.ua_unified_attention.restype = ctypes.c_int
         lib.ua_unified_attention_noalloc.argtypes = lib.ua_unified_attention.argtypes
         lib.ua_unified_attention_noalloc.restype = ctypes.c_int
+        lib.ua_append_kv.argtypes = [ctypes.POINTER(UaAppend), vp]
+        lib.ua_append_kv.restype = ctypes.c_int
         lib.ua_plan.argtypes = [ctypes.POINTER(UaShape), i32, i32, i32, i32, i32, i32, i32, i32,
                                 ctypes.POINTER(UaPlan)]
         lib.ua_plan.restype = ctypes.c_int

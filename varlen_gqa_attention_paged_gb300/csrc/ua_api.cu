@@ -570,6 +570,11 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
 
 }  // namespace
 
+namespace ua {
+int status_word(unsigned int** out) { return ::status_word(out); }
+int device_sm_count(int* out) { return ::device_sm_count(out); }
+}  // namespace ua
+
 extern "C" {
 
 int ua_unified_attention(const void* q, const void* k_cache, const void* v_cache, void* out,
@@ -621,7 +626,7 @@ int ua_device_status(void* stream, int* status) {
   if (cudaStreamSynchronize(st) != cudaSuccess) return UA_ERR_CUDA;
   unsigned int word = 0;
   if (cudaMemcpyFromSymbol(&word, g_device_status, sizeof(word)) != cudaSuccess) return UA_ERR_CUDA;
-  *status = (word & (ua::DEV_BAD_BLOCK | ua::DEV_BAD_SHAPE)) ? UA_ERR_DEVICE_CHECK
+  *status = (word & (ua::DEV_BAD_BLOCK | ua::DEV_BAD_SHAPE | ua::DEV_BAD_POSITION)) ? UA_ERR_DEVICE_CHECK
             : (word & ua::DEV_TIMEOUT) ? UA_ERR_TIMEOUT
                                        : UA_OK;
   return UA_OK;

@@ -12,7 +12,17 @@ namespace ua {
 enum KvKind { KV_F16 = 0, KV_BF16 = 1, KV_E4M3 = 2 };
 
 // Bits of the device status word (OR-ed by kernels, read by ua_device_status).
-enum : unsigned { DEV_BAD_BLOCK = 1u, DEV_TIMEOUT = 2u, DEV_BAD_SHAPE = 4u };
+enum : unsigned { DEV_BAD_BLOCK = 1u, DEV_TIMEOUT = 2u, DEV_BAD_SHAPE = 4u, DEV_BAD_POSITION = 8u };
+
+// The range of a token's or a block's scale: ua_append_kv keeps its scales within it, and the
+// attention kernels read a block's scale as the nearest value of it.
+constexpr float kScaleMin = 1.f / 1099511627776.f;  // 2^-40
+constexpr float kScaleMax = 1099511627776.f;        // 2^40
+
+// Host look-ups, cached per device (ua_status_t codes): the current device's status word and
+// SM count.
+int status_word(unsigned int** out);
+int device_sm_count(int* out);
 
 // Everything one launch of the attention tile kernel needs (passed by value).
 struct AttnParams {
