@@ -23,7 +23,8 @@
  *   out  = sum_j e^{s_j} V_j / (e^{sinks[h]} (if sinks != NULL) + sum_j e^{s_j})
  *                                      (fp8 cache: V_j = e4m3 * v_scale; per-token
  *                                       scales, when given, replace k_scale / v_scale
- *                                       key by key: see ua_shape_t)
+ *                                       key by key, and per-block scales block by block,
+ *                                       of e4m3 or int8 codes: see ua_shape_t)
  * A row with no allowed key (possible only when kv_len < q_len, e.g. a decode slot
  * with kv_len 0) is written as 0.
  *
@@ -128,6 +129,16 @@ typedef struct {
   const float* v_scale_tok;
   int64_t k_scale_stride[3];
   int64_t v_scale_stride[3];
+  /* e4m3 or int8 caches: a scale for each block and kv-head, as ua_append_kv writes them, or
+   * NULL.  Device float32 arrays over (block, kv-head): the scale of physical block b, kv-head
+   * g, is k_scale_blk[b * k_scale_blk_stride[0] + g * k_scale_blk_stride[1]] (strides in
+   * elements, each >= 0); V likewise.  Both or neither, and not together with the per-token
+   * scales; an int8 cache needs them.  Every kernel reads them (any head_dim, block_size and
+   * batch shape).  Values are taken within [2^-40, 2^40]. */
+  const float* k_scale_blk;
+  const float* v_scale_blk;
+  int64_t k_scale_blk_stride[2];
+  int64_t v_scale_blk_stride[2];
 } ua_shape_t;
 
 /* What the dispatcher chose for a call (see ua_plan). */
@@ -171,9 +182,10 @@ typedef struct {
  * window_left   >= 0: a query at position p sees keys p - window_left .. p
  *               (a window of W keys including the query itself is W - 1); < 0: off
  * alibi_slopes, qq_bias, sinks: device float32 arrays, or NULL to disable
- * kv_dtype      ua_dtype_t of both caches: F16, BF16 (q_dtype must match) or F8E4M3
- *               (OCP e4m3fn; q may be F16 or BF16, |q| < 65504)
- * kv_scale      device float32[2] {k_scale, v_scale}, required with F8E4M3
+ * kv_dtype      ua_dtype_t of both caches: F16, BF16 (q_dtype must match), F8E4M3
+ *               (OCP e4m3fn) or I8 (both: q may be F16 or BF16, |q| < 65504)
+ * kv_scale      device float32[2] {k_scale, v_scale}, required with F8E4M3 unless the shape
+ *               gives per-token or per-block scales
  * backend       ua_backend_t
  * stream        cudaStream_t to launch on
  * shape         host-side sizes (must not be NULL)

@@ -49,7 +49,8 @@ def _ptr(t):
 
 
 def _shape(q, k_cache, block_table, cu_seqlens_q, max_seqlen_q, max_seqlen_k, qq_bias,
-           out_dtype_code, num_splits, workspace, events, k_scale_tok=None, v_scale_tok=None):
+           out_dtype_code, num_splits, workspace, events, k_scale_tok=None, v_scale_tok=None,
+           k_scale_blk=None, v_scale_blk=None):
     sh = _lib.UaShape()
     sh.num_seqs = cu_seqlens_q.numel() - 1
     sh.total_q = q.shape[0]
@@ -82,6 +83,16 @@ def _shape(q, k_cache, block_table, cu_seqlens_q, max_seqlen_q, max_seqlen_k, qq
                 raise ValueError("per-token scales must be [num_blocks, block_size, H_kv]")
             setattr(sh, ptr, t.data_ptr())
             setattr(sh, strides, (ctypes.c_int64 * 3)(*t.stride()))
+    if (k_scale_blk is None) != (v_scale_blk is None):
+        raise ValueError("per-block scales: give both k_scale_blk and v_scale_blk, or neither")
+    if k_scale_blk is not None:
+        for t, ptr in ((k_scale_blk, "k_scale_blk"), (v_scale_blk, "v_scale_blk")):
+            if t.dtype != torch.float32 or t.device != k_cache.device or \
+                    tuple(t.shape) != (k_cache.shape[0], k_cache.shape[2]):
+                raise ValueError("per-block scales must be float32 [num_blocks, H_kv] on the "
+                                 "caches' device")
+            setattr(sh, ptr, t.data_ptr())
+            setattr(sh, ptr + "_stride", (ctypes.c_int64 * 2)(*t.stride()))
     return sh
 
 
@@ -89,17 +100,19 @@ def unified_attention(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table
                       max_seqlen_q: int, max_seqlen_k: int, scale: float | None = None,
                       softcap: float = 0.0, window_left: int = -1, alibi_slopes=None,
                       qq_bias=None, sinks=None, kv_scale=None, k_scale_tok=None,
-                      v_scale_tok=None, out=None, out_dtype=None,
-                      backend: str = "auto", num_splits: int = 0, workspace=None, stream=None,
+                      v_scale_tok=None, k_scale_blk=None, v_scale_blk=None, out=None,
+                      out_dtype=None, backend: str = "auto", num_splits: int = 0, workspace=None, stream=None,
                       events=None):
     """Paged varlen GQA attention on the GPU; returns ``out`` [total_q, H_q, D].
 
     q [total_q, H_q, D] f16/bf16; k_cache, v_cache [num_blocks, block_size, H_kv, D]
-    f16/bf16/float8_e4m3fn; cu_seqlens_q [S+1], seq_lens_k [S], block_table [S, max_blocks]
+    f16/bf16/float8_e4m3fn/int8; cu_seqlens_q [S+1], seq_lens_k [S], block_table [S, max_blocks]
     int32; alibi_slopes / sinks [H_q] and qq_bias [rows, stride] float32; kv_scale float32[2]
     (k_scale, v_scale) for the fp8 cache, or k_scale_tok / v_scale_tok float32 [num_blocks,
-    block_size, H_kv] (any strides) for per-token fp8 scales.  max_seqlen_q / max_seqlen_k
-    are host ints.
+    block_size, H_kv] (any strides) for per-token fp8 scales, or k_scale_blk / v_scale_blk
+    float32 [num_blocks, H_kv] (any strides) for an fp8 or int8 cache with a scale for each
+    block and kv-head (what :func:`append_kv` writes).  max_seqlen_q / max_seqlen_k are host
+    ints.
     """
     lib = _lib.load()
     total_q, hq, d = q.shape
@@ -121,7 +134,8 @@ def unified_attention(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table
     if stream is None:
         stream = torch.cuda.current_stream(q.device)
     sh = _shape(q, k_cache, block_table, cu_seqlens_q, max_seqlen_q, max_seqlen_k, qq_bias,
-                _dtype_code(out), num_splits, workspace, events, k_scale_tok, v_scale_tok)
+                _dtype_code(out), num_splits, workspace, events, k_scale_tok, v_scale_tok,
+                k_scale_blk, v_scale_blk)
     rc = lib.ua_unified_attention(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(cu_seqlens_q), _ptr(seq_lens_k),
         _ptr(block_table), block_size, hq, hkv, d, float(scale), float(softcap or 0.0),
@@ -179,8 +193,8 @@ class PreparedAttention:
 def prepare(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *, max_seqlen_q: int,
             max_seqlen_k: int, scale: float | None = None, softcap: float = 0.0,
             window_left: int = -1, alibi_slopes=None, qq_bias=None, sinks=None, kv_scale=None,
-            k_scale_tok=None, v_scale_tok=None, out=None, out_dtype=None, backend: str = "auto",
-            num_splits: int = 0, workspace=None, stream=None) -> PreparedAttention:
+            k_scale_tok=None, v_scale_tok=None, k_scale_blk=None, v_scale_blk=None, out=None,
+            out_dtype=None, backend: str = "auto", num_splits: int = 0, workspace=None, stream=None) -> PreparedAttention:
     """Validate and marshal a ``unified_attention`` call once (same arguments); the
     returned :class:`PreparedAttention` makes the call with new per-step tensors."""
     lib = _lib.load()
@@ -203,7 +217,8 @@ def prepare(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *, max_s
     if stream is None:
         stream = torch.cuda.current_stream(q.device)
     sh = _shape(q, k_cache, block_table, cu_seqlens_q, max_seqlen_q, max_seqlen_k, qq_bias,
-                _dtype_code(out), num_splits, workspace, None, k_scale_tok, v_scale_tok)
+                _dtype_code(out), num_splits, workspace, None, k_scale_tok, v_scale_tok,
+                k_scale_blk, v_scale_blk)
     args = [_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(cu_seqlens_q),
             _ptr(seq_lens_k), _ptr(block_table), block_size, hq, hkv, d, float(scale),
             float(softcap or 0.0), int(window_left if window_left is not None else -1),
@@ -214,7 +229,7 @@ def prepare(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *, max_s
     prep = PreparedAttention(lib, args, sh, tensors, stream)
     # the caches, score features and scales the prepared call points at stay alive with it
     prep._static = (k_cache, v_cache, alibi_slopes, qq_bias, sinks, kv_scale, k_scale_tok,
-                    v_scale_tok, workspace)
+                    v_scale_tok, k_scale_blk, v_scale_blk, workspace)
     return prep
 
 
@@ -459,19 +474,22 @@ def append_kv(k, v, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *,
 def plan(*, num_seqs, total_q, max_seqlen_q, max_seqlen_k, block_size, num_q_heads,
          num_kv_heads, head_dim, window_left=-1, kv_dtype=UA_DT_BF16, q_dtype=None,
          backend="auto", num_splits=0, num_sms=0, max_blocks_per_seq=1, num_blocks=1,
-         per_token_scales=False):
+         per_token_scales=False, per_block_scales=False):
     """The dispatcher's decision for these sizes (host only; no GPU needed when num_sms > 0).
     per_token_scales: plan for an fp8 call with per-token K/V scales (the dispatcher only
-    tests the scale pointers for null; this passes a placeholder that is never read)."""
+    tests the scale pointers for null; this passes a placeholder that is never read);
+    per_block_scales: for an fp8 call with per-block scales (an int8 one always has them)."""
     lib = _lib.load()
     sh = _lib.UaShape()
     if per_token_scales:
         sh.k_scale_tok = sh.v_scale_tok = 256
+    if per_block_scales or kv_dtype == UA_DT_I8:
+        sh.k_scale_blk = sh.v_scale_blk = 256
     sh.num_seqs, sh.total_q = num_seqs, total_q
     sh.max_seqlen_q, sh.max_seqlen_k = max_seqlen_q, max_seqlen_k
     sh.max_blocks_per_seq, sh.num_blocks = max_blocks_per_seq, num_blocks
-    sh.q_dtype = q_dtype if q_dtype is not None else (UA_DT_BF16 if kv_dtype == UA_DT_F8E4M3
-                                                      else kv_dtype)
+    sh.q_dtype = q_dtype if q_dtype is not None else (
+        UA_DT_BF16 if kv_dtype in (UA_DT_F8E4M3, UA_DT_I8) else kv_dtype)
     sh.out_dtype = sh.q_dtype
     sh.num_splits = num_splits
     pl = _lib.UaPlan()

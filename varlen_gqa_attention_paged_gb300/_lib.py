@@ -43,6 +43,10 @@ class UaShape(ctypes.Structure):
         ("v_scale_tok", ctypes.c_void_p),
         ("k_scale_stride", ctypes.c_int64 * 3),
         ("v_scale_stride", ctypes.c_int64 * 3),
+        ("k_scale_blk", ctypes.c_void_p),
+        ("v_scale_blk", ctypes.c_void_p),
+        ("k_scale_blk_stride", ctypes.c_int64 * 2),
+        ("v_scale_blk_stride", ctypes.c_int64 * 2),
     ]
 
 

@@ -142,10 +142,11 @@ bool encode_cache_map(CUtensorMap* map, const void* base, int kv_dtype, int num_
   if (map_cache().find(key, map)) return true;
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (enc == nullptr) return false;
-  const int esz = kv_dtype == UA_DT_F8E4M3 ? 1 : 2;
+  const bool codes = kv_dtype == UA_DT_F8E4M3 || kv_dtype == UA_DT_I8;
+  const int esz = codes ? 1 : 2;
   const int row_bytes = d * esz;
   const int cbw = row_bytes >= 128 ? 128 : row_bytes;
-  const CUtensorMapDataType dt = kv_dtype == UA_DT_F8E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+  const CUtensorMapDataType dt = codes                    ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                  : kv_dtype == UA_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const cuuint64_t rows = static_cast<cuuint64_t>(num_blocks) * block_size;
@@ -197,15 +198,27 @@ int check_sizes(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, in
     return UA_ERR_INVALID_ARG;
   if (block_size < 1 || hq < 1 || hkv < 1 || hq % hkv != 0) return UA_ERR_INVALID_ARG;
   if (d != 64 && d != 128 && d != 256) return UA_ERR_INVALID_ARG;
-  if (kv_dtype != UA_DT_F16 && kv_dtype != UA_DT_BF16 && kv_dtype != UA_DT_F8E4M3)
+  if (kv_dtype != UA_DT_F16 && kv_dtype != UA_DT_BF16 && kv_dtype != UA_DT_F8E4M3 &&
+      kv_dtype != UA_DT_I8)
     return UA_ERR_INVALID_ARG;
   if (sh->q_dtype != UA_DT_F16 && sh->q_dtype != UA_DT_BF16) return UA_ERR_INVALID_ARG;
   if (sh->out_dtype != UA_DT_F16 && sh->out_dtype != UA_DT_BF16 && sh->out_dtype != UA_DT_F32)
     return UA_ERR_INVALID_ARG;
   if (backend != UA_BACKEND_AUTO && backend != UA_BACKEND_2D && backend != UA_BACKEND_SPLIT)
     return UA_ERR_INVALID_ARG;
-  if (kv_dtype != UA_DT_F8E4M3 && sh->q_dtype != kv_dtype) return UA_ERR_UNSUPPORTED;
+  if (kv_dtype != UA_DT_F8E4M3 && kv_dtype != UA_DT_I8 && sh->q_dtype != kv_dtype)
+    return UA_ERR_UNSUPPORTED;
   return UA_OK;
+}
+
+// What the caches hold, by their element type and the scales given.
+int kv_kind(const ua_shape_t* sh, int kv_dtype) {
+  switch (kv_dtype) {
+    case UA_DT_F16: return ua::KV_F16;
+    case UA_DT_BF16: return ua::KV_BF16;
+    case UA_DT_I8: return ua::KV_I8B;
+    default: return sh->k_scale_blk != nullptr ? ua::KV_E4M3B : ua::KV_E4M3;
+  }
 }
 
 // The dispatcher.  Split the key walk (UA_BACKEND_AUTO) only when the 2D grid leaves
@@ -227,6 +240,9 @@ void make_plan(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, int
                int kv_dtype, int backend, int num_sms, bool allow_tc, bool allow_dec,
                bool query_device, ua_plan_t* pl) {
   const int group = hq / hkv;
+  const int kv = kv_kind(sh, kv_dtype);
+  const bool blk = kv == ua::KV_E4M3B || kv == ua::KV_I8B;
+  if (blk) allow_tc = allow_dec = false;
   const long long rows_max = static_cast<long long>(sh->max_seqlen_q) * group;
   const bool tc = allow_tc && rows_max > 16 && group <= 128 && block_size % 16 == 0;
   // decode with at most 8 rows per kv-head: the key-major decode tile (page boxes)
@@ -262,8 +278,8 @@ void make_plan(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, int
       static_cast<long long>(num_sms) *
       (tc    ? 1
        : pair ? ua::decode_pair_ctas_per_sm(d)
-       : dec  ? ua::decode_ctas_per_sm(d, kv_dtype)
-              : ua::tile_ctas_per_sm(d, kv_dtype, wm));
+       : dec  ? ua::decode_ctas_per_sm(d, kv)
+              : ua::tile_ctas_per_sm(d, kv, wm));
   const long long by_walk = std::max<long long>(1, walk / kMinPartitionKeys);
   const long long fit = std::max<long long>(2, std::min(wave / base, by_walk));
   int n_part = 1;
@@ -308,7 +324,7 @@ void make_plan(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, int
       const int c = cy * cz;
       if (c <= 1) break;
       long long cap = -1;
-      if (dec && query_device) cap = ua::decode_cluster_capacity(d, kv_dtype, false, pair, cy, cz);
+      if (dec && query_device) cap = ua::decode_cluster_capacity(d, kv, false, pair, cy, cz);
       if (cap < 0) cap = c <= 2 ? wave / c : (wave * 9 / 10) / c;
       if (slots * (gy / cy) <= cap) break;
     }
@@ -323,7 +339,7 @@ void make_plan(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, int
     wide = true;
     if (cy * cz > 1) {
       long long cap = -1;
-      if (query_device) cap = ua::decode_cluster_capacity(d, kv_dtype, true, false, cy, cz);
+      if (query_device) cap = ua::decode_cluster_capacity(d, kv, true, false, cy, cz);
       if (cap < 0) cap = (static_cast<long long>(num_sms) * 9 / 10) / (cy * cz);
       wide = slots * (hkv / cy) <= cap;
     }
@@ -405,10 +421,25 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
     return UA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
     return UA_ERR_INVALID_ARG;
+  const int kv = kv_kind(sh, kv_dtype);
+  const bool blk_scales = kv == ua::KV_E4M3B || kv == ua::KV_I8B;
   const bool tok_scales = kv_dtype == UA_DT_F8E4M3 && sh->k_scale_tok != nullptr;
+  if (kv_dtype == UA_DT_F8E4M3 || kv_dtype == UA_DT_I8) {
+    if ((sh->k_scale_blk == nullptr) != (sh->v_scale_blk == nullptr)) return UA_ERR_INVALID_ARG;
+    if (kv_dtype == UA_DT_I8 && !sh->k_scale_blk) return UA_ERR_INVALID_ARG;
+    if (blk_scales) {
+      if (sh->k_scale_tok || sh->v_scale_tok ||
+          (reinterpret_cast<uintptr_t>(sh->k_scale_blk) & 3) ||
+          (reinterpret_cast<uintptr_t>(sh->v_scale_blk) & 3))
+        return UA_ERR_INVALID_ARG;
+      for (int i = 0; i < 2; ++i)
+        if (sh->k_scale_blk_stride[i] < 0 || sh->v_scale_blk_stride[i] < 0)
+          return UA_ERR_INVALID_ARG;
+    }
+  }
   if (kv_dtype == UA_DT_F8E4M3) {
     if ((sh->k_scale_tok == nullptr) != (sh->v_scale_tok == nullptr)) return UA_ERR_INVALID_ARG;
-    if (!tok_scales && kv_scale == nullptr) return UA_ERR_INVALID_ARG;
+    if (!tok_scales && !blk_scales && kv_scale == nullptr) return UA_ERR_INVALID_ARG;
     if (tok_scales) {
       if ((reinterpret_cast<uintptr_t>(sh->k_scale_tok) & 3) ||
           (reinterpret_cast<uintptr_t>(sh->v_scale_tok) & 3))
@@ -449,6 +480,14 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
       p.v_scale_stride[i] = sh->v_scale_stride[i];
     }
   }
+  if (blk_scales) {
+    p.k_scale_blk = sh->k_scale_blk;
+    p.v_scale_blk = sh->v_scale_blk;
+    for (int i = 0; i < 2; ++i) {
+      p.k_blk_stride[i] = sh->k_scale_blk_stride[i];
+      p.v_blk_stride[i] = sh->v_scale_blk_stride[i];
+    }
+  }
   p.num_seqs = sh->num_seqs;
   p.total_q = sh->total_q;
   p.max_seqlen_q = sh->max_seqlen_q;
@@ -468,7 +507,6 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
   p.softcap = softcap > 0.f ? softcap : 0.f;
   if ((rc = status_word(&p.status)) != UA_OK) return rc;
 
-  const int kv = kv_dtype == UA_DT_F16 ? ua::KV_F16 : kv_dtype == UA_DT_BF16 ? ua::KV_BF16 : ua::KV_E4M3;
   const bool feat = softcap > 0.f || alibi != nullptr || qq_bias != nullptr;
   // The tensor-memory kernel needs TMA maps of q and both caches; if one cannot be made,
   // the call is planned again for the tile kernel.
@@ -545,6 +583,11 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
   } else if (pl.kernel == ua::KERNEL_DEC8W) {
     err = d == 64 ? ua::launch_decode_w8_d64(tp, grid, kv, feat, pl.cluster_y, pl.cluster_z, st)
                   : ua::launch_decode_w8_d128(tp, grid, kv, feat, pl.cluster_y, pl.cluster_z, st);
+  } else if (blk_scales) {
+    const auto launch = d == 64    ? ua::launch_tile_blk_d64
+                        : d == 128 ? ua::launch_tile_blk_d128
+                                   : ua::launch_tile_blk_d256;
+    err = launch(tp, grid, pl.kernel, kv, feat, tma, pl.cluster_y, pl.cluster_z, st);
   } else switch (d) {
     case 64: err = ua::launch_tile_d64(tp, grid, pl.kernel, kv, feat, tma, pl.cluster_y, pl.cluster_z, st); break;
     case 128: err = ua::launch_tile_d128(tp, grid, pl.kernel, kv, feat, tma, pl.cluster_y, pl.cluster_z, st); break;

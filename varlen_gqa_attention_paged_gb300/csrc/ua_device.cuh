@@ -464,6 +464,36 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32
       : "r"(w));
 }
 
+// The four int8 codes of a word -> two f16x2 words, exactly: a code's byte with its sign bit
+// flipped is 128 + code, and under the high byte 0x64 an f16 of 1024 + 128 + code.
+__device__ __forceinline__ void i8x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), h = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&l), off);
+  const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&h), off);
+  lo = *reinterpret_cast<const uint32_t*>(&a);
+  hi = *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// The four 8-bit codes of a word -> two f16x2 words.
+template <bool I8>
+__device__ __forceinline__ void codes4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (I8) i8x4_to_f16x4(w, lo, hi);
+  else e4m3x4_to_f16x4(w, lo, hi);
+}
+
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A block's scale as the kernels take it: the nearest value of [2^-40, 2^40] (a NaN: 2^-40).
+__device__ __forceinline__ float block_scale(float s) {
+  return fminf(fmaxf(s, 1.f / 1099511627776.f), 1099511627776.f);
+}
+
 // Two floats -> two e4m3fn codes (round to nearest even, saturating at +-448), `lo` in the
 // low byte.
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {

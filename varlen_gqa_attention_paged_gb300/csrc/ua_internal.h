@@ -9,7 +9,9 @@
 
 namespace ua {
 
-enum KvKind { KV_F16 = 0, KV_BF16 = 1, KV_E4M3 = 2 };
+// What the caches hold: 16-bit values, e4m3 codes with per-tensor or per-token scales, or (the
+// block-scaled kinds) e4m3 or int8 codes with a scale for each block and kv-head.
+enum KvKind { KV_F16 = 0, KV_BF16 = 1, KV_E4M3 = 2, KV_E4M3B = 3, KV_I8B = 4 };
 
 // Bits of the device status word (OR-ed by kernels, read by ua_device_status).
 enum : unsigned { DEV_BAD_BLOCK = 1u, DEV_TIMEOUT = 2u, DEV_BAD_SHAPE = 4u, DEV_BAD_POSITION = 8u };
@@ -43,6 +45,12 @@ struct AttnParams {
   const float* v_scale_tok;
   long long k_scale_stride[3];
   long long v_scale_stride[3];
+  // block-scaled kinds: the scale of physical block b, kv-head g is at [b * stride[0] +
+  // g * stride[1]]
+  const float* k_scale_blk;
+  const float* v_scale_blk;
+  long long k_blk_stride[2];
+  long long v_blk_stride[2];
   float* ws_m;                  // [total_q, hq, n_part]     (n_part > 1)
   float* ws_l;                  // [total_q, hq, n_part]
   float* ws_acc;                // [total_q, hq, n_part, D]
@@ -100,6 +108,13 @@ cudaError_t launch_tile_d128(const TileParams& tp, dim3 grid, int wm, int kv, bo
                              int cluster_y, int cluster_z, cudaStream_t s);
 cudaError_t launch_tile_d256(const TileParams& tp, dim3 grid, int wm, int kv, bool feat, bool tma,
                              int cluster_y, int cluster_z, cudaStream_t s);
+// the same for the block-scaled kinds
+cudaError_t launch_tile_blk_d64(const TileParams& tp, dim3 grid, int wm, int kv, bool feat,
+                                bool tma, int cluster_y, int cluster_z, cudaStream_t s);
+cudaError_t launch_tile_blk_d128(const TileParams& tp, dim3 grid, int wm, int kv, bool feat,
+                                 bool tma, int cluster_y, int cluster_z, cudaStream_t s);
+cudaError_t launch_tile_blk_d256(const TileParams& tp, dim3 grid, int wm, int kv, bool feat,
+                                 bool tma, int cluster_y, int cluster_z, cudaStream_t s);
 // key-major decode tile (head_dim 64, 128; TMA page boxes; at most 8 rows per kv-head), with
 // four consumer warps (64-key stages, three CTAs per SM) or eight (128-key stages, one CTA
 // per SM, for small grids)

@@ -21,6 +21,12 @@
 //               shuffles.  fp8 e4m3 codes are turned into f16 MMA operands in
 //               registers: the head dimension is permuted so that every lane's operand
 //               bytes are contiguous in shared memory (see kPermD).
+//               Block-scaled caches (KvTraits::kBlk): a key's scales are copied beside its
+//               tile.  The K scale joins the score's factor.  The V scale joins the
+//               exponent: a key's weight is w = 2^(x + log2 vs - M) with M the running max
+//               of x + log2 vs, O sums w times the codes and the row sum takes w / vs, so
+//               P.V runs on the codes, the weights stay in f16's range whatever the scales
+//               are, and a row's state merges with others as before.
 //   WM = 1 (decode-shaped q-blocks, BM = 16): the four consumer warps share the 16
 //          rows and each takes 16 keys of every tile; their states merge at the end.
 //   WM = 4 (BM = 64): each consumer warp owns 16 rows and walks every key.
@@ -44,16 +50,31 @@ template <>
 struct KvTraits<KV_F16> {
   static constexpr int kEsz = 2;
   static constexpr bool kF16Mma = true;
+  static constexpr bool kCodes = false, kBlk = false, kI8 = false;
 };
 template <>
 struct KvTraits<KV_BF16> {
   static constexpr int kEsz = 2;
   static constexpr bool kF16Mma = false;
+  static constexpr bool kCodes = false, kBlk = false, kI8 = false;
 };
 template <>
 struct KvTraits<KV_E4M3> {
   static constexpr int kEsz = 1;
   static constexpr bool kF16Mma = true;
+  static constexpr bool kCodes = true, kBlk = false, kI8 = false;
+};
+template <>
+struct KvTraits<KV_E4M3B> {
+  static constexpr int kEsz = 1;
+  static constexpr bool kF16Mma = true;
+  static constexpr bool kCodes = true, kBlk = true, kI8 = false;
+};
+template <>
+struct KvTraits<KV_I8B> {
+  static constexpr int kEsz = 1;
+  static constexpr bool kF16Mma = true;
+  static constexpr bool kCodes = true, kBlk = true, kI8 = true;
 };
 
 // Byte offset of 16-byte chunk `c` of row `r` inside a 128-byte-swizzled column block.
@@ -79,7 +100,7 @@ struct TileCfg {
   // fp8 operands are dequantised in registers, with the head dimension permuted: the
   // QK^T sum runs over d in any order (Q and K permuted alike), and the P.V output
   // columns are put back in order when written.
-  static constexpr bool kPermD = KV == KV_E4M3;
+  static constexpr bool kPermD = KvTraits<KV>::kCodes;
   static constexpr int kMergeBytes = (kWN > 1) ? kConsumerWarps * (2 * 16 + (D / 8) * 32 * 4) * 4 : 0;
   // decode-shaped CTAs of one cluster exchange their partitions' rows (max, sum, D
   // unnormalised outputs of 16 rows) through distributed shared memory
@@ -92,13 +113,15 @@ struct TileCfg {
                                       ? kStages * kStageBytes
                                       : kMergeBytes + kPartBytes;
   static constexpr int kPipeBytes = (kPipeRaw + 1023) & ~1023;
-  static constexpr int kSmemBytes = 1024 + kPipeBytes + 2 * kStages * 8;
+  // block-scaled caches: a stage's K scales and V scales, one a key, behind the barriers
+  static constexpr int kScaleBytes = KvTraits<KV>::kBlk ? kStages * 2 * kT * 4 : 0;
+  static constexpr int kSmemBytes = 1024 + kPipeBytes + 2 * kStages * 8 + kScaleBytes;
   // two CTAs per SM when they fit, but not at d256, whose 16 x 256 fp32 accumulators alone
   // take 128 registers a thread
   static constexpr int kMinBlocks = (D <= 128 && 2 * kSmemBytes <= 227 * 1024) ? 2 : 1;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
   static_assert(kRowBytes % kCBW == 0 && kCBW % 16 == 0, "rows are whole column blocks");
-  static_assert(kSwz || KV == KV_E4M3, "16-bit rows are at least 128 bytes");
+  static_assert(kSwz || KvTraits<KV>::kCodes, "16-bit rows are at least 128 bytes");
 
   // Byte offset of 16-byte chunk c of tile row r in a K or V stage.
   static __device__ __forceinline__ uint32_t raw_off(uint32_t r, uint32_t c) {
@@ -289,6 +312,9 @@ __global__ void __launch_bounds__(160, (TileCfg<D, KV, WM>::kMinBlocks))
   uint8_t* const pipe = smem;
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + C::kPipeBytes);
   uint64_t* const empty = full + S;
+  float* const sks = reinterpret_cast<float*>(empty + S);  // [S][T] K scales (block-scaled)
+  float* const svs = sks + S * T;                           // [S][T] V scales
+  constexpr bool kBlk = KvTraits<KV>::kBlk, kI8 = KvTraits<KV>::kI8;
   __shared__ int s_abort;
 
   const int warp = threadIdx.x >> 5;
@@ -353,6 +379,16 @@ __global__ void __launch_bounds__(160, (TileCfg<D, KV, WM>::kMinBlocks))
     const uint64_t policy = l2_policy_evict_first();
     const int bs = p.block_size;
     int issued = 0;
+    // block-scaled caches: the scales of key `kt` of stage s, whose block is blk (< 0: none, 1)
+    auto stage_scales = [&](int s, int kt, int blk) {
+      if (blk >= 0) {
+        cp_async_4(sks + s * T + kt, p.k_scale_blk + blk * p.k_blk_stride[0] + g * p.k_blk_stride[1]);
+        cp_async_4(svs + s * T + kt, p.v_scale_blk + blk * p.v_blk_stride[0] + g * p.v_blk_stride[1]);
+      } else {
+        sks[s * T + kt] = 1.f;
+        svs[s * T + kt] = 1.f;
+      }
+    };
     if constexpr (TMA) {
       // lane j < T/16 owns page slice j (keys key0 + 16j .. +15) of every tile
       const int oob = p.num_blocks * bs;  // first row coordinate past the cache: zero fill
@@ -377,6 +413,14 @@ __global__ void __launch_bounds__(160, (TileCfg<D, KV, WM>::kMinBlocks))
           break;
         uint8_t* kdst = pipe + s * C::kStageBytes;
         uint8_t* vdst = kdst + C::kCB * C::kCBBytes;
+        if constexpr (kBlk) {  // keys 2 lane, 2 lane + 1: one page's
+          const int rowp = __shfl_sync(0xffffffffu, row, lane / 8);
+          const int blk = rowp == oob ? -1 : rowp / bs;
+          stage_scales(s, 2 * lane, blk);
+          stage_scales(s, 2 * lane + 1, blk);
+          cp_async_arrive(&full[s]);
+          __syncwarp();
+        }
         if (lane == 0) mbar_arrive_expect_tx(&full[s], C::kStageBytes);
         __syncwarp();
         if (lane < T / 16) {
@@ -410,14 +454,17 @@ __global__ void __launch_bounds__(160, (TileCfg<D, KV, WM>::kMinBlocks))
           const int row = lane + 32 * rr;
           const int key = key0 + row;
           long long off = -1;
+          int kblk = -1;
           if (key < ke && key < kv_len) {
             const int col = key / bs;
             const int blk = col < p.max_blocks_per_seq ? __ldg(bt + col) : -1;
-            if (static_cast<unsigned>(blk) < static_cast<unsigned>(p.num_blocks))
+            if (static_cast<unsigned>(blk) < static_cast<unsigned>(p.num_blocks)) {
               off = static_cast<long long>((static_cast<size_t>(blk) * bs + key % bs) * slot_pitch);
-            else
+              kblk = blk;
+            } else
               atomicOr(p.status, DEV_BAD_BLOCK);
           }
+          if constexpr (kBlk) stage_scales(s, row, kblk);
 #pragma unroll 4
           for (int c = 0; c < kChunks; ++c) {
             const uint32_t so = C::raw_off(row, c);
@@ -509,7 +556,7 @@ __global__ void __launch_bounds__(160, (TileCfg<D, KV, WM>::kMinBlocks))
         const uint16_t* qrow = static_cast<const uint16_t*>(p.q) +
                                (static_cast<size_t>(rt[rr]) * p.hq + rh[rr]) * D;
         v = __ldg(reinterpret_cast<const unsigned int*>(qrow + col));
-        if constexpr (KV == KV_E4M3) {
+        if constexpr (C::kPermD) {
           if (p.q_dtype == UA_DT_BF16) v = pack_f16(bf16_lo(v), bf16_hi(v));
         }
       }
@@ -527,12 +574,13 @@ __global__ void __launch_bounds__(160, (TileCfg<D, KV, WM>::kMinBlocks))
   const float inv_softcap = p.softcap > 0.f ? 1.f / p.softcap : 0.f;
 
   // Online-softmax state (base 2).  The sink is the initial running max of partition 0
-  // and adds e^{sink - m} once to the row sum (counted by lane cq == 0 of the quad).
+  // and adds e^{sink - m} once to the row sum (counted by lane cq == 0 of the quad);
+  // block-scaled caches, whose running max carries the V scales, add it at the end.
   float m_run[2], l_run[2];
   float o_acc[D / 8][4];
 #pragma unroll
   for (int rr = 0; rr < 2; ++rr) {
-    const bool sink = p.sinks != nullptr && z == 0 && kgp == 0 && rv[rr];
+    const bool sink = !kBlk && p.sinks != nullptr && z == 0 && kgp == 0 && rv[rr];
     m_run[rr] = sink ? __ldg(p.sinks + rh[rr]) * kLog2e : -INFINITY;
     l_run[rr] = (sink && cq == 0) ? 1.f : 0.f;
   }
@@ -580,9 +628,11 @@ __global__ void __launch_bounds__(160, (TileCfg<D, KV, WM>::kMinBlocks))
                 *reinterpret_cast<const uint4*>(kst + C::raw_byte(trow, cq * (D / 4) + 16 * u));
             const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              mma_16816<true>(sc[n], qf[4 * u + q], e4m3x2_to_f16x2(static_cast<uint16_t>(w[q])),
-                              e4m3x2_to_f16x2(static_cast<uint16_t>(w[q] >> 16)));
+            for (int q = 0; q < 4; ++q) {
+              uint32_t b0, b1;
+              codes4_to_f16x4<kI8>(w[q], b0, b1);
+              mma_16816<true>(sc[n], qf[4 * u + q], b0, b1);
+            }
           }
         }
       } else {
@@ -601,11 +651,27 @@ __global__ void __launch_bounds__(160, (TileCfg<D, KV, WM>::kMinBlocks))
 
       // ---- score transform and mask (log2 domain)
       const bool need_mask = kc0 < lomax || kc0 + 15 > pmin || kc0 + 16 > ke;
+      // block-scaled: the scales of this lane's keys 8 n + 2 cq + i of the chunk, V's as its
+      // logarithm and reciprocal
+      float kf[2][2], vl[2][2], vi[2][2];
+      if constexpr (kBlk) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int kt = s * T + 16 * ch + 8 * n + 2 * cq + i;
+            kf[n][i] = block_scale(sks[kt]);
+            const float vs = block_scale(svs[kt]);
+            vl[n][i] = fast_log2(vs);
+            vi[n][i] = fast_rcp(vs);
+          }
+      }
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int rr = e >> 1;
+          if constexpr (kBlk) sc[n][e] *= kf[n][e & 1];
           const int j = kc0 + n * 8 + 2 * cq + (e & 1);
           float x;
           if constexpr (FEAT) {
@@ -619,6 +685,7 @@ __global__ void __launch_bounds__(160, (TileCfg<D, KV, WM>::kMinBlocks))
           } else {
             x = sc[n][e] * scale_log2;
           }
+          if constexpr (kBlk) x += vl[n][e & 1];
           if (need_mask) {
             const bool ok = rv[rr] && j >= rlo[rr] && j <= rpos[rr] && j < ke;
             x = ok ? x : -INFINITY;
@@ -648,7 +715,8 @@ __global__ void __launch_bounds__(160, (TileCfg<D, KV, WM>::kMinBlocks))
         for (int n = 0; n < 2; ++n) {
           sc[n][2 * rr] = fast_exp2(sc[n][2 * rr] - m_use);
           sc[n][2 * rr + 1] = fast_exp2(sc[n][2 * rr + 1] - m_use);
-          rs += sc[n][2 * rr] + sc[n][2 * rr + 1];
+          if constexpr (kBlk) rs += sc[n][2 * rr] * vi[n][0] + sc[n][2 * rr + 1] * vi[n][1];
+          else rs += sc[n][2 * rr] + sc[n][2 * rr + 1];
         }
         l_run[rr] = l_run[rr] * alpha[rr] + rs;
       }
@@ -718,14 +786,18 @@ __global__ void __launch_bounds__(160, (TileCfg<D, KV, WM>::kMinBlocks))
             const uint32_t p1[2] = {__byte_perm(vw[2][x], vw[3][x], 0x5140),
                                     __byte_perm(vw[2][x], vw[3][x], 0x7362)};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t b0 = e4m3x2_to_f16x2(static_cast<uint16_t>(p0[q >> 1] >> (16 * (q & 1))));
-              uint32_t b1 = e4m3x2_to_f16x2(static_cast<uint16_t>(p1[q >> 1] >> (16 * (q & 1))));
-              if (tail) {
-                b0 &= m01;
-                b1 &= m89;
+            for (int q2 = 0; q2 < 2; ++q2) {
+              uint32_t b0[2], b1[2];
+              codes4_to_f16x4<kI8>(p0[q2], b0[0], b0[1]);
+              codes4_to_f16x4<kI8>(p1[q2], b1[0], b1[1]);
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                if (tail) {
+                  b0[q] &= m01;
+                  b1[q] &= m89;
+                }
+                mma_16816<true>(o_acc[4 * x + 2 * q2 + q], pa, b0[q], b1[q]);
               }
-              mma_16816<true>(o_acc[4 * x + q], pa, b0, b1);
             }
           }
         } else {
@@ -775,6 +847,28 @@ __global__ void __launch_bounds__(160, (TileCfg<D, KV, WM>::kMinBlocks))
 
   const size_t n_part = static_cast<size_t>(p.n_part);
   float* const partial = reinterpret_cast<float*>(pipe + C::kMergeBytes);  // [16][D], m[16], l[16]
+  // block-scaled caches: the sink joins a finished row, whose running max it may pass by any
+  // amount (a partition of far keys under ALiBi)
+  auto add_sink = [&]() {
+    if (!kBlk || p.sinks == nullptr || z != 0) return;
+#pragma unroll
+    for (int rr = 0; rr < 2; ++rr) {
+      if (!rv[rr]) continue;
+      const float x = __ldg(p.sinks + rh[rr]) * kLog2e;
+      if (x > m_run[rr]) {  // (from -inf: a row that saw no key)
+        const float f = fast_exp2(m_run[rr] - x);
+        m_run[rr] = x;
+        l_run[rr] = l_run[rr] * f + 1.f;
+#pragma unroll
+        for (int nd = 0; nd < D / 8; ++nd) {
+          o_acc[nd][2 * rr] *= f;
+          o_acc[nd][2 * rr + 1] *= f;
+        }
+      } else {
+        l_run[rr] += fast_exp2(x - m_run[rr]);
+      }
+    }
+  };
   // Rows rr of the warp's fragments: the normalised output (one partition), the
   // partition's max / sum / unnormalised output in the split scratch, or (cluster merge)
   // in this CTA's shared memory.
@@ -807,6 +901,7 @@ __global__ void __launch_bounds__(160, (TileCfg<D, KV, WM>::kMinBlocks))
   };
   if constexpr (C::kWN == 1) {
     // Each warp owns its 16 rows: write straight from registers.
+    add_sink();
     write_rows();
   } else {
     // Four warps hold the same 16 rows over different keys (the pipeline buffers are free:
@@ -861,6 +956,7 @@ __global__ void __launch_bounds__(160, (TileCfg<D, KV, WM>::kMinBlocks))
           o_acc[nd][3] += o4.w;
         }
       }
+      add_sink();
       if (ok) write_rows();
     }
   }
@@ -914,7 +1010,8 @@ cudaError_t launch_tile_t(const TileParams& tp, dim3 grid, int cluster_y, int cl
                             cluster_z, tp);
 }
 
-template <int D>
+// Plain caches (BLK false) or block-scaled ones, in translation units of their own.
+template <int D, bool BLK = false>
 cudaError_t launch_tile_dispatch(const TileParams& tp, dim3 grid, int wm, int kv, bool feat,
                                  bool tma, int cluster_y, int cluster_z, cudaStream_t s) {
 #define UA_TILE_CASE(KVV, WMV)                                                        \
@@ -925,18 +1022,27 @@ cudaError_t launch_tile_dispatch(const TileParams& tp, dim3 grid, int wm, int kv
     return feat ? launch_tile_t<D, KVV, WMV, true, false>(tp, grid, cluster_y, cluster_z, s)     \
                 : launch_tile_t<D, KVV, WMV, false, false>(tp, grid, cluster_y, cluster_z, s);   \
   }
-  UA_TILE_CASE(KV_F16, 1)
-  UA_TILE_CASE(KV_F16, 4)
-  UA_TILE_CASE(KV_BF16, 1)
-  UA_TILE_CASE(KV_BF16, 4)
-  UA_TILE_CASE(KV_E4M3, 1)
-  UA_TILE_CASE(KV_E4M3, 4)
+  if constexpr (BLK) {
+    UA_TILE_CASE(KV_E4M3B, 1)
+    UA_TILE_CASE(KV_E4M3B, 4)
+    UA_TILE_CASE(KV_I8B, 1)
+    UA_TILE_CASE(KV_I8B, 4)
+  } else {
+    UA_TILE_CASE(KV_F16, 1)
+    UA_TILE_CASE(KV_F16, 4)
+    UA_TILE_CASE(KV_BF16, 1)
+    UA_TILE_CASE(KV_BF16, 4)
+    UA_TILE_CASE(KV_E4M3, 1)
+    UA_TILE_CASE(KV_E4M3, 4)
+  }
 #undef UA_TILE_CASE
   return cudaErrorInvalidValue;
 }
 
 template <int D>
 int tile_ctas_per_sm_d(int kv, int wm) {
+  if (kv >= KV_E4M3B)
+    return wm == 1 ? TileCfg<D, KV_I8B, 1>::kMinBlocks : TileCfg<D, KV_I8B, 4>::kMinBlocks;
   if (kv == KV_E4M3)
     return wm == 1 ? TileCfg<D, KV_E4M3, 1>::kMinBlocks : TileCfg<D, KV_E4M3, 4>::kMinBlocks;
   return wm == 1 ? TileCfg<D, KV_BF16, 1>::kMinBlocks : TileCfg<D, KV_BF16, 4>::kMinBlocks;
