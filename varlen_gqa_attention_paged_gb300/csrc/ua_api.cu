@@ -242,7 +242,7 @@ void make_plan(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, int
   const int group = hq / hkv;
   const int kv = kv_kind(sh, kv_dtype);
   const bool blk = kv == ua::KV_E4M3B || kv == ua::KV_I8B;
-  if (blk) allow_tc = allow_dec = false;
+  if (blk) allow_dec = false;
   const long long rows_max = static_cast<long long>(sh->max_seqlen_q) * group;
   const bool tc = allow_tc && rows_max > 16 && group <= 128 && block_size % 16 == 0;
   // decode with at most 8 rows per kv-head: the key-major decode tile (page boxes)
@@ -569,7 +569,12 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
   if (is_tc(pl.kernel)) {
     pp.p = p;
     const int nq = pl.kernel == ua::KERNEL_TC256 ? 2 : 1;
-    switch (d) {
+    if (blk_scales) {
+      const auto launch = d == 64    ? ua::launch_prefill_blk_d64
+                          : d == 128 ? ua::launch_prefill_blk_d128
+                                     : ua::launch_prefill_blk_d256;
+      err = launch(pp, grid, kv, feat, nq, st);
+    } else switch (d) {
       case 64: err = ua::launch_prefill_d64(pp, grid, kv, feat, nq, st); break;
       case 128: err = ua::launch_prefill_d128(pp, grid, kv, feat, nq, st); break;
       default: err = ua::launch_prefill_d256(pp, grid, kv, feat, nq, st); break;

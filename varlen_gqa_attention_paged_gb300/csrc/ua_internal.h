@@ -149,6 +149,14 @@ cudaError_t launch_prefill_d128(const PrefillParams& pp, dim3 grid, int kv, bool
 cudaError_t launch_prefill_d256(const PrefillParams& pp, dim3 grid, int kv, bool feat, int nq,
                                cudaStream_t s);
 
+// the same for the block-scaled kinds
+cudaError_t launch_prefill_blk_d64(const PrefillParams& pp, dim3 grid, int kv, bool feat, int nq,
+                                   cudaStream_t s);
+cudaError_t launch_prefill_blk_d128(const PrefillParams& pp, dim3 grid, int kv, bool feat, int nq,
+                                    cudaStream_t s);
+cudaError_t launch_prefill_blk_d256(const PrefillParams& pp, dim3 grid, int kv, bool feat, int nq,
+                                    cudaStream_t s);
+
 // Plan kernel codes.
 enum : int { KERNEL_TILE16 = 1, KERNEL_DEC8 = 2, KERNEL_TILE64 = 4, KERNEL_TC128 = 8, KERNEL_TC256 = 16,
              KERNEL_DEC8W = 32, KERNEL_DEC8P = 64 };

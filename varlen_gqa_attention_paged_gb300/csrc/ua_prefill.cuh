@@ -74,4 +74,46 @@ __device__ __forceinline__ PfSeq pf_seq_of_slot(const int32_t* __restrict__ cu,
   return r;
 }
 
+// Block-scaled caches (BLK 1: e4m3 codes, 2: int8).  Per key tile the dequant warps leave, for
+// each of its eight 16-key groups (one block's), the K scale, log2 of the V scale and its
+// reciprocal in a ring of shared memory; the softmax takes
+//   x = c ks s + log2 vs,   w = 2^(x - M),   l += w / vs,   O += w (codes)
+// with M the running max of x: one FMA per score as without scales, P.V on the codes, and
+// weights that stay in f16's range whatever the scales are.
+constexpr int kTileGroups = 8;
+struct GroupScales {
+  float kf[kTileGroups], vl[kTileGroups], vi[kTileGroups];
+};
+
+// The scales of key `key`'s block (both 1 past ke, or for a bad block).
+__device__ __forceinline__ float2 key_block_scales(const AttnParams& p, const int32_t* bt, int g,
+                                                   int key, int ke) {
+  if (key >= ke) return make_float2(1.f, 1.f);
+  const int col = key / p.block_size;
+  const int blk = col < p.max_blocks_per_seq ? __ldg(bt + col) : -1;
+  if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks))
+    return make_float2(1.f, 1.f);
+  return make_float2(__ldg(p.k_scale_blk + blk * p.k_blk_stride[0] + g * p.k_blk_stride[1]),
+                     __ldg(p.v_scale_blk + blk * p.v_blk_stride[0] + g * p.v_blk_stride[1]));
+}
+
+__device__ __forceinline__ void put_group_scales(GroupScales* dst, int grp, float2 s) {
+  const float vs = block_scale(s.y);
+  dst->kf[grp] = block_scale(s.x);
+  dst->vl[grp] = fast_log2(vs);
+  dst->vi[grp] = fast_rcp(vs);
+}
+
+// The sink (log2 units x) joins a finished row: returns the factor its O takes.
+__device__ __forceinline__ float late_sink(float x, float& m, float& l) {
+  if (x > m) {  // (from -inf: a row that saw no key)
+    const float f = fast_exp2(m - x);
+    m = x;
+    l = l * f + 1.f;
+    return f;
+  }
+  l += fast_exp2(x - m);
+  return 1.f;
+}
+
 }  // namespace ua

@@ -52,7 +52,7 @@ namespace ua {
 
 // SW: softmax warps per tensor-memory lane quarter of a q tile (1, or 2 or 4 splitting the
 // key columns of S and the columns of O between them).
-template <int D, int NQ, bool F8 = false, int SW = 1>
+template <int D, int NQ, bool F8 = false, int SW = 1, int BLK = 0>
 struct PrefillTmCfg {
   static constexpr int kBM = 128;                        // MMA rows of one q tile
   static constexpr int kBN = 128;                        // keys per tile
@@ -73,8 +73,13 @@ struct PrefillTmCfg {
       (227 * 1024 - 1024 - kBarBytes - NQ * kQBytes - kF8Bytes - kXchBytes) / kTileBytes;
   static constexpr int kRingK = (kSlots + 1) / 2 > 4 ? 4 : (kSlots + 1) / 2;
   static constexpr int kRingV = kSlots / 2 > 4 ? 4 : kSlots / 2;
-  static constexpr int kSmemBytes =
-      1024 + NQ * kQBytes + (kRingK + kRingV) * kTileBytes + kF8Bytes + kBarBytes + kXchBytes;
+  // block-scaled caches: a tile's group scales, written once its K slot is free, which is
+  // after Q K^T of tile j - kRingK and so after the softmax of tile j - kRingK - 2: tiles
+  // j - kRingK - 1 .. j may still be read
+  static constexpr int kScaleSlots = BLK ? kRingK + 2 : 0;
+  static constexpr int kScaleBytes = kScaleSlots * 96;
+  static constexpr int kSmemBytes = 1024 + NQ * kQBytes + (kRingK + kRingV) * kTileBytes +
+                                    kF8Bytes + kBarBytes + kXchBytes + kScaleBytes;
   static constexpr int kTmemStride = kBN + D;            // S/P, then O, of one q tile
   static constexpr int kTmemCols = 512;
   static constexpr int kSoftmaxWarps = 4 * NQ * SW;
@@ -83,15 +88,18 @@ struct PrefillTmCfg {
   static constexpr int kThreads = 32 * kSoftmaxWarps + 96 + 32 * kDeqWarps;
   static_assert(D <= 128, "two 128-key K/V rings must fit");
   static_assert(NQ * kTmemStride <= kTmemCols, "tensor memory budget");
-  static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+  // (16 bytes of static shared memory beside it)
+  static_assert(kSmemBytes + 16 <= 227 * 1024, "shared memory budget");
+  static_assert(BLK == 0 || F8, "block scales go with 8-bit codes");
+  static_assert(sizeof(GroupScales) == 96);
   static_assert(kRingK >= 2 && kRingV >= 2, "at least double-buffered K and V");
   static_assert(!F8 || D == 64 || D == 128, "fp8 caches: head_dim 64 or 128");
 };
 
-template <int D, int NQ, bool BF16, bool FEAT, bool F8 = false, int SW = 1>
-__global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW>::kThreads, 1)
+template <int D, int NQ, bool BF16, bool FEAT, bool F8 = false, int SW = 1, int BLK = 0>
+__global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
     ua_prefill_tm_kernel(const __grid_constant__ PrefillParams pp) {
-  using C = PrefillTmCfg<D, NQ, F8, SW>;
+  using C = PrefillTmCfg<D, NQ, F8, SW, BLK>;
   constexpr int BN = C::kBN;
   constexpr int RK = C::kRingK, RV = C::kRingV;
   constexpr int kProducerK = C::kSoftmaxWarps, kProducerV = C::kSoftmaxWarps + 1;
@@ -135,6 +143,11 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW>::kThreads, 1)
   // the final row-sum exchange ([NQ][4][2]), and the exchanged maxima
   uint64_t* const xch_bars = reinterpret_cast<uint64_t*>(lo_flag + 2 * NQ + 1);  // 8-byte aligned
   uint16_t* const xch = reinterpret_cast<uint16_t*>(bars) + C::kBarBytes / 2;  // [NQ][2][SW][128]
+  // block-scaled caches: the group scales of a tile (slot j mod kScaleSlots) and their barriers
+  uint64_t* const sc_full = bars + 48;
+  static_assert(C::kScaleSlots <= 8 && 56 * 8 <= C::kBarBytes);
+  GroupScales* const scales =
+      reinterpret_cast<GroupScales*>(reinterpret_cast<uint8_t*>(xch) + C::kXchBytes);
   __shared__ int s_abort;
 
   const int warp = threadIdx.x >> 5;
@@ -166,6 +179,7 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW>::kThreads, 1)
     }
     if constexpr (SW > 1)
       for (int i = 0; i < NQ * 4 * 2; ++i) mbar_init(&xch_bars[i], 32 * SW);
+    for (int i = 0; i < C::kScaleSlots; ++i) mbar_init(&sc_full[i], C::kDeqWarps);
     mbar_init(s_full_b(1), 1);
     mbar_init(p_full_b(1), 4 * SW);
     for (int qt = 0; qt < NQ; ++qt) {
@@ -466,8 +480,11 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW>::kThreads, 1)
     if (lane == 0) mbar_arrive(q_ready);
     // per-token scales: each key's K (V) row is written times its own scale, rounded once
     // to f16 (0 for keys past the partition's walk)
-    const bool tok = p.k_scale_tok != nullptr;
+    const bool tok = BLK == 0 && p.k_scale_tok != nullptr;
     const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_blocks_per_seq;
+    // block scales, loaded a tile ahead (16 threads a group)
+    float2 bsc = make_float2(1.f, 1.f);
+    if constexpr (BLK != 0) bsc = key_block_scales(p, bt, g, ks + (td & ~15), ke);
     auto key_scale = [&](int j, int op) -> float {
       const int key = ks + j * BN + td;
       if (key >= ke) return 0.f;
@@ -514,6 +531,14 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW>::kThreads, 1)
           ok = false;
           break;
         }
+        if constexpr (BLK != 0) {
+          if (op == 0) {
+            if ((td & 15) == 0) put_group_scales(scales + j % C::kScaleSlots, td >> 4, bsc);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sc_full[j % C::kScaleSlots]);
+            bsc = key_block_scales(p, bt, g, ks + (j + 1) * BN + (td & ~15), ke);
+          }
+        }
         uint8_t* dst = (op ? sV : sK) + (j % R) * C::kTileBytes + td * 128;
         const bool zero = op == 1 && ks + j * BN + td >= kv_len;
 #pragma unroll
@@ -522,7 +547,7 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW>::kThreads, 1)
           const uint32_t w[4] = {r.x, r.y, r.z, r.w};
           uint32_t h[8];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) e4m3x4_to_f16x4(w[q], h[2 * q], h[2 * q + 1]);
+          for (int q = 0; q < 4; ++q) codes4_to_f16x4<BLK == 2>(w[q], h[2 * q], h[2 * q + 1]);
           if (tok) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -590,13 +615,14 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW>::kThreads, 1)
     // FMA.  Otherwise scores are transformed first and c = log2(e).
     // fp8: the per-tensor k_scale joins the score scale, v_scale the output
     // (per-token scales are already in the f16 tiles)
-    const bool tok8 = F8 && p.k_scale_tok != nullptr;
-    const float kq = F8 && !tok8 ? p.scale * __ldg(p.kv_scale) : p.scale;
-    const float v_mul = F8 && !tok8 ? __ldg(p.kv_scale + 1) : 1.f;
+    const bool own8 = F8 && (BLK != 0 || p.k_scale_tok != nullptr);
+    const float kq = F8 && !own8 ? p.scale * __ldg(p.kv_scale) : p.scale;
+    float v_mul = F8 && !own8 ? __ldg(p.kv_scale + 1) : 1.f;
     const float c = FEAT ? kLog2e : kq * kLog2e;
     const bool sink = p.sinks != nullptr && z == 0 && rv;
-    float m_used = sink ? __ldg(p.sinks + h) * kLog2e : -INFINITY;
-    float l = sink && half == 0 ? 1.f : 0.f;  // the sink's share, counted once per row
+    // (block-scaled caches, whose running max carries the V scales, add the sink at the end)
+    float m_used = sink && BLK == 0 ? __ldg(p.sinks + h) * kLog2e : -INFINITY;
+    float l = sink && BLK == 0 && half == 0 ? 1.f : 0.f;  // the sink's share, once per row
     // one q tile: S buffers at columns 0 and BN, O at 2 BN; two: tile qt's S then O
     constexpr bool DB = NQ == 1;
     const uint32_t lane_off = (32u * quad) << 16;
@@ -644,12 +670,33 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW>::kThreads, 1)
       const bool rewrite = FEAT || need_mask;
       float mx0 = -INFINITY, mx1 = -INFINITY;
       constexpr bool kTwo = kCols >= 64;  // two 32-column loads an iteration
+      const GroupScales* const gs = scales + (jb + n) % (BLK ? C::kScaleSlots : 1);
+      if constexpr (BLK != 0) {
+        static_assert(kTwo, "four groups an iteration");
+        if (!pf_wait_warp(&sc_full[(jb + n) % C::kScaleSlots], ((jb + n) / C::kScaleSlots) & 1,
+                          abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+      }
 #pragma unroll 1
       for (int c0 = half * kCols; c0 < (half + 1) * kCols; c0 += kTwo ? 64 : 32) {
         uint32_t ra[32], rb[32];
         tmem_ld32(tS + c0, ra);
         if constexpr (kTwo) tmem_ld32(tS + c0 + 32, rb);
+        float kf[4] = {1.f, 1.f, 1.f, 1.f};
+        if constexpr (BLK != 0) {
+          const float4 k4 = *reinterpret_cast<const float4*>(gs->kf + c0 / 16);
+          kf[0] = k4.x, kf[1] = k4.y, kf[2] = k4.z, kf[3] = k4.w;
+        }
         tmem_ld_wait();
+        if constexpr (BLK != 0 && FEAT) {  // the features apply to scores with their K scale
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            ra[e] = __float_as_uint(__uint_as_float(ra[e]) * kf[e / 16]);
+            rb[e] = __float_as_uint(__uint_as_float(rb[e]) * kf[2 + e / 16]);
+          }
+        }
         if (rewrite) {
           const float ab = FEAT ? slope * static_cast<float>(k0 + c0 - ctx) : 0.f;
           if (need_mask) {
@@ -670,14 +717,30 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW>::kThreads, 1)
           tmem_st32(tS + c0, ra);
           if constexpr (kTwo) tmem_st32(tS + c0 + 32, rb);
         }
+        if constexpr (BLK != 0) {  // the groups' own maxima, scaled; mx0 is in log2 units
+          const float4 l4 = *reinterpret_cast<const float4*>(gs->vl + c0 / 16);
+          const float vl[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          mx0 = fmax3(mx0, __uint_as_float(ra[e]), __uint_as_float(ra[e + 1]));
-          if constexpr (kTwo) mx1 = fmax3(mx1, __uint_as_float(rb[e]), __uint_as_float(rb[e + 1]));
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t* r16 = (q < 2 ? ra : rb) + 16 * (q & 1);
+            float mg = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2)
+              mg = fmax3(mg, __uint_as_float(r16[e]), __uint_as_float(r16[e + 1]));
+            mx0 = fmaxf(mx0, fmaf(mg, FEAT ? c : c * kf[q], vl[q]));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            mx0 = fmax3(mx0, __uint_as_float(ra[e]), __uint_as_float(ra[e + 1]));
+            if constexpr (kTwo)
+              mx1 = fmax3(mx1, __uint_as_float(rb[e]), __uint_as_float(rb[e + 1]));
+          }
         }
       }
       if (rewrite) tmem_st_wait();
-      float mx = fmaxf(mx0, mx1) * c;  // row max in log2 units (-inf stays -inf)
+      // row max in log2 units (-inf stays -inf)
+      float mx = BLK != 0 ? mx0 : fmaxf(mx0, mx1) * c;
       if constexpr (SW > 1) {
         // the row's other column slices: every lane arrives once its value is written.  Two
         // slots: a warp writes tile n + 2's slot only after its S wait, which follows the
@@ -727,15 +790,31 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW>::kThreads, 1)
 
       // ---- pass 2: P = 2^(c s - m) over S, 32 keys at a time: 16 columns of high part
       // (bf16 or f16 pairs), then 16 columns of bf16 remainder (zeros when not needed)
-      const float2 cc = make_float2(c, c), mm = make_float2(-m_use, -m_use);
+      float2 cc = make_float2(c, c), mm = make_float2(-m_use, -m_use);
       float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+      float lacc = 0.f;  // block-scaled: the sum of w / vs
       // one 32-key group: P and its remainder over the group's S columns
       auto p_group = [&](int c0, uint32_t* rr) {
         float xv[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) xv[e] = __uint_as_float(rr[e]);
+        float2 kf2, vl2, vi2;  // block-scaled: the two groups' scales
+        if constexpr (BLK != 0) {
+          kf2 = *reinterpret_cast<const float2*>(gs->kf + c0 / 16);
+          vl2 = *reinterpret_cast<const float2*>(gs->vl + c0 / 16);
+          vi2 = *reinterpret_cast<const float2*>(gs->vi + c0 / 16);
+        }
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
+          if constexpr (BLK != 0) {
+            if (e % 16 == 0) {
+              const float f = FEAT ? c : c * (e ? kf2.y : kf2.x);
+              const float o = (e ? vl2.y : vl2.x) - m_use;
+              cc = make_float2(f, f);
+              mm = make_float2(o, o);
+              acc0 = acc1 = make_float2(0.f, 0.f);
+            }
+          }
           const float2 u = __ffma2_rn(make_float2(xv[e], xv[e + 1]), cc, mm);
           const float2 w = __ffma2_rn(make_float2(xv[e + 2], xv[e + 3]), cc, mm);
           xv[e] = fast_exp2(u.x);
@@ -744,6 +823,10 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW>::kThreads, 1)
           xv[e + 3] = fast_exp2(w.y);
           acc0 = __fadd2_rn(acc0, make_float2(xv[e], xv[e + 1]));
           acc1 = __fadd2_rn(acc1, make_float2(xv[e + 2], xv[e + 3]));
+          if constexpr (BLK != 0) {
+            if (e % 16 == 12)
+              lacc = fmaf((acc0.x + acc0.y) + (acc1.x + acc1.y), e > 16 ? vi2.y : vi2.x, lacc);
+          }
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -766,7 +849,7 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW>::kThreads, 1)
         tmem_ld_wait();
         p_group(c0, rr);
       }
-      l = l * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y));
+      l = l * alpha + (BLK != 0 ? lacc : (acc0.x + acc0.y) + (acc1.x + acc1.y));
       tmem_st_wait();
       if (warp_lo && lane == 0) lo_flag[2 * qt + (n & 1)] = n + 1;
       tc_fence_before();
@@ -801,6 +884,7 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW>::kThreads, 1)
         }
       }
     }
+    if (BLK != 0 && sink) v_mul = late_sink(__ldg(p.sinks + h) * kLog2e, m_used, l);
     if (ok && active) {
       const size_t orow = static_cast<size_t>(q0 + i_q) * p.hq + h;
       const size_t n_part = static_cast<size_t>(p.n_part);
@@ -907,11 +991,11 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW>::kThreads, 1)
 // (the dequant warps' registers).  A CTA would otherwise have one softmax warp per SM
 // sub-partition.  Two q tiles already alternate on the tensor cores; splitting their
 // softmax too measured slower on GB300 (the d128 long prefill went from 1.12 to 1.19 ms).
-template <int D, int NQ, bool BF16, bool FEAT, bool F8 = false>
+template <int D, int NQ, bool BF16, bool FEAT, bool F8 = false, int BLK = 0>
 cudaError_t launch_prefill_tm_t(const PrefillParams& pp, dim3 grid, cudaStream_t stream) {
   constexpr int SW = NQ == 1 ? (D == 128 && !F8 ? 4 : 2) : 1;
-  using C = PrefillTmCfg<D, NQ, F8, SW>;
-  auto kern = ua_prefill_tm_kernel<D, NQ, BF16, FEAT, F8, SW>;
+  using C = PrefillTmCfg<D, NQ, F8, SW, BLK>;
+  auto kern = ua_prefill_tm_kernel<D, NQ, BF16, FEAT, F8, SW, BLK>;
   static std::atomic<unsigned long long> configured{0};  // one bit per device
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -937,6 +1021,19 @@ cudaError_t launch_prefill_tm_nq(const PrefillParams& pp, dim3 grid, int kv, boo
   if (kv == KV_E4M3)
     return feat ? launch_prefill_tm_t<D, NQ, false, true, true>(pp, grid, s)
                 : launch_prefill_tm_t<D, NQ, false, false, true>(pp, grid, s);
+  return cudaErrorInvalidValue;
+}
+
+// Block-scaled caches (in a translation unit of their own).
+template <int D, int NQ>
+cudaError_t launch_prefill_tm_blk(const PrefillParams& pp, dim3 grid, int kv, bool feat,
+                                  cudaStream_t s) {
+  if (kv == KV_E4M3B)
+    return feat ? launch_prefill_tm_t<D, NQ, false, true, true, 1>(pp, grid, s)
+                : launch_prefill_tm_t<D, NQ, false, false, true, 1>(pp, grid, s);
+  if (kv == KV_I8B)
+    return feat ? launch_prefill_tm_t<D, NQ, false, true, true, 2>(pp, grid, s)
+                : launch_prefill_tm_t<D, NQ, false, false, true, 2>(pp, grid, s);
   return cudaErrorInvalidValue;
 }
 

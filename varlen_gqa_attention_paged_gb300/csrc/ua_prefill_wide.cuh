@@ -48,7 +48,7 @@ namespace ua {
 // write it into its f16 slot, exactly (every e4m3 value is an f16), so the f16 MMAs and the softmax run
 // unchanged; k_scale joins the score scale and v_scale the output (per-token scales:
 // folded into each key's f16 row instead).
-template <int D, bool F8 = false>
+template <int D, bool F8 = false, int BLK = 0>
 struct PrefillWideCfg {
   static constexpr int kBM = 128;                   // MMA rows of the q tile
   static constexpr int kBN = 128;                   // keys per tile
@@ -61,8 +61,11 @@ struct PrefillWideCfg {
   static constexpr int kStage = F8 ? 2 : 0;         // fp8: staging slots of codes
   static constexpr int kStageBytes = kBN * 128;     // one staged half tile of codes
   static constexpr int kBarBytes = 512;
-  static constexpr int kSmemBytes =
-      1024 + kQBytes + kSlots * kSlotBytes + kStage * kStageBytes + kBarBytes;
+  // block-scaled caches: a tile's group scales, written once the first half of its K tile has
+  // its slot, which is after Q K^T of tile j - 1 and so after the softmax of tile j - 3
+  static constexpr int kScaleSlots = BLK ? 4 : 0;
+  static constexpr int kSmemBytes = 1024 + kQBytes + kSlots * kSlotBytes + kStage * kStageBytes +
+                                    kBarBytes + kScaleSlots * 96;
   static constexpr int kTmemCols = 512;             // S0, S1, O
   // TMA producer warps: a 16-bit half tile is 16 page boxes, an fp8 one 8.  Each producer
   // reuses the staging slot of its own previous item, so the fp8 staging ring holds as many
@@ -86,10 +89,10 @@ __device__ __forceinline__ int wide_item_v(int j, int h, int nt) {
   return j < nt - 1 ? 4 * j + 4 + h : 4 * j + 2 + h;
 }
 
-template <int D, bool BF16, bool FEAT, bool F8 = false>
-__global__ void __launch_bounds__(PrefillWideCfg<D, F8>::kThreads, 1)
+template <int D, bool BF16, bool FEAT, bool F8 = false, int BLK = 0>
+__global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
     ua_prefill_wide_kernel(const __grid_constant__ PrefillParams pp) {
-  using C = PrefillWideCfg<D, F8>;
+  using C = PrefillWideCfg<D, F8, BLK>;
   constexpr int BN = C::kBN;
   constexpr int NS = C::kSlots;
   constexpr int kMma = 4 + C::kProducers;
@@ -118,6 +121,10 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8>::kThreads, 1)
   uint64_t* const s8_empty = s8_full + C::kStage;     // [kStage]
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(s8_empty + C::kStage);
   int* const lo_flag = reinterpret_cast<int*>(tmem_holder + 1);  // [2]: step + 1 when P_lo matters
+  // block-scaled caches: the group scales of a tile (slot j mod kScaleSlots) and their barriers
+  uint64_t* const sc_full = bars + 40;
+  GroupScales* const scales =
+      reinterpret_cast<GroupScales*>(reinterpret_cast<uint8_t*>(bars) + C::kBarBytes);
   __shared__ int s_abort;
   __shared__ int s_last[C::kProducers];  // last item each producer warp issued
 
@@ -149,6 +156,7 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8>::kThreads, 1)
         mbar_init(&s8_empty[i], C::kDeqWarps);
       }
     }
+    for (int i = 0; i < C::kScaleSlots; ++i) mbar_init(&sc_full[i], C::kDeqWarps / 2);
     s_abort = 0;
     mbar_fence_init();
   }
@@ -396,8 +404,11 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8>::kThreads, 1)
     fence_proxy_async_smem();  // generic writes, read by the tensor cores
     __syncwarp();
     if (lane == 0) mbar_arrive(q_ready);
-    const bool tok = p.k_scale_tok != nullptr;
+    const bool tok = BLK == 0 && p.k_scale_tok != nullptr;
     const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_blocks_per_seq;
+    // block scales, loaded a tile ahead (16 threads a group)
+    float2 bsc = make_float2(1.f, 1.f);
+    if constexpr (BLK != 0) bsc = key_block_scales(p, bt, g, ks + (td & ~15), ke);
     // the per-token scale of this thread's key of tile j (0 past the partition's keys)
     auto key_scale = [&](int j, bool is_k) -> float {
       const int key = ks + j * BN + td;
@@ -442,6 +453,14 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8>::kThreads, 1)
         ok = false;
         break;
       }
+      if constexpr (BLK != 0) {
+        if (is_k && h == 0 && hc == 0) {  // uniform for the warp
+          if ((td & 15) == 0) put_group_scales(scales + j % C::kScaleSlots, td >> 4, bsc);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sc_full[j % C::kScaleSlots]);
+          bsc = key_block_scales(p, bt, g, ks + (j + 1) * BN + (td & ~15), ke);
+        }
+      }
       uint8_t* dst = sR + sl * C::kSlotBytes + td * 128;
       const bool zero = !is_k && ks + j * BN + td >= kv_len;
 #pragma unroll
@@ -451,7 +470,7 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8>::kThreads, 1)
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
         uint32_t hh[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) e4m3x4_to_f16x4(w[q], hh[2 * q], hh[2 * q + 1]);
+        for (int q = 0; q < 4; ++q) codes4_to_f16x4<BLK == 2>(w[q], hh[2 * q], hh[2 * q + 1]);
         if (tok) {  // the key's scale, rounded once to f16 with each value
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
@@ -495,13 +514,14 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8>::kThreads, 1)
     }
     // fp8: the per-tensor k_scale joins the score scale, v_scale the output (per-token
     // scales are already in the f16 tiles)
-    const bool tok8 = F8 && p.k_scale_tok != nullptr;
-    const float kq = F8 && !tok8 ? p.scale * __ldg(p.kv_scale) : p.scale;
-    const float v_mul = F8 && !tok8 ? __ldg(p.kv_scale + 1) : 1.f;
+    const bool own8 = F8 && (BLK != 0 || p.k_scale_tok != nullptr);
+    const float kq = F8 && !own8 ? p.scale * __ldg(p.kv_scale) : p.scale;
+    float v_mul = F8 && !own8 ? __ldg(p.kv_scale + 1) : 1.f;
     const float c = FEAT ? kLog2e : kq * kLog2e;
     const bool sink = p.sinks != nullptr && z == 0 && rv;
-    float m_used = sink ? __ldg(p.sinks + h) * kLog2e : -INFINITY;
-    float l = sink ? 1.f : 0.f;
+    // (block-scaled caches, whose running max carries the V scales, add the sink at the end)
+    float m_used = sink && BLK == 0 ? __ldg(p.sinks + h) * kLog2e : -INFINITY;
+    float l = sink && BLK == 0 ? 1.f : 0.f;
     const uint32_t lane_off = (32u * warp) << 16;
     const uint32_t tOr = tO + lane_off;
     bool ok = true;
@@ -535,12 +555,32 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8>::kThreads, 1)
       // ---- pass 1: row max; transformed / masked scores written back over S
       const bool rewrite = FEAT || need_mask;
       float mx0 = -INFINITY, mx1 = -INFINITY;
+      const GroupScales* const gs = scales + j % (BLK ? C::kScaleSlots : 1);
+      if constexpr (BLK != 0) {
+        if (!pf_wait_warp(&sc_full[j % C::kScaleSlots], (j / C::kScaleSlots) & 1, abort_flag,
+                          p.status)) {
+          ok = false;
+          break;
+        }
+      }
 #pragma unroll 1
       for (int c0 = 0; c0 < BN; c0 += 64) {
         uint32_t ra[32], rb[32];
         tmem_ld32(tS + c0, ra);
         tmem_ld32(tS + c0 + 32, rb);
+        float kf[4] = {1.f, 1.f, 1.f, 1.f};
+        if constexpr (BLK != 0) {
+          const float4 k4 = *reinterpret_cast<const float4*>(gs->kf + c0 / 16);
+          kf[0] = k4.x, kf[1] = k4.y, kf[2] = k4.z, kf[3] = k4.w;
+        }
         tmem_ld_wait();
+        if constexpr (BLK != 0 && FEAT) {  // the features apply to scores with their K scale
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            ra[e] = __float_as_uint(__uint_as_float(ra[e]) * kf[e / 16]);
+            rb[e] = __float_as_uint(__uint_as_float(rb[e]) * kf[2 + e / 16]);
+          }
+        }
         if (rewrite) {
           const float ab = FEAT ? slope * static_cast<float>(k0 + c0 - ctx) : 0.f;
           if (need_mask) {
@@ -559,14 +599,28 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8>::kThreads, 1)
           tmem_st32(tS + c0, ra);
           tmem_st32(tS + c0 + 32, rb);
         }
+        if constexpr (BLK != 0) {  // the groups' own maxima, scaled; mx0 is in log2 units
+          const float4 l4 = *reinterpret_cast<const float4*>(gs->vl + c0 / 16);
+          const float vl[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          mx0 = fmax3(mx0, __uint_as_float(ra[e]), __uint_as_float(ra[e + 1]));
-          mx1 = fmax3(mx1, __uint_as_float(rb[e]), __uint_as_float(rb[e + 1]));
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t* r16 = (q < 2 ? ra : rb) + 16 * (q & 1);
+            float mg = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2)
+              mg = fmax3(mg, __uint_as_float(r16[e]), __uint_as_float(r16[e + 1]));
+            mx0 = fmaxf(mx0, fmaf(mg, FEAT ? c : c * kf[q], vl[q]));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            mx0 = fmax3(mx0, __uint_as_float(ra[e]), __uint_as_float(ra[e + 1]));
+            mx1 = fmax3(mx1, __uint_as_float(rb[e]), __uint_as_float(rb[e + 1]));
+          }
         }
       }
       if (rewrite) tmem_st_wait();
-      const float mx = fmaxf(mx0, mx1) * c;
+      const float mx = BLK != 0 ? mx0 : fmaxf(mx0, mx1) * c;
       float alpha = 1.f;
       const bool grow = mx > m_used + 8.f || (m_used == -INFINITY && mx > -INFINITY);
       if (grow) {
@@ -605,8 +659,9 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8>::kThreads, 1)
 
       // ---- pass 2: P = 2^(c s - m) over S, 32 keys at a time (16 columns of high part,
       // then, when the tile needs it, 16 of bf16 remainder)
-      const float2 cc = make_float2(c, c), mm = make_float2(-m_use, -m_use);
+      float2 cc = make_float2(c, c), mm = make_float2(-m_use, -m_use);
       float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+      float lacc = 0.f;  // block-scaled: the sum of w / vs
 #pragma unroll 1
       for (int c0 = 0; c0 < BN; c0 += 32) {
         uint32_t rr[32];
@@ -615,8 +670,23 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8>::kThreads, 1)
         float xv[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) xv[e] = __uint_as_float(rr[e]);
+        float2 kf2, vl2, vi2;  // block-scaled: the two groups' scales
+        if constexpr (BLK != 0) {
+          kf2 = *reinterpret_cast<const float2*>(gs->kf + c0 / 16);
+          vl2 = *reinterpret_cast<const float2*>(gs->vl + c0 / 16);
+          vi2 = *reinterpret_cast<const float2*>(gs->vi + c0 / 16);
+        }
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
+          if constexpr (BLK != 0) {
+            if (e % 16 == 0) {
+              const float f = FEAT ? c : c * (e ? kf2.y : kf2.x);
+              const float o = (e ? vl2.y : vl2.x) - m_use;
+              cc = make_float2(f, f);
+              mm = make_float2(o, o);
+              acc0 = acc1 = make_float2(0.f, 0.f);
+            }
+          }
           const float2 u = __ffma2_rn(make_float2(xv[e], xv[e + 1]), cc, mm);
           const float2 w = __ffma2_rn(make_float2(xv[e + 2], xv[e + 3]), cc, mm);
           xv[e] = fast_exp2(u.x);
@@ -625,6 +695,10 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8>::kThreads, 1)
           xv[e + 3] = fast_exp2(w.y);
           acc0 = __fadd2_rn(acc0, make_float2(xv[e], xv[e + 1]));
           acc1 = __fadd2_rn(acc1, make_float2(xv[e + 2], xv[e + 3]));
+          if constexpr (BLK != 0) {
+            if (e % 16 == 12)
+              lacc = fmaf((acc0.x + acc0.y) + (acc1.x + acc1.y), e > 16 ? vi2.y : vi2.x, lacc);
+          }
         }
         if (tile_lo) {
 #pragma unroll
@@ -644,7 +718,7 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8>::kThreads, 1)
           tmem_st16(tS + c0, hw);
         }
       }
-      l = l * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y));
+      l = l * alpha + (BLK != 0 ? lacc : (acc0.x + acc0.y) + (acc1.x + acc1.y));
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -655,6 +729,7 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8>::kThreads, 1)
     if (ok && nt >= 2) ok = pf_wait_warp(pv_done, (nt - 2) & 1, abort_flag, p.status);
     if (ok && nt >= 1) ok = pf_wait_warp(pv_done, (nt - 1) & 1, abort_flag, p.status);
     tc_fence_after();
+    if (BLK != 0 && sink) v_mul = late_sink(__ldg(p.sinks + h) * kLog2e, m_used, l);
     if (ok) {
       const size_t orow = static_cast<size_t>(q0 + i_q) * p.hq + h;
       const size_t n_part = static_cast<size_t>(p.n_part);
@@ -712,10 +787,10 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8>::kThreads, 1)
   if (warp == kMma) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-template <int D, bool BF16, bool FEAT, bool F8 = false>
+template <int D, bool BF16, bool FEAT, bool F8 = false, int BLK = 0>
 cudaError_t launch_prefill_wide_t(const PrefillParams& pp, dim3 grid, cudaStream_t stream) {
-  using C = PrefillWideCfg<D, F8>;
-  auto kern = ua_prefill_wide_kernel<D, BF16, FEAT, F8>;
+  using C = PrefillWideCfg<D, F8, BLK>;
+  auto kern = ua_prefill_wide_kernel<D, BF16, FEAT, F8, BLK>;
   static std::atomic<unsigned long long> configured{0};  // one bit per device
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
