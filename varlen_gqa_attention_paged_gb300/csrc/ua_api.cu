@@ -242,7 +242,6 @@ void make_plan(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, int
   const int group = hq / hkv;
   const int kv = kv_kind(sh, kv_dtype);
   const bool blk = kv == ua::KV_E4M3B || kv == ua::KV_I8B;
-  if (blk) allow_dec = false;
   const long long rows_max = static_cast<long long>(sh->max_seqlen_q) * group;
   const bool tc = allow_tc && rows_max > 16 && group <= 128 && block_size % 16 == 0;
   // decode with at most 8 rows per kv-head: the key-major decode tile (page boxes)
@@ -250,7 +249,7 @@ void make_plan(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, int
                    static_cast<long long>(sh->num_blocks) * block_size + 16 <= INT32_MAX;
   // fp8 decode with at most 4 rows per kv-head and per-tensor scales: two kv-heads a CTA
   // (their q-blocks fill the tile's 8 columns; one page box carries both heads' rows)
-  const bool pair = dec && kv_dtype == UA_DT_F8E4M3 && rows_max <= 4 && hkv % 2 == 0 &&
+  const bool pair = dec && (kv_dtype == UA_DT_F8E4M3 || blk) && rows_max <= 4 && hkv % 2 == 0 &&
                     sh->k_scale_tok == nullptr;
   const int gy = pair ? hkv / 2 : hkv;  // CTAs of one slot (grid y)
   const int wm = dec ? ua::KERNEL_DEC8 : rows_max <= 16 ? 1 : 4;
@@ -579,6 +578,13 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
       case 128: err = ua::launch_prefill_d128(pp, grid, kv, feat, nq, st); break;
       default: err = ua::launch_prefill_d256(pp, grid, kv, feat, nq, st); break;
     }
+  } else if (blk_scales && dec_kernel && tma) {
+    const bool d64 = d == 64;
+    const auto launch =
+        pl.kernel == ua::KERNEL_DEC8P ? (d64 ? ua::launch_decode_blk_pair_d64 : ua::launch_decode_blk_pair_d128)
+        : pl.kernel == ua::KERNEL_DEC8W ? (d64 ? ua::launch_decode_blk_w8_d64 : ua::launch_decode_blk_w8_d128)
+                                        : (d64 ? ua::launch_decode_blk_w4_d64 : ua::launch_decode_blk_w4_d128);
+    err = launch(tp, grid, kv, feat, pl.cluster_y, pl.cluster_z, st);
   } else if (pl.kernel == ua::KERNEL_DEC8) {
     err = d == 64 ? ua::launch_decode_w4_d64(tp, grid, kv, feat, pl.cluster_y, pl.cluster_z, st)
                   : ua::launch_decode_w4_d128(tp, grid, kv, feat, pl.cluster_y, pl.cluster_z, st);

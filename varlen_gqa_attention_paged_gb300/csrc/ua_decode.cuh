@@ -14,7 +14,10 @@
 // streams 64-key stages of one-head TMA page boxes through an mbarrier ring; the consumers
 // take 16 keys of every stage each (the FA-RDNA2 "Change" 1 packing of a kv-head's GQA
 // heads into one tile; the aiter split-K partitioning); fp8 codes become f16 operands in
-// registers with a permuted head dimension.  The q-block's rows leave a CTA as one
+// registers with a permuted head dimension (int8 codes for Q K^T too, against a q in f16).
+// Block-scaled caches: a 16-key chunk lies in one block, so its two scales are two numbers a
+// warp reads beside the stage; they join the score's factor and its exponent as in the tile
+// kernel (weights w = 2^(x + log2 vs - M), row sums of w / vs).  The q-block's rows leave a CTA as one
 // partial per row in shared memory: written out (one partition), merged with the other
 // partitions of the cluster through distributed shared memory, or handed to the merge
 // kernel through the global scratch.
@@ -49,7 +52,7 @@ struct DecCfg {
   static constexpr int kCB = kRowBytes / kCBW;
   static constexpr int kCBBytes = kT * HP * kCBW;  // one column block of a stage's keys x heads
   static constexpr int kStageBytes = 2 * kCB * kCBBytes;  // K then V
-  static constexpr bool kPermD = KV == KV_E4M3;     // fp8: permuted head dimension
+  static constexpr bool kPermD = KvTraits<KV>::kCodes;  // 8-bit codes: permuted head dimension
   static constexpr int kMT = D / 16;                // O^T m-tiles of 16 d
   // end of a CTA: the warps' maxima and sums [4][8] each, then their O^T fragments
   // [4][kMT][32] float4; then the CTA's partial rows [8][D], maxima [8] and sums [8]
@@ -66,8 +69,10 @@ struct DecCfg {
                                       ? kStages * kStageBytes
                                       : kMergeBytes + kPartBytes;
   static constexpr int kPipeBytes = (kPipeRaw + 1023) & ~1023;
-  // fp8 per-token scales of a stage's keys, K then V, behind the barriers
-  static constexpr int kScaleBytes = kPermD ? kStages * 2 * kT * 4 : 0;
+  // the scales of a stage's keys (per token) or of its 16-key chunks and heads (per block), K
+  // then V, behind the barriers
+  static constexpr int kScales = KvTraits<KV>::kBlk ? W * HP : kT;
+  static constexpr int kScaleBytes = kPermD ? kStages * 2 * kScales * 4 : 0;
   static constexpr int kSmemBytes = 1024 + kPipeBytes + 2 * kStages * 8 + kScaleBytes;
   static constexpr int kMinBlocks = W != 4    ? 1
                                    : HP == 2  ? 2
@@ -76,8 +81,8 @@ struct DecCfg {
   static_assert(W == 4 || W == 8, "four or eight consumer warps");
   static_assert(D <= 128, "the key-major decode tile covers head_dim <= 128");
   static_assert(kRowBytes % kCBW == 0 && kCBW % 16 == 0, "rows are whole column blocks");
-  static_assert(HP == 1 || (HP == 2 && KV == KV_E4M3 && W == 4),
-                "two kv-heads a CTA: fp8 caches, four consumer warps");
+  static_assert(HP == 1 || (HP == 2 && KvTraits<KV>::kCodes && W == 4),
+                "two kv-heads a CTA: 8-bit caches, four consumer warps");
 
   // Line of head h's row of stage key r in a column block: a page box of HP heads lands
   // head by head (16 lines each), so a line's swizzle phase is r mod 8 for every head.
@@ -118,8 +123,10 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP>::kThreads,
   uint8_t* const pipe = smem;
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + C::kPipeBytes);
   uint64_t* const empty = full + S;
-  float* const sks = reinterpret_cast<float*>(empty + S);  // [S][T] K scales (per-token fp8)
-  float* const svs = sks + S * T;                           // [S][T] V scales
+  constexpr bool kBlk = KvTraits<KV>::kBlk, kI8 = KvTraits<KV>::kI8;
+  // [S][T] K scales (per token), or [S][W][HP] (per block: of a chunk and head)
+  float* const sks = reinterpret_cast<float*>(empty + S);
+  float* const svs = sks + S * C::kScales;  // V scales
   __shared__ int s_abort;
 
   const int warp = threadIdx.x >> 5;
@@ -264,6 +271,25 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP>::kThreads,
         cp_async_arrive(&full[s]);
         __syncwarp();
       }
+      if constexpr (kBlk) {  // a page lane's chunk: its block's scales, HP heads
+        if (lane < W) {
+          const int blk = row == oob ? -1 : row / bs;
+#pragma unroll
+          for (int hh = 0; hh < HP; ++hh) {
+            float* const ksd = sks + (s * W + lane) * HP + hh;
+            float* const vsd = svs + (s * W + lane) * HP + hh;
+            if (blk >= 0) {
+              cp_async_4(ksd, p.k_scale_blk + blk * p.k_blk_stride[0] + (g + hh) * p.k_blk_stride[1]);
+              cp_async_4(vsd, p.v_scale_blk + blk * p.v_blk_stride[0] + (g + hh) * p.v_blk_stride[1]);
+            } else {
+              *ksd = 1.f;
+              *vsd = 1.f;
+            }
+          }
+          cp_async_arrive(&full[s]);
+        }
+        __syncwarp();
+      }
       if (lane == 0) mbar_arrive_expect_tx(&full[s], C::kStageBytes);
       __syncwarp();
       issue(s, row);
@@ -323,10 +349,15 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP>::kThreads,
   // e4m3's smallest subnormal, 2^-9, are lost: under 2^-17 of the row's largest value).
   // Lane cq holds d = cq D/4 + 8t + {0..3} (b0) and + {4..7} (b1) of k-step t, the bytes of
   // the K rows it reads; the score then takes the factor 2^-c back.
-  constexpr int kQT = C::kPermD ? QT : 1;
-  uint32_t qt[C::kPermD ? 1 : D / 16][2];
-  uint32_t q8[kQT][C::kPermD ? D / 32 : 1][2];
-  float row_scale[2] = {1.f, 1.f};  // 2^-c of rows 2cq and 2cq + 1 (fp8)
+  //
+  // int8 caches: the codes become f16 in registers, and Q^T f16 under the same power of two
+  // (exact for a bf16 q down to 2^-22 of its row's largest value); lane cq holds d = cq D/4 +
+  // 4 kk + {0, 1} and + {2, 3} of 16-d slice kk.
+  constexpr bool kQ8 = C::kPermD && !kI8;  // e4m3 terms
+  constexpr int kQT = kQ8 ? QT : 1;
+  uint32_t qt[kQ8 ? 1 : D / 16][2];
+  uint32_t q8[kQT][kQ8 ? D / 32 : 1][2];
+  float row_scale[2] = {1.f, 1.f};  // 2^-c of rows 2cq and 2cq + 1 (8-bit caches)
   {
     const int rq = gq % RH;  // column gq: row rq of kv-head g + gq / RH
     const bool qv = rq < nr && q0 + rq / G < p.total_q;
@@ -376,8 +407,15 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP>::kThreads,
       const float down = __uint_as_float(static_cast<uint32_t>(127 - c) << 23);
 #pragma unroll
       for (int i = 0; i < kN; ++i) x[i] *= up;
+      if constexpr (kI8) {
 #pragma unroll
-      for (int term = 0; term < kQT; ++term) {
+        for (int kk = 0; kk < D / 16; ++kk) {
+          qt[kk][0] = pack_f16(x[4 * kk], x[4 * kk + 1]);
+          qt[kk][1] = pack_f16(x[4 * kk + 2], x[4 * kk + 3]);
+        }
+      }
+#pragma unroll
+      for (int term = 0; kQ8 && term < kQT; ++term) {
 #pragma unroll
         for (int t = 0; t < D / 32; ++t) {
 #pragma unroll
@@ -424,7 +462,8 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP>::kThreads,
   float m_run[2], l_run[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const bool sink = p.sinks != nullptr && z == 0 && kgp == 0 && rv[e];
+    // (block-scaled caches, whose running max carries the V scales, add the sink at the end)
+    const bool sink = !kBlk && p.sinks != nullptr && z == 0 && kgp == 0 && rv[e];
     m_run[e] = sink ? __ldg(p.sinks + rh[e]) * kLog2e : -INFINITY;
     l_run[e] = (sink && gq == 0) ? 1.f : 0.f;
   }
@@ -453,7 +492,53 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP>::kThreads,
       // ---- S^T = K Q^T for 16 keys: element e of the accumulator is key kc0 + gq + 8(e>>1),
       // row 2cq + (e & 1)
       float st[4] = {0.f, 0.f, 0.f, 0.f};
-      if constexpr (C::kPermD) {
+      if constexpr (kI8) {
+        // Word j of a lane's 16-byte chunk u holds its d of 16-d slice kk = 4 u + j: the A
+        // registers are the pairs of K rows gq and gq + 8.  Two kv-heads: head g's pairs on
+        // k 0..7 and head g + 1's on k 8..15 against a block-diagonal B, one MMA a pair.  Two
+        // accumulators halve the MMA chain.
+        float sx[2][4];
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sx[a][e] = 0.f;
+        const uint32_t bm0 = gq < RH ? 0xffffffffu : 0u, bm1 = ~bm0;
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) {
+          uint32_t w0[HP][4], w8[HP][4];
+#pragma unroll
+          for (int hh = 0; hh < HP; ++hh) {
+            const uint4 k0 = *reinterpret_cast<const uint4*>(
+                kst + C::raw_byte(16 * ch + gq, cq * (D / 4) + 16 * u, hh));
+            const uint4 k8 = *reinterpret_cast<const uint4*>(
+                kst + C::raw_byte(16 * ch + gq + 8, cq * (D / 4) + 16 * u, hh));
+            w0[hh][0] = k0.x, w0[hh][1] = k0.y, w0[hh][2] = k0.z, w0[hh][3] = k0.w;
+            w8[hh][0] = k8.x, w8[hh][1] = k8.y, w8[hh][2] = k8.z, w8[hh][3] = k8.w;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int kk = 4 * u + j;
+            uint32_t a0[HP][2], a8[HP][2];  // pairs {0, 1} and {2, 3} of rows gq, gq + 8
+#pragma unroll
+            for (int hh = 0; hh < HP; ++hh) {
+              i8x4_to_f16x4(w0[hh][j], a0[hh][0], a0[hh][1]);
+              i8x4_to_f16x4(w8[hh][j], a8[hh][0], a8[hh][1]);
+            }
+            if constexpr (HP == 1) {
+              const uint32_t a[4] = {a0[0][0], a8[0][0], a0[0][1], a8[0][1]};
+              mma_16816<true>(sx[j & 1], a, qt[kk][0], qt[kk][1]);
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t a[4] = {a0[0][h], a8[0][h], a0[HP - 1][h], a8[HP - 1][h]};
+                mma_16816<true>(sx[h], a, qt[kk][h] & bm0, qt[kk][h] & bm1);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st[e] = sx[0][e] + sx[1][e];
+      } else if constexpr (C::kPermD) {
         // Lane (gq, cq) reads bytes [cq D/4, (cq + 1) D/4) of K rows gq and gq + 8: words
         // 2tt and 2tt + 1 of its 16-byte chunk u are the A registers (rows gq | gq + 8) of
         // k-step t = 2u + tt.  One accumulator per Q term keeps the MMA chains short.
@@ -537,6 +622,17 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP>::kThreads,
         }
       }
 
+      // block-scaled: the chunk's scales for this lane's rows (columns 2 cq and 2 cq + 1 belong
+      // to one head), V's as its logarithm and reciprocal
+      float kf = 1.f, vl = 0.f, vi = 1.f;
+      if constexpr (kBlk) {
+        const int at = (s * W + ch) * HP + (2 * cq) / RH;
+        kf = block_scale(sks[at]);
+        const float vs = block_scale(svs[at]);
+        vl = fast_log2(vs);
+        vi = fast_rcp(vs);
+      }
+
       // ---- score transform and mask (log2 domain)
       const bool need_mask = kc0 < lomax || kc0 + 15 > pmin || kc0 + 16 > ke;
 #pragma unroll
@@ -545,13 +641,15 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP>::kThreads,
         const int j = kc0 + gq + 8 * (e >> 1);
         float x;
         if constexpr (FEAT) {
-          x = st[e] * srow[rr];
+          x = st[e] * (kBlk ? srow[rr] * kf : srow[rr]);
           if (p.softcap > 0.f) x = p.softcap * fast_tanh(x * inv_softcap);
           x += slope[rr] * static_cast<float>(j - ctx);
           if (p.qq_bias != nullptr && rv[rr] && j >= ctx && j <= rpos[rr] &&
               ri[rr] < p.max_seqlen_q)
             x += __ldg(p.qq_bias + static_cast<size_t>(ri[rr]) * p.qq_stride + (j - ctx));
-          x *= kLog2e;
+          x = kBlk ? fmaf(x, kLog2e, vl) : x * kLog2e;
+        } else if constexpr (kBlk) {
+          x = fmaf(st[e], srow2[rr] * kf, vl);
         } else {
           x = st[e] * srow2[rr];
         }
@@ -581,7 +679,8 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP>::kThreads,
         const float m_use = (m_run[e] == -INFINITY) ? 0.f : m_run[e];
         st[e] = fast_exp2(st[e] - m_use);
         st[e + 2] = fast_exp2(st[e + 2] - m_use);
-        l_run[e] = l_run[e] * alpha[e] + (st[e] + st[e + 2]);
+        l_run[e] = kBlk ? fmaf(st[e] + st[e + 2], vi, l_run[e] * alpha[e])
+                        : l_run[e] * alpha[e] + (st[e] + st[e + 2]);
       }
       if (__any_sync(0xffffffffu, grow_any)) {
 #pragma unroll
@@ -668,9 +767,9 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP>::kThreads,
             for (int h = 0; h < 2; ++h) {
               const uint32_t w0 = h ? hi0 : lo0, w8 = h ? hi8 : lo8;
               uint32_t a[4];
-              e4m3x4_to_f16x4(w0, a[0], a[1]);
-              e4m3x4_to_f16x4(w8, a[2], a[3]);
-              if (tail) {
+              codes4_to_f16x4<kI8>(w0, a[0], a[1]);
+              codes4_to_f16x4<kI8>(w8, a[2], a[3]);
+              if (!kI8 && tail) {  // (no int8 code is a NaN)
                 a[0] &= m01;
                 a[1] &= m01;
                 a[2] &= m89;
@@ -759,6 +858,17 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP>::kThreads,
   for (int m = 0; m < C::kMT; ++m)
     sm_o[(warp * C::kMT + m) * 32 + lane] = make_float4(ot[m][0], ot[m][1], ot[m][2], ot[m][3]);
   named_bar_sync(1, 32 * W4);
+  // block-scaled: the sink joins rows 2cq and 2cq + 1 (their sum, where warp 0 adds it up)
+  float o_mul[2] = {v_scale, v_scale}, l_sum[2] = {0.f, 0.f};
+  if (warp == 0 || kBlk) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int w = 0; w < W4; ++w) l_sum[e] += sm_l[w * NR + 2 * cq + e];
+      if (kBlk && p.sinks != nullptr && z == 0 && rv[e])
+        o_mul[e] = late_sink(__ldg(p.sinks + rh[e]) * kLog2e, m_run[e], l_sum[e]);
+    }
+  }
   // partial rows (v_scale applied): O^T element (m-tile m, fragment row gq + 8h, column
   // 2cq + e) is output column out_col(m, gq + 8h) of row 2cq + e
   for (int m = warp; m < C::kMT; m += W4) {
@@ -774,16 +884,13 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP>::kThreads,
     const float o[4] = {o4.x, o4.y, o4.z, o4.w};
 #pragma unroll
     for (int e4 = 0; e4 < 4; ++e4)
-      partial[(2 * cq + (e4 & 1)) * D + C::out_col(m, gq + 8 * (e4 >> 1))] = o[e4] * v_scale;
+      partial[(2 * cq + (e4 & 1)) * D + C::out_col(m, gq + 8 * (e4 >> 1))] = o[e4] * o_mul[e4 & 1];
   }
   if (warp == 0 && gq == 0) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float L = 0.f;
-#pragma unroll
-      for (int w = 0; w < W4; ++w) L += sm_l[w * NR + 2 * cq + e];
       partial[NR * D + 2 * cq + e] = m_run[e];
-      partial[NR * D + NR + 2 * cq + e] = L;
+      partial[NR * D + NR + 2 * cq + e] = l_sum[e];
     }
   }
   named_bar_sync(1, 32 * W4);
@@ -889,6 +996,22 @@ cudaError_t launch_decode_width(const TileParams& tp, dim3 grid, int kv, bool fe
   return cudaErrorInvalidValue;
 }
 
+// The block-scaled kinds (in translation units of their own); HP kv-heads a CTA.
+template <int D, int W, int HP = 1>
+cudaError_t launch_decode_blk(const TileParams& tp, dim3 grid, int kv, bool feat, int cluster_y,
+                              int cluster_z, cudaStream_t s) {
+#define UA_DEC_CASE(KVV, QT)                                                                   \
+  return feat ? launch_decode_t<D, KVV, true, QT, W, HP>(tp, grid, cluster_y, cluster_z, s)    \
+              : launch_decode_t<D, KVV, false, QT, W, HP>(tp, grid, cluster_y, cluster_z, s);
+  if (kv == KV_I8B) UA_DEC_CASE(KV_I8B, 1)
+  if (kv == KV_E4M3B) {
+    if (tp.p.q_dtype == UA_DT_BF16) UA_DEC_CASE(KV_E4M3B, 2)
+    UA_DEC_CASE(KV_E4M3B, 3)
+  }
+#undef UA_DEC_CASE
+  return cudaErrorInvalidValue;
+}
+
 // Two kv-heads a CTA (fp8 caches, four consumer warps; tensor maps over the head-outer
 // view with boxes of two heads).
 template <int D>
@@ -907,7 +1030,8 @@ cudaError_t launch_decode_pair(const TileParams& tp, dim3 grid, bool feat, int c
 template <int D, int KV, int W, int HP = 1>
 int decode_cluster_capacity_t(int cluster_y, int cluster_z) {
   using C = DecCfg<D, KV, W, HP>;
-  auto kern = ua_decode_kernel<D, KV, false, KV == KV_E4M3 ? 2 : 1, W, HP>;
+  constexpr bool kQ8 = KvTraits<KV>::kCodes && !KvTraits<KV>::kI8;
+  auto kern = ua_decode_kernel<D, KV, false, kQ8 ? 2 : 1, W, HP>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) !=
           cudaSuccess ||
       cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
@@ -936,6 +1060,7 @@ int decode_cluster_capacity_d(int kv, int cluster_y, int cluster_z) {
 
 template <int D>
 int decode_ctas_per_sm_d(int kv) {
+  if (kv == KV_I8B || kv == KV_E4M3B) return DecCfg<D, KV_I8B>::kMinBlocks;
   if (kv == KV_E4M3) return DecCfg<D, KV_E4M3>::kMinBlocks;
   return DecCfg<D, KV_BF16>::kMinBlocks;
 }

@@ -23,13 +23,17 @@ int decode_cluster_capacity(int head_dim, int kv, bool wide, bool pair, int clus
   static std::map<std::array<int, 6>, int> cache;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return -1;
-  const std::array<int, 6> key = {dev, head_dim, kv == KV_E4M3 ? 1 : 0,
+  const std::array<int, 6> key = {dev, head_dim, kv < KV_E4M3 ? KV_BF16 : kv,
                                   pair ? 2 : wide ? 1 : 0, cluster_y, cluster_z};
   std::lock_guard<std::mutex> lock(mu);
   auto it = cache.find(key);
   if (it != cache.end()) return it->second;
   int n;
-  if (pair) n = decode_cluster_capacity_pair(head_dim, cluster_y, cluster_z);
+  if (kv >= KV_E4M3B)
+    n = (pair   ? decode_cluster_capacity_blk_pair
+         : wide ? decode_cluster_capacity_blk_w8
+                : decode_cluster_capacity_blk_w4)(head_dim, kv, cluster_y, cluster_z);
+  else if (pair) n = decode_cluster_capacity_pair(head_dim, cluster_y, cluster_z);
   else if (wide) n = decode_cluster_capacity_w8(head_dim, kv, cluster_y, cluster_z);
   else n = head_dim == 64 ? decode_cluster_capacity_d<64, 4>(kv, cluster_y, cluster_z)
                           : decode_cluster_capacity_d<128, 4>(kv, cluster_y, cluster_z);

@@ -494,6 +494,19 @@ __device__ __forceinline__ float block_scale(float s) {
   return fminf(fmaxf(s, 1.f / 1099511627776.f), 1099511627776.f);
 }
 
+// The sink (log2 units x) joins a finished row of a block-scaled cache, whose
+// running max m carries the V scales and may lie far below: returns the factor its O takes.
+__device__ __forceinline__ float late_sink(float x, float& m, float& l) {
+  if (x > m) {  // (from -inf: a row that saw no key)
+    const float f = fast_exp2(m - x);
+    m = x;
+    l = l * f + 1.f;
+    return f;
+  }
+  l += fast_exp2(x - m);
+  return 1.f;
+}
+
 // Two floats -> two e4m3fn codes (round to nearest even, saturating at +-448), `lo` in the
 // low byte.
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {

@@ -134,6 +134,22 @@ cudaError_t launch_decode_pair_d128(const TileParams& tp, dim3 grid, bool feat, 
                                     int cluster_z, cudaStream_t s);
 int decode_cluster_capacity_pair(int head_dim, int cluster_y, int cluster_z);
 int decode_pair_ctas_per_sm(int head_dim);
+// the decode tile for the block-scaled kinds: four consumer warps, eight, two kv-heads a CTA
+cudaError_t launch_decode_blk_w4_d64(const TileParams& tp, dim3 grid, int kv, bool feat,
+                                       int cluster_y, int cluster_z, cudaStream_t s);
+cudaError_t launch_decode_blk_w4_d128(const TileParams& tp, dim3 grid, int kv, bool feat,
+                                       int cluster_y, int cluster_z, cudaStream_t s);
+int decode_cluster_capacity_blk_w4(int head_dim, int kv, int cluster_y, int cluster_z);
+cudaError_t launch_decode_blk_w8_d64(const TileParams& tp, dim3 grid, int kv, bool feat,
+                                       int cluster_y, int cluster_z, cudaStream_t s);
+cudaError_t launch_decode_blk_w8_d128(const TileParams& tp, dim3 grid, int kv, bool feat,
+                                       int cluster_y, int cluster_z, cudaStream_t s);
+int decode_cluster_capacity_blk_w8(int head_dim, int kv, int cluster_y, int cluster_z);
+cudaError_t launch_decode_blk_pair_d64(const TileParams& tp, dim3 grid, int kv, bool feat,
+                                       int cluster_y, int cluster_z, cudaStream_t s);
+cudaError_t launch_decode_blk_pair_d128(const TileParams& tp, dim3 grid, int kv, bool feat,
+                                       int cluster_y, int cluster_z, cudaStream_t s);
+int decode_cluster_capacity_blk_pair(int head_dim, int kv, int cluster_y, int cluster_z);
 // resident CTAs per SM of the four-warp decode tile
 int decode_ctas_per_sm(int head_dim, int kv);
 // co-resident clusters of cluster_y x cluster_z decode CTAs (four or, wide, eight consumer

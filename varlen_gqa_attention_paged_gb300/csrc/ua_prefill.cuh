@@ -104,16 +104,4 @@ __device__ __forceinline__ void put_group_scales(GroupScales* dst, int grp, floa
   dst->vi[grp] = fast_rcp(vs);
 }
 
-// The sink (log2 units x) joins a finished row: returns the factor its O takes.
-__device__ __forceinline__ float late_sink(float x, float& m, float& l) {
-  if (x > m) {  // (from -inf: a row that saw no key)
-    const float f = fast_exp2(m - x);
-    m = x;
-    l = l * f + 1.f;
-    return f;
-  }
-  l += fast_exp2(x - m);
-  return 1.f;
-}
-
 }  // namespace ua

@@ -847,25 +847,17 @@ __global__ void __launch_bounds__(160, (TileCfg<D, KV, WM>::kMinBlocks))
 
   const size_t n_part = static_cast<size_t>(p.n_part);
   float* const partial = reinterpret_cast<float*>(pipe + C::kMergeBytes);  // [16][D], m[16], l[16]
-  // block-scaled caches: the sink joins a finished row, whose running max it may pass by any
-  // amount (a partition of far keys under ALiBi)
+  // block-scaled caches: the sink joins a finished row
   auto add_sink = [&]() {
     if (!kBlk || p.sinks == nullptr || z != 0) return;
 #pragma unroll
     for (int rr = 0; rr < 2; ++rr) {
       if (!rv[rr]) continue;
-      const float x = __ldg(p.sinks + rh[rr]) * kLog2e;
-      if (x > m_run[rr]) {  // (from -inf: a row that saw no key)
-        const float f = fast_exp2(m_run[rr] - x);
-        m_run[rr] = x;
-        l_run[rr] = l_run[rr] * f + 1.f;
+      const float f = late_sink(__ldg(p.sinks + rh[rr]) * kLog2e, m_run[rr], l_run[rr]);
 #pragma unroll
-        for (int nd = 0; nd < D / 8; ++nd) {
-          o_acc[nd][2 * rr] *= f;
-          o_acc[nd][2 * rr + 1] *= f;
-        }
-      } else {
-        l_run[rr] += fast_exp2(x - m_run[rr]);
+      for (int nd = 0; nd < D / 8; ++nd) {
+        o_acc[nd][2 * rr] *= f;
+        o_acc[nd][2 * rr + 1] *= f;
       }
     }
   };
