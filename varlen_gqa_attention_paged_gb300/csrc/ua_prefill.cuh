@@ -104,4 +104,79 @@ __device__ __forceinline__ void put_group_scales(GroupScales* dst, int grp, floa
   dst->vi[grp] = fast_rcp(vs);
 }
 
+// One row's part in the scores of a block-scaled cache.
+struct BlkRow {
+  float scale, softcap, slope;
+  const float* qq_row;  // or null
+  bool bias;            // ALiBi or a QQ-bias in this call
+  bool valid;
+  int ctx, pos, lo, ke;
+};
+
+// 32 raw scores (keys key0 .. key0 + 31, two groups at gs[grp], gs[grp + 1]) in place: with
+// FEAT the transformed score (its K scale in it), and the mask on a boundary tile; returns the
+// larger of mx and their maximum in log2 units with the V scales.  Each feature is a loop of
+// its own behind a branch that the whole grid takes alike: a softcap alone costs two special
+// function operations and 1.5 others a score (as one loop with every feature tested at each
+// score it took over 30: 463 against 261 us for three chunks of up to 1501 tokens at head_dim 256).
+template <bool FEAT>
+__device__ __forceinline__ float blk_scores32(const BlkRow& w, const GroupScales* gs, int grp,
+                                              int key0, bool need_mask, float c, uint32_t (&r)[32],
+                                              float mx) {
+  const float2 kf = *reinterpret_cast<const float2*>(gs->kf + grp);
+  const float2 vl = *reinterpret_cast<const float2*>(gs->vl + grp);
+  if constexpr (FEAT) {
+    if (w.softcap > 0.f) {
+      // sc tanh(s / sc) = sc - 2 sc / (1 + 2^(2 log2(e) s / sc))
+      const float k = w.scale * 2.f * kLog2e / w.softcap;
+      const float2 one = make_float2(1.f, 1.f), sc = make_float2(w.softcap, w.softcap);
+      const float2 m2 = make_float2(-2.f * w.softcap, -2.f * w.softcap);
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        const float f = k * (e < 16 ? kf.x : kf.y);
+        float2 u = __fmul2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                              make_float2(f, f));
+        u = __fadd2_rn(make_float2(fast_exp2(u.x), fast_exp2(u.y)), one);
+        u = __ffma2_rn(make_float2(fast_rcp(u.x), fast_rcp(u.y)), m2, sc);
+        r[e] = __float_as_uint(u.x);
+        r[e + 1] = __float_as_uint(u.y);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        r[e] = __float_as_uint(__uint_as_float(r[e]) * (w.scale * (e < 16 ? kf.x : kf.y)));
+    }
+    if (w.bias) {
+      const float base = w.slope * static_cast<float>(key0 - w.ctx);
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        r[e] = __float_as_uint(__uint_as_float(r[e]) + fmaf(w.slope, static_cast<float>(e), base));
+      if (w.qq_row != nullptr) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int j = key0 + e;
+          if (j >= w.ctx && j <= w.pos)
+            r[e] = __float_as_uint(__uint_as_float(r[e]) + __ldg(w.qq_row + (j - w.ctx)));
+        }
+      }
+    }
+  }
+  if (need_mask) {
+    const int a = max(w.lo - key0, 0), b = min(min(w.pos, w.ke - 1) - key0, 31);
+    const uint32_t live = w.valid && a <= b ? (0xffffffffu >> (31 - b)) & (0xffffffffu << a) : 0u;
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      r[e] = (live & (1u << e)) ? r[e] : __float_as_uint(-INFINITY);
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    float mg = -INFINITY;
+#pragma unroll
+    for (int e = 16 * q; e < 16 * q + 16; e += 2)
+      mg = fmax3(mg, __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+    mx = fmaxf(mx, fmaf(mg, FEAT ? c : c * (q ? kf.y : kf.x), q ? vl.y : vl.x));
+  }
+  return mx;
+}
+
 }  // namespace ua

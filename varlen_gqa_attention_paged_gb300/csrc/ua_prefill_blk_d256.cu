@@ -4,15 +4,18 @@
 
 namespace ua {
 
+// With score features two softmax warps share a lane quarter (two chunks of 4096 behind 4096,
+// 24/4 heads, softcap: see the kernel's notes); without them one is as fast, and the halves'
+// exchange of row maxima costs 3 % (1.32 against 1.36 ms for e4m3).
 cudaError_t launch_prefill_blk_d256(const PrefillParams& pp, dim3 grid, int kv, bool feat, int nq,
                                     cudaStream_t s) {
   if (nq != 1) return cudaErrorInvalidValue;
   if (kv == KV_E4M3B)
-    return feat ? launch_prefill_wide_t<256, false, true, true, 1>(pp, grid, s)
-                : launch_prefill_wide_t<256, false, false, true, 1>(pp, grid, s);
+    return feat ? launch_prefill_wide_t<256, false, true, true, 1, 2>(pp, grid, s)
+                : launch_prefill_wide_t<256, false, false, true, 1, 1>(pp, grid, s);
   if (kv == KV_I8B)
-    return feat ? launch_prefill_wide_t<256, false, true, true, 2>(pp, grid, s)
-                : launch_prefill_wide_t<256, false, false, true, 2>(pp, grid, s);
+    return feat ? launch_prefill_wide_t<256, false, true, true, 2, 2>(pp, grid, s)
+                : launch_prefill_wide_t<256, false, false, true, 2, 1>(pp, grid, s);
   return cudaErrorInvalidValue;
 }
 

@@ -650,6 +650,9 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
       return v;
     };
 
+    const BlkRow brow = {p.scale, sc, slope, qq_row, p.alibi != nullptr || p.qq_bias != nullptr,
+                         rv, ctx, pos, lo_r, ke};
+
     for (int n = 0; n < n_tiles; ++n) {
       uint64_t* const sf = DB ? s_full_b(n & 1) : s_full(qt);
       uint64_t* const pf = DB ? p_full_b(n & 1) : p_full(qt);
@@ -672,64 +675,52 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
       constexpr bool kTwo = kCols >= 64;  // two 32-column loads an iteration
       const GroupScales* const gs = scales + (jb + n) % (BLK ? C::kScaleSlots : 1);
       if constexpr (BLK != 0) {
-        static_assert(kTwo, "four groups an iteration");
         if (!pf_wait_warp(&sc_full[(jb + n) % C::kScaleSlots], ((jb + n) / C::kScaleSlots) & 1,
                           abort_flag, p.status)) {
           ok = false;
           break;
         }
-      }
+        constexpr bool k64 = !FEAT && kCols >= 64;
 #pragma unroll 1
-      for (int c0 = half * kCols; c0 < (half + 1) * kCols; c0 += kTwo ? 64 : 32) {
-        uint32_t ra[32], rb[32];
-        tmem_ld32(tS + c0, ra);
-        if constexpr (kTwo) tmem_ld32(tS + c0 + 32, rb);
-        float kf[4] = {1.f, 1.f, 1.f, 1.f};
-        if constexpr (BLK != 0) {
-          const float4 k4 = *reinterpret_cast<const float4*>(gs->kf + c0 / 16);
-          kf[0] = k4.x, kf[1] = k4.y, kf[2] = k4.z, kf[3] = k4.w;
-        }
-        tmem_ld_wait();
-        if constexpr (BLK != 0 && FEAT) {  // the features apply to scores with their K scale
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            ra[e] = __float_as_uint(__uint_as_float(ra[e]) * kf[e / 16]);
-            rb[e] = __float_as_uint(__uint_as_float(rb[e]) * kf[2 + e / 16]);
+        for (int c0 = half * kCols; c0 < (half + 1) * kCols; c0 += k64 ? 64 : 32) {
+          uint32_t ra[32], rb[32];
+          tmem_ld32(tS + c0, ra);
+          if constexpr (k64) tmem_ld32(tS + c0 + 32, rb);
+          tmem_ld_wait();
+          mx0 = blk_scores32<FEAT>(brow, gs, c0 / 16, k0 + c0, need_mask, c, ra, mx0);
+          if (rewrite) tmem_st32(tS + c0, ra);
+          if constexpr (k64) {
+            mx0 = blk_scores32<FEAT>(brow, gs, c0 / 16 + 2, k0 + c0 + 32, need_mask, c, rb, mx0);
+            if (rewrite) tmem_st32(tS + c0 + 32, rb);
           }
         }
-        if (rewrite) {
-          const float ab = FEAT ? slope * static_cast<float>(k0 + c0 - ctx) : 0.f;
-          if (need_mask) {
+      } else {
+#pragma unroll 1
+        for (int c0 = half * kCols; c0 < (half + 1) * kCols; c0 += kTwo ? 64 : 32) {
+          uint32_t ra[32], rb[32];
+          tmem_ld32(tS + c0, ra);
+          if constexpr (kTwo) tmem_ld32(tS + c0 + 32, rb);
+          tmem_ld_wait();
+          if (rewrite) {
+            const float ab = FEAT ? slope * static_cast<float>(k0 + c0 - ctx) : 0.f;
+            if (need_mask) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              ra[e] = __float_as_uint(score(__uint_as_float(ra[e]), k0 + c0 + e, ab, e, std::true_type{}));
-              if constexpr (kTwo)
-                rb[e] = __float_as_uint(score(__uint_as_float(rb[e]), k0 + c0 + 32 + e, ab, 32 + e, std::true_type{}));
+              for (int e = 0; e < 32; ++e) {
+                ra[e] = __float_as_uint(score(__uint_as_float(ra[e]), k0 + c0 + e, ab, e, std::true_type{}));
+                if constexpr (kTwo)
+                  rb[e] = __float_as_uint(score(__uint_as_float(rb[e]), k0 + c0 + 32 + e, ab, 32 + e, std::true_type{}));
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                ra[e] = __float_as_uint(score(__uint_as_float(ra[e]), k0 + c0 + e, ab, e, std::false_type{}));
+                if constexpr (kTwo)
+                  rb[e] = __float_as_uint(score(__uint_as_float(rb[e]), k0 + c0 + 32 + e, ab, 32 + e, std::false_type{}));
+              }
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              ra[e] = __float_as_uint(score(__uint_as_float(ra[e]), k0 + c0 + e, ab, e, std::false_type{}));
-              if constexpr (kTwo)
-                rb[e] = __float_as_uint(score(__uint_as_float(rb[e]), k0 + c0 + 32 + e, ab, 32 + e, std::false_type{}));
-            }
+            tmem_st32(tS + c0, ra);
+            if constexpr (kTwo) tmem_st32(tS + c0 + 32, rb);
           }
-          tmem_st32(tS + c0, ra);
-          if constexpr (kTwo) tmem_st32(tS + c0 + 32, rb);
-        }
-        if constexpr (BLK != 0) {  // the groups' own maxima, scaled; mx0 is in log2 units
-          const float4 l4 = *reinterpret_cast<const float4*>(gs->vl + c0 / 16);
-          const float vl[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t* r16 = (q < 2 ? ra : rb) + 16 * (q & 1);
-            float mg = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 16; e += 2)
-              mg = fmax3(mg, __uint_as_float(r16[e]), __uint_as_float(r16[e + 1]));
-            mx0 = fmaxf(mx0, fmaf(mg, FEAT ? c : c * kf[q], vl[q]));
-          }
-        } else {
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             mx0 = fmax3(mx0, __uint_as_float(ra[e]), __uint_as_float(ra[e + 1]));

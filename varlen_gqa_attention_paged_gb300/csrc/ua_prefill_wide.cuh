@@ -48,7 +48,9 @@ namespace ua {
 // write it into its f16 slot, exactly (every e4m3 value is an f16), so the f16 MMAs and the softmax run
 // unchanged; k_scale joins the score scale and v_scale the output (per-token scales:
 // folded into each key's f16 row instead).
-template <int D, bool F8 = false, int BLK = 0>
+// SW: softmax warps per tensor-memory lane quarter (2: each takes half the key columns of S
+// and half the columns of O, and the row maxima meet in shared memory once a tile).
+template <int D, bool F8 = false, int BLK = 0, int SW = 1>
 struct PrefillWideCfg {
   static constexpr int kBM = 128;                   // MMA rows of the q tile
   static constexpr int kBN = 128;                   // keys per tile
@@ -64,8 +66,12 @@ struct PrefillWideCfg {
   // block-scaled caches: a tile's group scales, written once the first half of its K tile has
   // its slot, which is after Q K^T of tile j - 1 and so after the softmax of tile j - 3
   static constexpr int kScaleSlots = BLK ? 4 : 0;
+  // SW > 1: row maxima of the SW halves as bf16 rounded up, two tiles in flight (at the end
+  // the same bytes hold the row sums of the halves as fp32)
+  static constexpr int kXchBytes = SW > 1 ? 2 * SW * 128 * 2 : 0;
+  static constexpr int kSoft = 4 * SW;              // softmax warps
   static constexpr int kSmemBytes = 1024 + kQBytes + kSlots * kSlotBytes + kStage * kStageBytes +
-                                    kBarBytes + kScaleSlots * 96;
+                                    kBarBytes + kScaleSlots * 96 + kXchBytes;
   static constexpr int kTmemCols = 512;             // S0, S1, O
   // TMA producer warps: a 16-bit half tile is 16 page boxes, an fp8 one 8.  Each producer
   // reuses the staging slot of its own previous item, so the fp8 staging ring holds as many
@@ -75,10 +81,11 @@ struct PrefillWideCfg {
   // eight dequant warps: thread = (key, column half); with four (thread = key) each item's
   // conversion took twice as long on the critical path
   static constexpr int kDeqWarps = F8 ? 8 : 0;
-  static constexpr int kThreads = 32 * (4 + kProducers + 1 + kDeqWarps);
+  static constexpr int kThreads = 32 * (kSoft + kProducers + 1 + kDeqWarps);
   static_assert(D == 256, "two half tiles of 128 columns");
   static_assert(2 * kBN + D <= kTmemCols, "tensor memory budget");
-  static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+  static_assert(kSmemBytes + 32 <= 227 * 1024, "shared memory budget (32: static)");
+  static_assert(SW == 1 || SW == 2, "one or two softmax warps per lane quarter");
   static_assert(!F8 || kStage == kProducers, "one staging slot per producer warp");
 };
 
@@ -89,13 +96,14 @@ __device__ __forceinline__ int wide_item_v(int j, int h, int nt) {
   return j < nt - 1 ? 4 * j + 4 + h : 4 * j + 2 + h;
 }
 
-template <int D, bool BF16, bool FEAT, bool F8 = false, int BLK = 0>
-__global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
+template <int D, bool BF16, bool FEAT, bool F8 = false, int BLK = 0, int SW = 1>
+__global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
     ua_prefill_wide_kernel(const __grid_constant__ PrefillParams pp) {
-  using C = PrefillWideCfg<D, F8, BLK>;
+  using C = PrefillWideCfg<D, F8, BLK, SW>;
+  static_assert(SW == 1 || !BF16, "P's low part is agreed on by four warps");
   constexpr int BN = C::kBN;
   constexpr int NS = C::kSlots;
-  constexpr int kMma = 4 + C::kProducers;
+  constexpr int kMma = C::kSoft + C::kProducers;
   constexpr int kDeq0 = kMma + 1;  // fp8: dequant warps kDeq0 .. kDeq0 + 7
   static_assert(!F8 || !BF16, "fp8 caches run the f16 MMAs");
   const AttnParams& p = pp.p;
@@ -125,6 +133,8 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
   uint64_t* const sc_full = bars + 40;
   GroupScales* const scales =
       reinterpret_cast<GroupScales*>(reinterpret_cast<uint8_t*>(bars) + C::kBarBytes);
+  uint64_t* const xch_bars = bars + 46;  // [4]: SW > 1, the row-max exchange of a lane quarter
+  uint16_t* const xch = reinterpret_cast<uint16_t*>(scales + C::kScaleSlots);  // [2][SW][128]
   __shared__ int s_abort;
   __shared__ int s_last[C::kProducers];  // last item each producer warp issued
 
@@ -142,7 +152,7 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
     mbar_init(lo_bar, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], C::kSoft);
       lo_flag[i] = 0;
     }
     for (int i = 0; i < NS; ++i) {
@@ -157,6 +167,8 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
       }
     }
     for (int i = 0; i < C::kScaleSlots; ++i) mbar_init(&sc_full[i], C::kDeqWarps / 2);
+    if constexpr (SW > 1)
+      for (int i = 0; i < 4; ++i) mbar_init(&xch_bars[i], 32 * SW);
     s_abort = 0;
     mbar_fence_init();
   }
@@ -174,7 +186,7 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
     tmem_alloc(tmem_holder, C::kTmemCols);
     tmem_relinquish();
   }
-  if (warp == 4 && lane == 0) {
+  if (warp == C::kSoft && lane == 0) {
     tma_prefetch_desc(&pp.tmap_q);
     tma_prefetch_desc(&pp.tmap_k);
     tma_prefetch_desc(&pp.tmap_v);
@@ -210,7 +222,7 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
   const int ke = min(ks + part, hi);
   const int nt = (ke - ks + BN - 1) / BN;
 
-  if (warp >= 4 && warp < 4 + C::kProducers) {
+  if (warp >= C::kSoft && warp < C::kSoft + C::kProducers) {
     // ======================================================== TMA producers
     // Producer warp pw issues the items u = pw, pw + NP, ... of the slot sequence; lane
     // i < 16 issues page i / 2 (16 keys), column block i % 2 of the item's half tile
@@ -218,7 +230,7 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
     // slot u % NP).
     constexpr int NP = C::kProducers;
     constexpr int NR = F8 ? C::kStage : NS;  // slots this warp's copies land in
-    const int pw = warp - 4;
+    const int pw = warp - C::kSoft;
     const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_blocks_per_seq;
     const int bs = p.block_size;
     const int oob = p.num_blocks * bs;
@@ -491,7 +503,10 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
     }
   } else {
     // ======================================================== softmax warps (thread = row)
-    const int r = 32 * warp + lane;
+    constexpr int kCols = BN / SW, kOCols = D / SW;
+    const int quad = warp & 3, half = warp >> 2;  // lane quarter, column slice
+    const int r = 32 * quad + lane;
+    uint16_t* const xrow = xch + r;  // + (slot * SW + half) * 128
     // the row's token within the tile and head within the group (rows token * G + head)
     const int tl = r / G;
     const bool rv = r < TQ * G && tl <= t_last - t_first && q0 + t_first + tl < p.total_q;
@@ -521,8 +536,8 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
     const bool sink = p.sinks != nullptr && z == 0 && rv;
     // (block-scaled caches, whose running max carries the V scales, add the sink at the end)
     float m_used = sink && BLK == 0 ? __ldg(p.sinks + h) * kLog2e : -INFINITY;
-    float l = sink && BLK == 0 ? 1.f : 0.f;
-    const uint32_t lane_off = (32u * warp) << 16;
+    float l = sink && BLK == 0 && half == 0 ? 1.f : 0.f;
+    const uint32_t lane_off = (32u * quad) << 16;
     const uint32_t tOr = tO + lane_off;
     bool ok = true;
 
@@ -544,6 +559,9 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
       return v;
     };
 
+    const BlkRow brow = {p.scale, sc, slope, qq_row, p.alibi != nullptr || p.qq_bias != nullptr,
+                         rv, ctx, pos, lo_r, ke};
+
     for (int j = 0; j < nt; ++j) {
       const int bb = j & 1;
       if (!pf_wait_warp(&s_full[bb], (j >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
@@ -562,56 +580,45 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
           ok = false;
           break;
         }
-      }
+        constexpr bool k64 = !FEAT && kCols >= 64;
 #pragma unroll 1
-      for (int c0 = 0; c0 < BN; c0 += 64) {
-        uint32_t ra[32], rb[32];
-        tmem_ld32(tS + c0, ra);
-        tmem_ld32(tS + c0 + 32, rb);
-        float kf[4] = {1.f, 1.f, 1.f, 1.f};
-        if constexpr (BLK != 0) {
-          const float4 k4 = *reinterpret_cast<const float4*>(gs->kf + c0 / 16);
-          kf[0] = k4.x, kf[1] = k4.y, kf[2] = k4.z, kf[3] = k4.w;
-        }
-        tmem_ld_wait();
-        if constexpr (BLK != 0 && FEAT) {  // the features apply to scores with their K scale
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            ra[e] = __float_as_uint(__uint_as_float(ra[e]) * kf[e / 16]);
-            rb[e] = __float_as_uint(__uint_as_float(rb[e]) * kf[2 + e / 16]);
+        for (int c0 = half * kCols; c0 < (half + 1) * kCols; c0 += k64 ? 64 : 32) {
+          uint32_t ra[32], rb[32];
+          tmem_ld32(tS + c0, ra);
+          if constexpr (k64) tmem_ld32(tS + c0 + 32, rb);
+          tmem_ld_wait();
+          mx0 = blk_scores32<FEAT>(brow, gs, c0 / 16, k0 + c0, need_mask, c, ra, mx0);
+          if (rewrite) tmem_st32(tS + c0, ra);
+          if constexpr (k64) {
+            mx0 = blk_scores32<FEAT>(brow, gs, c0 / 16 + 2, k0 + c0 + 32, need_mask, c, rb, mx0);
+            if (rewrite) tmem_st32(tS + c0 + 32, rb);
           }
         }
-        if (rewrite) {
-          const float ab = FEAT ? slope * static_cast<float>(k0 + c0 - ctx) : 0.f;
-          if (need_mask) {
+      } else {
+#pragma unroll 1
+        for (int c0 = half * kCols; c0 < (half + 1) * kCols; c0 += 64) {
+          uint32_t ra[32], rb[32];
+          tmem_ld32(tS + c0, ra);
+          tmem_ld32(tS + c0 + 32, rb);
+          tmem_ld_wait();
+          if (rewrite) {
+            const float ab = FEAT ? slope * static_cast<float>(k0 + c0 - ctx) : 0.f;
+            if (need_mask) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              ra[e] = __float_as_uint(score(__uint_as_float(ra[e]), k0 + c0 + e, ab, e, std::true_type{}));
-              rb[e] = __float_as_uint(score(__uint_as_float(rb[e]), k0 + c0 + 32 + e, ab, 32 + e, std::true_type{}));
+              for (int e = 0; e < 32; ++e) {
+                ra[e] = __float_as_uint(score(__uint_as_float(ra[e]), k0 + c0 + e, ab, e, std::true_type{}));
+                rb[e] = __float_as_uint(score(__uint_as_float(rb[e]), k0 + c0 + 32 + e, ab, 32 + e, std::true_type{}));
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                ra[e] = __float_as_uint(score(__uint_as_float(ra[e]), k0 + c0 + e, ab, e, std::false_type{}));
+                rb[e] = __float_as_uint(score(__uint_as_float(rb[e]), k0 + c0 + 32 + e, ab, 32 + e, std::false_type{}));
+              }
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              ra[e] = __float_as_uint(score(__uint_as_float(ra[e]), k0 + c0 + e, ab, e, std::false_type{}));
-              rb[e] = __float_as_uint(score(__uint_as_float(rb[e]), k0 + c0 + 32 + e, ab, 32 + e, std::false_type{}));
-            }
+            tmem_st32(tS + c0, ra);
+            tmem_st32(tS + c0 + 32, rb);
           }
-          tmem_st32(tS + c0, ra);
-          tmem_st32(tS + c0 + 32, rb);
-        }
-        if constexpr (BLK != 0) {  // the groups' own maxima, scaled; mx0 is in log2 units
-          const float4 l4 = *reinterpret_cast<const float4*>(gs->vl + c0 / 16);
-          const float vl[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t* r16 = (q < 2 ? ra : rb) + 16 * (q & 1);
-            float mg = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 16; e += 2)
-              mg = fmax3(mg, __uint_as_float(r16[e]), __uint_as_float(r16[e + 1]));
-            mx0 = fmaxf(mx0, fmaf(mg, FEAT ? c : c * kf[q], vl[q]));
-          }
-        } else {
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             mx0 = fmax3(mx0, __uint_as_float(ra[e]), __uint_as_float(ra[e + 1]));
@@ -620,7 +627,20 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
         }
       }
       if (rewrite) tmem_st_wait();
-      const float mx = BLK != 0 ? mx0 : fmaxf(mx0, mx1) * c;
+      float mx = BLK != 0 ? mx0 : fmaxf(mx0, mx1) * c;
+      if constexpr (SW > 1) {
+        // the row's other half: every lane arrives once its value is written.  Two slots: a
+        // warp writes tile j + 2's slot only after its S wait, which follows the P.V of tile
+        // j, which waited for every warp's P of tile j, written after the reads.
+        const uint32_t u = __float_as_uint(mx);
+        uint16_t* const slot = xrow + bb * SW * 128;
+        slot[half * 128] = static_cast<uint16_t>(
+            ((u & 0xFFFFu) == 0u || (u >> 31)) ? (u >> 16) : (u >> 16) + 1u);  // round up
+        mbar_arrive(&xch_bars[quad]);
+        if (!pf_wait_warp(&xch_bars[quad], j & 1, abort_flag, p.status)) { ok = false; break; }
+        mx = fmaxf(__uint_as_float(static_cast<uint32_t>(slot[0]) << 16),
+                   __uint_as_float(static_cast<uint32_t>(slot[128]) << 16));
+      }
       float alpha = 1.f;
       const bool grow = mx > m_used + 8.f || (m_used == -INFINITY && mx > -INFINITY);
       if (grow) {
@@ -634,7 +654,7 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
         if (!pf_wait_warp(pv_done, (j - 1) & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
+        for (int c0 = half * kOCols; c0 < (half + 1) * kOCols; c0 += 32) {
           uint32_t ro[32];
           tmem_ld32(tOr + c0, ro);
           tmem_ld_wait();
@@ -663,7 +683,7 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
       float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
       float lacc = 0.f;  // block-scaled: the sum of w / vs
 #pragma unroll 1
-      for (int c0 = 0; c0 < BN; c0 += 32) {
+      for (int c0 = half * kCols; c0 < (half + 1) * kCols; c0 += 32) {
         uint32_t rr[32];
         tmem_ld32(tS + c0, rr);
         tmem_ld_wait();
@@ -729,13 +749,20 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
     if (ok && nt >= 2) ok = pf_wait_warp(pv_done, (nt - 2) & 1, abort_flag, p.status);
     if (ok && nt >= 1) ok = pf_wait_warp(pv_done, (nt - 1) & 1, abort_flag, p.status);
     tc_fence_after();
+    if constexpr (SW > 1) {  // the row sum over both halves (also after an abort)
+      float* const lx = reinterpret_cast<float*>(xch);  // [SW][128]
+      named_bar_sync(3, 32 * C::kSoft);                 // the maxima in these bytes are read
+      lx[half * 128 + r] = l;
+      named_bar_sync(3, 32 * C::kSoft);
+      l = lx[r] + lx[128 + r];
+    }
     if (BLK != 0 && sink) v_mul = late_sink(__ldg(p.sinks + h) * kLog2e, m_used, l);
     if (ok) {
       const size_t orow = static_cast<size_t>(q0 + i_q) * p.hq + h;
       const size_t n_part = static_cast<size_t>(p.n_part);
       const float inv = l > 0.f ? v_mul / l : 0.f;
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
+      for (int c0 = half * kOCols; c0 < (half + 1) * kOCols; c0 += 32) {
         uint32_t rr[32];
         if (nt > 0) {
           tmem_ld32(tOr + c0, rr);
@@ -787,10 +814,10 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK>::kThreads, 1)
   if (warp == kMma) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-template <int D, bool BF16, bool FEAT, bool F8 = false, int BLK = 0>
+template <int D, bool BF16, bool FEAT, bool F8 = false, int BLK = 0, int SW = 1>
 cudaError_t launch_prefill_wide_t(const PrefillParams& pp, dim3 grid, cudaStream_t stream) {
-  using C = PrefillWideCfg<D, F8, BLK>;
-  auto kern = ua_prefill_wide_kernel<D, BF16, FEAT, F8, BLK>;
+  using C = PrefillWideCfg<D, F8, BLK, SW>;
+  auto kern = ua_prefill_wide_kernel<D, BF16, FEAT, F8, BLK, SW>;
   static std::atomic<unsigned long long> configured{0};  // one bit per device
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
