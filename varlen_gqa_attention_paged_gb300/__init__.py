@@ -177,11 +177,13 @@ class PreparedAttention:
                         ("block_table", block_table), ("out", out)):
             if t is None:
                 continue
-            if (tuple(t.shape), t.dtype, t.device) != self._meta[name] or not t.is_contiguous():
-                raise ValueError(f"{name}: shape, dtype, device or layout differs from the "
-                                 "prepared call")
-            args[self._POS[name]] = ctypes.c_void_p(t.data_ptr())
-            self._keep[name] = t
+            if t is not self._keep[name]:
+                if (tuple(t.shape), t.dtype, t.device) != self._meta[name] or \
+                        not t.is_contiguous():
+                    raise ValueError(f"{name}: shape, dtype, device or layout differs from the "
+                                     "prepared call")
+                self._keep[name] = t
+            args[self._POS[name]] = t.data_ptr()
         if stream is not None:
             args[-2] = ctypes.c_void_p(stream.cuda_stream)
         rc = self._lib.ua_unified_attention(*args)
@@ -390,26 +392,33 @@ class PreparedAppend:
         self._static = static
         self._meta = {n: (t.shape, t.stride(), t.dtype, t.device)
                       for n, t in keep.items() if t is not None}
-        self._device = keep["k"].device
+        self._ptr = {n: t.data_ptr() for n, t in keep.items() if t is not None}
+        self._device = keep["k"].device.index
         self._stream = stream
 
     def __call__(self, k=None, v=None, q=None, q_out=None, cu_seqlens_q=None, seq_lens_k=None,
                  block_table=None, positions=None, stream=None):
-        keep, call = self._keep, self._call
+        keep, ptrs = self._keep, self._ptr
         for name, t in (("k", k), ("v", v), ("q", q), ("q_out", q_out),
                         ("cu_seqlens_q", cu_seqlens_q), ("seq_lens_k", seq_lens_k),
                         ("block_table", block_table), ("positions", positions)):
-            if t is None or t is keep[name]:
+            if t is None:
                 continue
-            if (t.shape, t.stride(), t.dtype, t.device) != self._meta.get(name):
-                raise ValueError(f"{name}: shape, strides, dtype or device differs from the "
-                                 "prepared call")
-            setattr(call, name, t.data_ptr())
-            keep[name] = t
-        if stream is None:
-            stream = self._stream
-        with torch.cuda.device(self._device):
-            rc = self._lib.ua_append_kv(self._ref, stream.cuda_stream)
+            if t is not keep[name]:
+                if (t.shape, t.stride(), t.dtype, t.device) != self._meta.get(name):
+                    raise ValueError(f"{name}: shape, strides, dtype or device differs from the "
+                                     "prepared call")
+                keep[name] = t
+            ptr = t.data_ptr()
+            if ptr != ptrs[name]:
+                setattr(self._call, name, ptr)
+                ptrs[name] = ptr
+        handle = (self._stream if stream is None else stream).cuda_stream
+        if torch.cuda.current_device() == self._device:
+            rc = self._lib.ua_append_kv(self._ref, handle)
+        else:
+            with torch.cuda.device(self._device):
+                rc = self._lib.ua_append_kv(self._ref, handle)
         if rc != 0:
             raise UaError(rc, "ua_append_kv")
         return keep["q_out"]

@@ -1,6 +1,7 @@
 // ua_api.cu -- C ABI of libua.so: argument checks, the dispatcher (2D vs split-KV from
 // grid fill and key-walk length), the split workspace, and the kernel launches.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstdint>
 #include <map>
@@ -24,20 +25,20 @@ __device__ unsigned int g_device_status = 0;
 constexpr int kMinPartitionKeys = 256;
 constexpr int kMaxPartitions = 128;
 
+// Per-device look-ups, cached without a lock (a race looks the same value up twice).
+constexpr int kMaxDevices = 64;
+
 int device_sm_count(int* out) {
-  static std::mutex mu;
-  static std::map<int, int> cache;
+  static std::atomic<int> cache[kMaxDevices];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return UA_ERR_CUDA;
-  std::lock_guard<std::mutex> lock(mu);
-  auto it = cache.find(dev);
-  if (it == cache.end()) {
-    int n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return UA_ERR_CUDA;
+  int n = cache[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
       return UA_ERR_CUDA;
-    it = cache.emplace(dev, n).first;
+    cache[dev].store(n, std::memory_order_relaxed);
   }
-  *out = it->second;
+  *out = n;
   return UA_OK;
 }
 
@@ -174,19 +175,18 @@ bool encode_cache_map(CUtensorMap* map, const void* base, int kv_dtype, int num_
 // Device address of the status word on the current device (looked up once per device; the
 // address does not survive cudaDeviceReset of that device).
 int status_word(unsigned int** out) {
-  static std::mutex mu;
-  static std::map<int, unsigned int*> cache;
+  static std::atomic<unsigned int*> cache[kMaxDevices];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return UA_ERR_CUDA;
-  std::lock_guard<std::mutex> lock(mu);
-  auto it = cache.find(dev);
-  if (it == cache.end()) {
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return UA_ERR_CUDA;
+  unsigned int* word = cache[dev].load(std::memory_order_relaxed);
+  if (word == nullptr) {
     void* ptr = nullptr;
     if (cudaGetSymbolAddress(&ptr, g_device_status) != cudaSuccess || ptr == nullptr)
       return UA_ERR_CUDA;
-    it = cache.emplace(dev, static_cast<unsigned int*>(ptr)).first;
+    word = static_cast<unsigned int*>(ptr);
+    cache[dev].store(word, std::memory_order_relaxed);
   }
-  *out = it->second;
+  *out = word;
   return UA_OK;
 }
 

@@ -55,71 +55,165 @@ struct AppendParams {
   int slots, heads_per_cta;   // block kernel: page slots, and kv-heads of a CTA
   int slot_per_seq;           // block kernel: slot x is sequence x (one new token at most)
   uint8_t axis_of[128];
+  uint8_t axis4[32];          // the axis of frequencies 4 i .. 4 i + 3, or 255: not one
 };
 
-// The last b in [0, n) with f(b) <= x (f non-decreasing, f(0) <= x), by one warp: 32 probes a
-// round, so one round of independent loads for up to 32 sequences, two for up to 1024.
+// The sequence owning x and its sizes: the last b in [0, n) with f(cu[b], b) <= x (f
+// non-decreasing, f(cu[0], 0) <= x), by one warp.  32 probes a round narrow it to 32
+// sequences, whose sizes all load in the last round (the only one for up to 32 sequences), so
+// that no load waits for the choice.
+struct SeqOf {
+  int b, q0, end, kv_len;
+};
 template <typename F>
-__device__ __forceinline__ int warp_last_le(int n, long long x, F f) {
+__device__ __forceinline__ SeqOf seq_of(const int32_t* __restrict__ cu,
+                                        const int32_t* __restrict__ kvl, int n, long long x, F f) {
   const int lane = threadIdx.x & 31;
   int lo = 0, len = n;
-  while (len > 1) {
+  while (len > 32) {
     const int step = (len + 31) / 32;
     const int i = lo + lane * step;
-    const unsigned m = __ballot_sync(0xffffffffu, lane * step < len && f(i) <= x);
+    const unsigned m = __ballot_sync(0xffffffffu, lane * step < len && f(__ldg(cu + i), i) <= x);
     const int last = m == 0u ? 0 : 31 - __clz(m);
     lo += last * step;
     len = min(step, len - last * step);
   }
-  return lo;
+  const int i = lo + min(lane, len - 1);
+  const int c0 = __ldg(cu + i), c1 = __ldg(cu + i + 1), kv = __ldg(kvl + i);
+  const unsigned m = __ballot_sync(0xffffffffu, lane < len && f(c0, i) <= x);
+  const int src = m == 0u ? 0 : 31 - __clz(m);
+  return SeqOf{lo + src, __shfl_sync(0xffffffffu, c0, src), __shfl_sync(0xffffffffu, c1, src),
+               __shfl_sync(0xffffffffu, kv, src)};
+}
+
+// A lane's 16 elements as fp32, first and second elements of its pairs apart: with halves
+// apart (and wherever nothing turns) word j of the first chunk is (a[2j], a[2j + 1]) and of the
+// second (b[2j], b[2j + 1]); interleaved, word j of the two chunks' eight is (a[j], b[j]).
+template <bool BF>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (BF) return make_float2(bf16_lo(w), bf16_hi(w));
+  else return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  return BF ? pack_bf16(x, y) : pack_f16(x, y);
 }
 
 template <bool BF>
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ void unpack16(const uint4& lo, const uint4& hi, bool interleaved,
+                                         float (&a)[8], float (&b)[8]) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (interleaved) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (BF) {
-      x[2 * i] = bf16_lo(ww[i]);
-      x[2 * i + 1] = bf16_hi(ww[i]);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ww[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
+    for (int j = 0; j < 8; ++j) {
+      const float2 f = unpack2<BF>(w[j]);
+      a[j] = f.x;
+      b[j] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack2<BF>(w[j]), g = unpack2<BF>(w[4 + j]);
+      a[2 * j] = f.x, a[2 * j + 1] = f.y;
+      b[2 * j] = g.x, b[2 * j + 1] = g.y;
     }
   }
 }
 
 template <bool BF>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  uint32_t w[4];
+__device__ __forceinline__ void pack16(const float (&a)[8], const float (&b)[8], bool interleaved,
+                                       uint4& lo, uint4& hi) {
+  uint32_t w[8];
+  if (interleaved) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = BF ? pack_bf16(x[2 * i], x[2 * i + 1]) : pack_f16(x[2 * i], x[2 * i + 1]);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int j = 0; j < 8; ++j) w[j] = pack2<BF>(a[j], b[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[j] = pack2<BF>(a[2 * j], a[2 * j + 1]);
+      w[4 + j] = pack2<BF>(b[2 * j], b[2 * j + 1]);
+    }
+  }
+  lo = make_uint4(w[0], w[1], w[2], w[3]);
+  hi = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// Eight codes of x * inv: e4m3 (round to nearest even, saturating) or int8 (the same, within
-// +-127).
+// The largest magnitude of 16 packed elements, exactly, without unpacking them.
+template <bool BF>
+__device__ __forceinline__ float amax_packed(const uint4& lo, const uint4& hi) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if constexpr (BF) {
+    __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
+#pragma unroll
+    for (int j = 1; j < 8; ++j)
+      m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[j])));
+    return fmaxf(__low2float(m), __high2float(m));
+  } else {
+    __half2 m = __habs2(*reinterpret_cast<const __half2*>(&w[0]));
+#pragma unroll
+    for (int j = 1; j < 8; ++j)
+      m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&w[j])));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+}
+
+__device__ __forceinline__ float amax16(const float (&a)[8], const float (&b)[8]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmax3(m, fabsf(a[i]), fabsf(b[i]));
+  return m;
+}
+
+// Two products, each rounded.  What is added to them afterwards goes through __fadd_rn and
+// __fsub_rn: a packed sum would be contracted with the packed products into one rounding
+// (seen with add.rn.f32x2 too), and the codes would not be reproducible.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+
+// Four codes of x (already divided by the scale): e4m3 (round to nearest even, saturating) or
+// int8 (the same).  An int8 value plus 1.5 * 2^23 is rounded to a whole number whose low byte
+// is the code; `wide` says that it may lie outside +-127 (a scale at the end of its range).
 template <bool I8>
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv) {
-  uint32_t w[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if constexpr (I8) {
-      uint32_t r = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float y = fminf(fmaxf(__fmul_rn(x[4 * h + i], inv), -127.f), 127.f);
-        r |= (static_cast<uint32_t>(__float2int_rn(y)) & 0xFFu) << (8 * i);
-      }
-      w[h] = r;
-    } else {
-      w[h] = f32x2_to_e4m3x2(__fmul_rn(x[4 * h], inv), __fmul_rn(x[4 * h + 1], inv)) |
-             (f32x2_to_e4m3x2(__fmul_rn(x[4 * h + 2], inv), __fmul_rn(x[4 * h + 3], inv)) << 16);
+__device__ __forceinline__ uint32_t codes4(float2 x, float2 y, bool wide) {
+  if constexpr (I8) {
+    if (wide) {
+      x = make_float2(fminf(fmaxf(x.x, -127.f), 127.f), fminf(fmaxf(x.y, -127.f), 127.f));
+      y = make_float2(fminf(fmaxf(y.x, -127.f), 127.f), fminf(fmaxf(y.y, -127.f), 127.f));
     }
+    constexpr float magic = 12582912.f;
+    const uint32_t u0 = __float_as_uint(__fadd_rn(x.x, magic));
+    const uint32_t u1 = __float_as_uint(__fadd_rn(x.y, magic));
+    const uint32_t u2 = __float_as_uint(__fadd_rn(y.x, magic));
+    const uint32_t u3 = __float_as_uint(__fadd_rn(y.y, magic));
+    return __byte_perm(__byte_perm(u0, u1, 0x0040), __byte_perm(u2, u3, 0x0040), 0x5410);
+  } else {
+    return f32x2_to_e4m3x2(x.x, x.y) | (f32x2_to_e4m3x2(y.x, y.y) << 16);
   }
-  return make_uint2(w[0], w[1]);
+}
+
+// The lane's 16 codes of (a, b) * mul, each product rounded.
+template <bool I8>
+__device__ __forceinline__ void codes16(const float (&a)[8], const float (&b)[8], float mul,
+                                        bool interleaved, bool wide, uint2& lo, uint2& hi) {
+  const float2 m = make_float2(mul, mul);
+  float2 x[4], y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[j] = mul2(make_float2(a[2 * j], a[2 * j + 1]), m);
+    y[j] = mul2(make_float2(b[2 * j], b[2 * j + 1]), m);
+  }
+  uint32_t w[4];
+  if (interleaved) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = codes4<I8>(make_float2(x[j].x, y[j].x), make_float2(x[j].y, y[j].y), wide);
+  } else {
+    w[0] = codes4<I8>(x[0], x[1], wide);
+    w[1] = codes4<I8>(x[2], x[3], wide);
+    w[2] = codes4<I8>(y[0], y[1], wide);
+    w[3] = codes4<I8>(y[2], y[3], wide);
+  }
+  lo = make_uint2(w[0], w[1]);
+  hi = make_uint2(w[2], w[3]);
 }
 
 // Eight codes' own values.
@@ -128,20 +222,12 @@ __device__ __forceinline__ void decode8(const uint2& w, float (&x)[8]) {
   const uint32_t ww[2] = {w.x, w.y};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    if constexpr (I8) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        x[4 * h + i] = static_cast<float>(static_cast<int8_t>(ww[h] >> (8 * i)));
-    } else {
-      uint32_t lo, hi;
-      e4m3x4_to_f16x4(ww[h], lo, hi);
-      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-      x[4 * h] = a.x;
-      x[4 * h + 1] = a.y;
-      x[4 * h + 2] = b.x;
-      x[4 * h + 3] = b.y;
-    }
+    uint32_t lo, hi;
+    codes4_to_f16x4<I8>(ww[h], lo, hi);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    x[4 * h] = a.x, x[4 * h + 1] = a.y;
+    x[4 * h + 2] = b.x, x[4 * h + 3] = b.y;
   }
 }
 
@@ -186,46 +272,45 @@ __device__ __forceinline__ bool load_turn(const AppendParams& p, int t, int pos,
       sn[4 * h] = s4.x, sn[4 * h + 1] = s4.y, sn[4 * h + 2] = s4.z, sn[4 * h + 3] = s4.w;
     }
   } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int f = (e < 4 ? f0 : f1) + (e & 3);
-      const int a = p.axis_of[f];
+    auto row_of = [&](int a) -> const float* {
       int at = pa[0];
 #pragma unroll
       for (int k = 1; k < kMaxAxes; ++k) at = a == k ? pa[k] : at;
-      const float* row = p.cos_sin + static_cast<size_t>(at) * p.rot_dim;
-      cs[e] = __ldg(row + f);
-      sn[e] = __ldg(row + half + f);
+      return p.cos_sin + static_cast<size_t>(at) * p.rot_dim;
+    };
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int f = h ? f1 : f0, a = p.axis4[f / 4];
+      if (a != 255) {
+        const float* row = row_of(a);
+        const float4 c4 = __ldg(reinterpret_cast<const float4*>(row + f));
+        const float4 s4 = __ldg(reinterpret_cast<const float4*>(row + half + f));
+        cs[4 * h] = c4.x, cs[4 * h + 1] = c4.y, cs[4 * h + 2] = c4.z, cs[4 * h + 3] = c4.w;
+        sn[4 * h] = s4.x, sn[4 * h + 1] = s4.y, sn[4 * h + 2] = s4.z, sn[4 * h + 3] = s4.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float* row = row_of(p.axis_of[f + e]);
+          cs[4 * h + e] = __ldg(row + f + e);
+          sn[4 * h + e] = __ldg(row + half + f + e);
+        }
+      }
     }
   }
   return true;
 }
 
-// One pair: every product and sum rounded.
-__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
-  const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-  const float y = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
-  a = x;
-  b = y;
-}
-
-__device__ __forceinline__ void turn(float (&x)[8], float (&y)[8], const float (&cs)[8],
-                                     const float (&sn)[8], bool interleaved) {
-  if (interleaved) {
+// Eight pairs, two at a time: every product and every sum rounded.
+__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (&cs)[8],
+                                     const float (&sn)[8]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) turn_pair(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) turn_pair(y[2 * i], y[2 * i + 1], cs[4 + i], sn[4 + i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) turn_pair(x[i], y[i], cs[i], sn[i]);
+  for (int i = 0; i < 8; i += 2) {
+    const float2 x = make_float2(a[i], a[i + 1]), y = make_float2(b[i], b[i + 1]);
+    const float2 c = make_float2(cs[i], cs[i + 1]), s = make_float2(sn[i], sn[i + 1]);
+    const float2 xc = mul2(x, c), ys = mul2(y, s), yc = mul2(y, c), xs = mul2(x, s);
+    a[i] = __fsub_rn(xc.x, ys.x), a[i + 1] = __fsub_rn(xc.y, ys.y);
+    b[i] = __fadd_rn(yc.x, xs.x), b[i + 1] = __fadd_rn(yc.y, xs.y);
   }
-}
-
-__device__ __forceinline__ float amax8(const float (&x)[8], float m) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-  return m;
 }
 
 // The scale of a group whose largest magnitude is amax: within [2^-40, 2^40], so that neither
@@ -234,133 +319,161 @@ __device__ __forceinline__ float group_scale(float amax, float inv_qmax) {
   return fminf(fmaxf(__fmul_rn(amax, inv_qmax), kScaleMin), kScaleMax);
 }
 
-// The rows (heads) p0 .. p1 - 1 (in passes of 512 / D) of token t: queries, keys and values, or
-// (ONLY_Q) queries alone.  U passes' loads are in flight before the token's sequence and
-// position are known.
-template <int D, bool BF, int KIND, bool ONLY_Q>
-__device__ __forceinline__ void append_rows(const AppendParams& p, int t, int p0, int p1) {
-  constexpr int LPR = D / 16;      // lanes a row
-  constexpr int RPP = 32 / LPR;    // rows a pass
-  constexpr int U = 4;
-  const int lane = threadIdx.x & 31;
-  const int sub = lane / LPR, c = lane % LPR;
-  const int hq = p.q != nullptr ? p.hq : 0;
-  const int nh = ONLY_Q ? hq : hq + 2 * p.hkv;
-  const LaneChunks<D> ch(c, p.rot_dim);
-  bool found = false, live = false, in_cache = false, turned = false;
-  size_t cache_row = 0;
-  int blk = 0, slot = 0;
+// Where a token's keys and values go, and its turn.
+struct TokenAt {
+  size_t cache_row;  // row of kv-head 0 in the cache
+  int blk, slot;
+  bool in_cache, turned;
   float cs[8], sn[8];
-#pragma unroll 1
-  for (int pass = p0; pass < p1; pass += U) {
-    uint4 a[U], b[U];
+};
+
+// U passes (rows h, h + 512 / D, ... of q, k or v: R 0, 1, 2) of one token as read in a and b;
+// n of them are real.
+template <int D, bool BF, int KIND, int R, int U>
+__device__ __forceinline__ void put_rows(const AppendParams& p, const TokenAt& at, int t, int h0,
+                                         int n, int c, const LaneChunks<D>& ch, uint4 (&a)[U],
+                                         uint4 (&b)[U]) {
+  constexpr int LPR = D / 16, RPP = 32 / LPR;
+  const int heads = R == 0 ? p.hq : p.hkv;
+  const bool inter = p.interleaved != 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = (pass + u) * RPP + sub;
-      a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (pass + u < p1 && h < nh) {
-        const uint16_t* src =
-            h < hq ? p.q + t * p.q_stride[0] + h * p.q_stride[1]
-            : h < hq + p.hkv ? p.k + t * p.k_stride[0] + (h - hq) * p.k_stride[1]
-                             : p.v + t * p.v_stride[0] + (h - hq - p.hkv) * p.v_stride[1];
-        a[u] = __ldg(reinterpret_cast<const uint4*>(src) + ch.lo);
-        b[u] = __ldg(reinterpret_cast<const uint4*>(src) + ch.hi);
-      }
+  for (int u = 0; u < U; ++u) {
+    const int h = h0 + u * RPP;
+    const bool valid = u < n && h < heads;
+    float x[8], y[8];
+    bool open = false;  // the row is in x and y
+    if (R != 2 && at.turned) {
+      unpack16<BF>(a[u], b[u], inter, x, y);
+      turn(x, y, at.cs, at.sn);
+      if (R == 0 || KIND == APP_16) pack16<BF>(x, y, inter, a[u], b[u]);
+      open = true;
     }
-    if (!found) {
-      found = true;
-      const int sq = warp_last_le(p.num_seqs, t, [&](int i) -> long long {
-        return __ldg(p.cu_seqlens_q + i);
-      });
-      const int end = __ldg(p.cu_seqlens_q + sq + 1);
-      const int pos = __ldg(p.seq_lens_k + sq) - end + t;
-      live = t < end && pos >= 0;
-      if (live && !ONLY_Q) {
-        const int col = pos / p.block_size;
-        slot = pos % p.block_size;
-        blk = col < p.max_blocks_per_seq
-                  ? __ldg(p.block_table + static_cast<size_t>(sq) * p.max_blocks_per_seq + col)
-                  : -1;
-        in_cache = static_cast<unsigned>(blk) < static_cast<unsigned>(p.num_blocks);
-        if (!in_cache && lane == 0) atomicOr(p.status, DEV_BAD_BLOCK);
-        cache_row = (static_cast<size_t>(in_cache ? blk : 0) * p.block_size + slot) * p.hkv;
+    if (R == 0) {
+      if (valid) {
+        uint4* dst = reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride[0] +
+                                              h * p.q_out_stride[1]);
+        dst[ch.lo] = a[u];
+        dst[ch.hi] = b[u];
       }
-      if (live && p.rot_dim > 0) {
-        live = load_turn(p, t, pos, ch.lo, ch.hi, ch.turned, cs, sn);
-        if (!live && lane == 0) atomicOr(p.status, DEV_BAD_POSITION);
-        turned = ch.turned;
-      }
-      if (!live) return;  // uniform for the warp: one token
+      continue;
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = (pass + u) * RPP + sub;
-      const bool valid = pass + u < p1 && h < nh;
-      float x[8], y[8];
-      const bool is_v = !ONLY_Q && h >= hq + p.hkv;
-      uint4 ra = a[u], rb = b[u];
-      if (!is_v && turned) {
-        unpack8<BF>(ra, x);
-        unpack8<BF>(rb, y);
-        turn(x, y, cs, sn, p.interleaved != 0);
-        if (KIND == APP_16 || h < hq) {
-          ra = pack8<BF>(x);
-          rb = pack8<BF>(y);
-        }
-      } else if (KIND != APP_16) {
-        unpack8<BF>(ra, x);
-        unpack8<BF>(rb, y);
+    const bool put = valid && at.in_cache;
+    void* const cache = R == 2 ? p.v_cache : p.k_cache;
+    if constexpr (KIND == APP_16) {
+      if (put) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(cache) +
+                                              (at.cache_row + h) * D);
+        dst[ch.lo] = a[u];
+        dst[ch.hi] = b[u];
       }
-      if (ONLY_Q || h < hq) {
-        if (valid) {
-          uint4* dst = reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride[0] +
-                                                h * p.q_out_stride[1]);
-          dst[ch.lo] = ra;
-          dst[ch.hi] = rb;
+    } else {
+      float inv;
+      if constexpr (KIND == APP_E4M3) {
+        inv = __frcp_rn(__ldg(p.kv_scale + (R == 2 ? 1 : 0)));
+      } else {  // the row's own scale: the largest magnitude of its lanes
+        float m = R != 2 && open ? amax16(x, y) : amax_packed<BF>(a[u], b[u]);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float sc = group_scale(m, 1.f / 448.f);
+        inv = __frcp_rn(sc);
+        if (put && c == 0) {
+          const long long* st = R == 2 ? p.v_scale_stride : p.k_scale_stride;
+          (R == 2 ? p.v_scale : p.k_scale)[at.blk * st[0] + at.slot * st[1] + h * st[2]] = sc;
         }
       }
-      if constexpr (!ONLY_Q) {
-        const int hk = is_v ? h - hq - p.hkv : h - hq;
-        const bool put = valid && in_cache && h >= hq;
-        void* const cache = is_v ? p.v_cache : p.k_cache;
-        if constexpr (KIND == APP_16) {
-          if (put) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(cache) +
-                                                  (cache_row + hk) * D);
-            dst[ch.lo] = ra;
-            dst[ch.hi] = rb;
-          }
-        } else {
-          float inv = 1.f;
-          if constexpr (KIND == APP_E4M3) {
-            if (put) inv = __frcp_rn(__ldg(p.kv_scale + (is_v ? 1 : 0)));
-          } else {  // the row's own scale: the largest magnitude of its lanes
-            float m = amax8(y, amax8(x, 0.f));
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float sc = group_scale(m, 1.f / 448.f);
-            inv = __frcp_rn(sc);
-            if (put && c == 0) {
-              const long long* st = is_v ? p.v_scale_stride : p.k_scale_stride;
-              (is_v ? p.v_scale : p.k_scale)[blk * st[0] + slot * st[1] + hk * st[2]] = sc;
-            }
-          }
-          if (put) {
-            uint2* dst =
-                reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + (cache_row + hk) * D);
-            dst[ch.lo] = codes8<false>(x, inv);
-            dst[ch.hi] = codes8<false>(y, inv);
-          }
-        }
+      if (!open) unpack16<BF>(a[u], b[u], false, x, y);
+      uint2 lo, hi;
+      codes16<false>(x, y, inv, R != 2 && open && inter, false, lo, hi);
+      if (put) {
+        uint2* dst =
+            reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + (at.cache_row + h) * D);
+        dst[ch.lo] = lo;
+        dst[ch.hi] = hi;
       }
     }
   }
 }
 
+// Passes p0 .. p1 - 1 of token t, by one warp: 512 / D rows a pass, the queries' passes first,
+// then (not ONLY_Q) the keys' and the values'.  U passes load together, and the first loads are
+// on their way before the token's sequence, place and angles are known.
+template <int D, bool BF, int KIND, bool ONLY_Q, int U>
+__device__ __forceinline__ void append_rows(const AppendParams& p, int t, int p0, int p1) {
+  constexpr int LPR = D / 16;      // lanes a row
+  constexpr int RPP = 32 / LPR;    // rows a pass
+  const int lane = threadIdx.x & 31;
+  const int sub = lane / LPR, c = lane % LPR;
+  const int nq = (p.hq + RPP - 1) / RPP, nk = (p.hkv + RPP - 1) / RPP;
+  const LaneChunks<D> ch(c, p.rot_dim);
+  TokenAt at;
+  at.in_cache = at.turned = false;
+  bool found = false;
+#pragma unroll 1
+  for (int pass = p0; pass < p1;) {
+    // the pass's tensor, and how many more passes of it (at most U) come next
+    const int r = ONLY_Q || pass < nq ? 0 : pass < nq + nk ? 1 : 2;
+    const int first = r == 0 ? 0 : r == 1 ? nq : nq + nk;
+    const int n = min(U, min(p1, r == 0 ? nq : first + nk) - pass);
+    const int heads = r == 0 ? p.hq : p.hkv;
+    const int h0 = (pass - first) * RPP + sub;
+    const uint16_t* const src = r == 0   ? p.q + t * p.q_stride[0]
+                                : r == 1 ? p.k + t * p.k_stride[0]
+                                         : p.v + t * p.v_stride[0];
+    const long long hs = r == 0 ? p.q_stride[1] : r == 1 ? p.k_stride[1] : p.v_stride[1];
+    uint4 a[U], b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * RPP;
+      a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (u < n && h < heads) {
+        const uint4* row = reinterpret_cast<const uint4*>(src + h * hs);
+        a[u] = __ldg(row + ch.lo);
+        b[u] = __ldg(row + ch.hi);
+      }
+    }
+    if (!found) {
+      found = true;
+      const SeqOf sq = seq_of(p.cu_seqlens_q, p.seq_lens_k, p.num_seqs, t,
+                              [](int c0, int) -> long long { return c0; });
+      const int pos = sq.kv_len - sq.end + t;
+      if (t >= sq.end || pos < 0) return;  // uniform for the warp: one token
+      if (!ONLY_Q) {
+        const int col = pos / p.block_size;
+        at.slot = pos % p.block_size;
+        at.blk = col < p.max_blocks_per_seq
+                     ? __ldg(p.block_table + static_cast<size_t>(sq.b) * p.max_blocks_per_seq + col)
+                     : -1;
+      }
+      if (p.rot_dim > 0) {
+        if (!load_turn(p, t, pos, ch.lo, ch.hi, ch.turned, at.cs, at.sn)) {
+          if (lane == 0) atomicOr(p.status, DEV_BAD_POSITION);
+          return;
+        }
+        at.turned = ch.turned;
+      }
+      if (!ONLY_Q) {
+        at.in_cache = static_cast<unsigned>(at.blk) < static_cast<unsigned>(p.num_blocks);
+        if (!at.in_cache && lane == 0) atomicOr(p.status, DEV_BAD_BLOCK);
+        at.cache_row = (static_cast<size_t>(at.in_cache ? at.blk : 0) * p.block_size + at.slot) * p.hkv;
+      }
+    }
+    if (r == 0) {
+      put_rows<D, BF, KIND, 0, U>(p, at, t, h0, n, c, ch, a, b);
+    } else if constexpr (!ONLY_Q) {
+      if (r == 1) put_rows<D, BF, KIND, 1, U>(p, at, t, h0, n, c, ch, a, b);
+      else put_rows<D, BF, KIND, 2, U>(p, at, t, h0, n, c, ch, a, b);
+    }
+    pass += n;
+  }
+}
+
 // Caches whose elements depend on their own row only: one warp takes pass_group passes of one
-// token (all of them for many tokens, one for few: the launch fills the device either way).
+// token.  Bound by HBM: two passes' loads a warp (64 bytes a lane) and six CTAs, 24 warps, an
+// SM keep 48 KB in flight (four passes and 16 warps: 67.0 against 64.5 us for 4 prompts of
+// 4096 tokens, 76.7 against 67.4 us for 16384 video tokens into e4m3 with token scales).
+constexpr int kRowsMinBlocks = 6, kRowsPasses = 2;
 template <int D, bool BF, int KIND>
-__global__ void __launch_bounds__(128) ua_append_rows_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(128, kRowsMinBlocks) ua_append_rows_kernel(const __grid_constant__ AppendParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int groups = (p.passes + p.pass_group - 1) / p.pass_group;
@@ -368,7 +481,7 @@ __global__ void __launch_bounds__(128) ua_append_rows_kernel(const __grid_consta
   const long long t = w / groups;
   if (t >= p.total_q) return;
   const int p0 = static_cast<int>(w % groups) * p.pass_group;
-  append_rows<D, BF, KIND, false>(p, static_cast<int>(t), p0, min(p0 + p.pass_group, p.passes));
+  append_rows<D, BF, KIND, false, kRowsPasses>(p, static_cast<int>(t), p0, min(p0 + p.pass_group, p.passes));
 }
 
 // Block-scaled caches.  CTA x < slots * (hkv / heads_per_cta) owns one page that new tokens
@@ -378,9 +491,16 @@ __global__ void __launch_bounds__(128) ua_append_rows_kernel(const __grid_consta
 //   s = the larger of (largest new magnitude) / qmax and, with tokens held, the old scale;
 // new rows are stored as rne(x / s), and rows held before as rne(code * (old / s)) where s
 // grew (else they stay).  Slot layout: sequence b's pages start at floor(cu[b] / bs) + 2 b
-// (n new tokens reach at most floor(n / bs) + 2 pages).
-template <int D, bool BF, bool I8, bool ONE>
-__global__ void __launch_bounds__(512) ua_append_blk_kernel(const __grid_constant__ AppendParams p) {
+// (n new tokens reach at most floor(n / bs) + 2 pages).  ONE: the page's rows fit the CTA's
+// threads once, and a row stays in registers between its two uses; else it is read twice.
+// MINB CTAs an SM: four (64 registers a thread, a few spilled) where the grid fills them, as
+// the latency of a page's chain of loads is what many pages are bound by (36.3 against 40.8
+// us for chunks of up to 1999 tokens, int8); three where it does not (3.7 against 4.3 us for
+// a decode step of 64 sequences).
+constexpr int kBlkThreads = 256;
+template <int D, bool BF, bool I8, bool ONE, int MINB>
+__global__ void __launch_bounds__(kBlkThreads, MINB)
+    ua_append_blk_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LPR = D / 16;
   constexpr float kInvQ = 1.f / (I8 ? 127.f : 448.f);
   __shared__ float red[2][2][16];
@@ -395,86 +515,102 @@ __global__ void __launch_bounds__(512) ua_append_blk_kernel(const __grid_constan
     const long long t = w / groups;
     if (t >= p.total_q) return;
     const int p0 = static_cast<int>(w % groups) * p.pass_group;
-    append_rows<D, BF, APP_16, true>(p, static_cast<int>(t), p0,
-                                     min(p0 + p.pass_group, p.passes));
+    append_rows<D, BF, APP_16, true, kRowsPasses>(p, static_cast<int>(t), p0,
+                                             min(p0 + p.pass_group, p.passes));
     return;
   }
   const int x = static_cast<int>(cta / hgroups);
   const int h0 = static_cast<int>(cta % hgroups) * p.heads_per_cta;
   const int h1 = min(h0 + p.heads_per_cta, p.hkv);
   const int bs = p.block_size;
-  const int b = p.slot_per_seq ? x : warp_last_le(p.num_seqs, x, [&](int i) -> long long {
-    return __ldg(p.cu_seqlens_q + i) / bs + 2LL * i;
-  });
-  const int q0 = __ldg(p.cu_seqlens_q + b);
-  const int q_len = __ldg(p.cu_seqlens_q + b + 1) - q0;
-  const int kv_len = __ldg(p.seq_lens_k + b);
-  const int ctx = kv_len - q_len;
-  const int seg = p.slot_per_seq ? 0 : x - (q0 / bs + 2 * b);
+  SeqOf sq;
+  if (p.slot_per_seq)
+    sq = SeqOf{x, __ldg(p.cu_seqlens_q + x), __ldg(p.cu_seqlens_q + x + 1), __ldg(p.seq_lens_k + x)};
+  else
+    sq = seq_of(p.cu_seqlens_q, p.seq_lens_k, p.num_seqs, x,
+                [bs](int c0, int i) -> long long { return c0 / bs + 2LL * i; });
+  const int q_len = sq.end - sq.q0;
+  const int ctx = sq.kv_len - q_len;
+  const int seg = p.slot_per_seq ? 0 : x - (sq.q0 / bs + 2 * sq.b);
   if (p.slot_per_seq && q_len > 1 && h0 == 0 && threadIdx.x == 0)
     atomicOr(p.status, DEV_BAD_SHAPE);  // q_len above max_seqlen_q
   if (q_len <= 0 || seg < 0) return;
   const int pg = max(ctx, 0) / bs + seg;
-  if (static_cast<long long>(pg) * bs >= kv_len) return;  // idle slot
+  if (static_cast<long long>(pg) * bs >= sq.kv_len) return;  // idle slot
   const int base = pg * bs;
-  const int s0 = max(ctx - base, 0);           // tokens the page held before
-  const int s1 = min(kv_len - base, bs);       // its slots in use now
-  const int blk = pg < p.max_blocks_per_seq
-                      ? __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks_per_seq + pg)
-                      : -1;
-  if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
-    if (threadIdx.x == 0) atomicOr(p.status, DEV_BAD_BLOCK);
-    return;
-  }
+  const int s0 = max(ctx - base, 0);        // tokens the page held before
+  const int s1 = min(sq.kv_len - base, bs);  // its slots in use now
   const int row0 = threadIdx.x / LPR, rows = blockDim.x / LPR;
   const LaneChunks<D> ch(threadIdx.x % LPR, p.rot_dim);
+  const int t0 = sq.q0 + base - ctx;         // token of the page's slot 0
+  uint4 k0, k1, v0, v1;  // a new row's chunks as read; codes held before in .x, .y
+  auto fetch_new = [&](int r, int h) {
+    const long long t = t0 + r;
+    const uint4* ks = reinterpret_cast<const uint4*>(p.k + t * p.k_stride[0] + h * p.k_stride[1]);
+    const uint4* vs = reinterpret_cast<const uint4*>(p.v + t * p.v_stride[0] + h * p.v_stride[1]);
+    k0 = __ldg(ks + ch.lo), k1 = __ldg(ks + ch.hi);
+    v0 = __ldg(vs + ch.lo), v1 = __ldg(vs + ch.hi);
+  };
+  // the first head's new rows start on their way before the page and the angles are known
+  if (ONE && row0 >= s0 && row0 < s1) fetch_new(row0, h0);
+  const int blk = pg < p.max_blocks_per_seq
+                      ? __ldg(p.block_table + static_cast<size_t>(sq.b) * p.max_blocks_per_seq + pg)
+                      : -1;
   float cs[8], sn[8];
   // one of the page's rows: 0 outside the page's slots in use, 1 held before, 2 new
   auto state = [&](int r) -> int {
     if (r >= s1) return 0;
     if (r < s0) return 1;
     if (p.rot_dim == 0) return 2;
-    if (load_turn(p, q0 + base + r - ctx, base + r, ch.lo, ch.hi, ch.turned, cs, sn)) return 2;
+    if (load_turn(p, t0 + r, base + r, ch.lo, ch.hi, ch.turned, cs, sn)) return 2;
     atomicOr(p.status, DEV_BAD_POSITION);
     return 0;
   };
   const int st0 = ONE ? state(row0) : 0;
+  if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
+    if (threadIdx.x == 0) atomicOr(p.status, DEV_BAD_BLOCK);
+    return;
+  }
+  auto cache_row = [&](void* cache, int r, int h) -> uint2* {
+    return reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) +
+                                    ((static_cast<size_t>(blk) * bs + r) * p.hkv + h) * D);
+  };
+  auto fetch_held = [&](int r, int h) {
+    const uint2* kp = cache_row(p.k_cache, r, h);
+    const uint2* vp = cache_row(p.v_cache, r, h);
+    const uint2 a = kp[ch.lo], b = kp[ch.hi], c = vp[ch.lo], d = vp[ch.hi];
+    k0.x = a.x, k0.y = a.y, k1.x = b.x, k1.y = b.y;
+    v0.x = c.x, v0.y = c.y, v1.x = d.x, v1.y = d.y;
+  };
+  const bool inter = p.interleaved != 0;
+  float xs[8], ys[8];
+  auto new_k = [&]() {
+    unpack16<BF>(k0, k1, inter && ch.turned, xs, ys);
+    if (ch.turned) turn(xs, ys, cs, sn);
+  };
+  auto put = [&](uint2* dst, float mul, bool pairs, bool wide) {
+    uint2 lo, hi;
+    codes16<I8>(xs, ys, mul, pairs, wide, lo, hi);
+    dst[ch.lo] = lo;
+    dst[ch.hi] = hi;
+  };
   for (int h = h0; h < h1; ++h) {
-    float kx[8], ky[8], vx[8], vy[8];
-    uint2 ok0, ok1, ov0, ov1;
-    uint8_t *kp = nullptr, *vp = nullptr;
     const float old_k = p.k_scale[blk * p.k_scale_stride[0] + h * p.k_scale_stride[2]];
     const float old_v = p.v_scale[blk * p.v_scale_stride[0] + h * p.v_scale_stride[2]];
-    // a row's data: new elements rotated, or the codes held
-    auto fetch = [&](int r, int st) {
-      const size_t off = ((static_cast<size_t>(blk) * bs + r) * p.hkv + h) * D;
-      kp = static_cast<uint8_t*>(p.k_cache) + off;
-      vp = static_cast<uint8_t*>(p.v_cache) + off;
-      if (st == 2) {
-        const long long t = q0 + base + r - ctx;
-        const uint4* ks = reinterpret_cast<const uint4*>(p.k + t * p.k_stride[0] + h * p.k_stride[1]);
-        const uint4* vs = reinterpret_cast<const uint4*>(p.v + t * p.v_stride[0] + h * p.v_stride[1]);
-        const uint4 k0 = __ldg(ks + ch.lo), k1 = __ldg(ks + ch.hi);
-        const uint4 v0 = __ldg(vs + ch.lo), v1 = __ldg(vs + ch.hi);
-        unpack8<BF>(k0, kx);
-        unpack8<BF>(k1, ky);
-        unpack8<BF>(v0, vx);
-        unpack8<BF>(v1, vy);
-        if (ch.turned) turn(kx, ky, cs, sn, p.interleaved != 0);
-      } else if (st == 1) {
-        ok0 = reinterpret_cast<const uint2*>(kp)[ch.lo];
-        ok1 = reinterpret_cast<const uint2*>(kp)[ch.hi];
-        ov0 = reinterpret_cast<const uint2*>(vp)[ch.lo];
-        ov1 = reinterpret_cast<const uint2*>(vp)[ch.hi];
-      }
-    };
     float mk = 0.f, mv = 0.f;
     for (int r = row0; r < bs; r += rows) {
       const int st = ONE ? st0 : state(r);
-      if (ONE || st == 2) fetch(r, st);
       if (st == 2) {
-        mk = amax8(ky, amax8(kx, mk));
-        mv = amax8(vy, amax8(vx, mv));
+        if (!ONE || h > h0) fetch_new(r, h);
+        if (ch.turned) {
+          new_k();
+          mk = fmaxf(mk, amax16(xs, ys));
+        } else {
+          mk = fmaxf(mk, amax_packed<BF>(k0, k1));
+        }
+        mv = fmaxf(mv, amax_packed<BF>(v0, v1));
+      } else if (ONE && st == 1) {
+        fetch_held(r, h);
       }
       if (ONE) break;
     }
@@ -508,27 +644,24 @@ __global__ void __launch_bounds__(512) ua_append_blk_kernel(const __grid_constan
     const float ik = __frcp_rn(sk), iv = __frcp_rn(sv);
     for (int r = row0; r < bs; r += rows) {
       const int st = ONE ? st0 : state(r);
-      const bool again_k = st == 1 && sk > hk, again_v = st == 1 && sv > hv;
-      if (!ONE && (st == 2 || again_k || again_v)) fetch(r, st);
-      if (st == 2) {
-        reinterpret_cast<uint2*>(kp)[ch.lo] = codes8<I8>(kx, ik);
-        reinterpret_cast<uint2*>(kp)[ch.hi] = codes8<I8>(ky, ik);
-        reinterpret_cast<uint2*>(vp)[ch.lo] = codes8<I8>(vx, iv);
-        reinterpret_cast<uint2*>(vp)[ch.hi] = codes8<I8>(vy, iv);
-      }
-      if (again_k) {
-        const float ratio = __fdiv_rn(hk, sk);
-        decode8<I8>(ok0, kx);
-        decode8<I8>(ok1, ky);
-        reinterpret_cast<uint2*>(kp)[ch.lo] = codes8<I8>(kx, ratio);
-        reinterpret_cast<uint2*>(kp)[ch.hi] = codes8<I8>(ky, ratio);
-      }
-      if (again_v) {
-        const float ratio = __fdiv_rn(hv, sv);
-        decode8<I8>(ov0, vx);
-        decode8<I8>(ov1, vy);
-        reinterpret_cast<uint2*>(vp)[ch.lo] = codes8<I8>(vx, ratio);
-        reinterpret_cast<uint2*>(vp)[ch.hi] = codes8<I8>(vy, ratio);
+      if (st == 2) {  // (the rotation again rather than 16 more registers)
+        if (!ONE) fetch_new(r, h);
+        new_k();
+        put(cache_row(p.k_cache, r, h), ik, inter && ch.turned, sk == kScaleMax);
+        unpack16<BF>(v0, v1, false, xs, ys);
+        put(cache_row(p.v_cache, r, h), iv, false, sv == kScaleMax);
+      } else if (st == 1 && (sk > hk || sv > hv)) {
+        if (!ONE) fetch_held(r, h);
+        if (sk > hk) {
+          decode8<I8>(make_uint2(k0.x, k0.y), xs);
+          decode8<I8>(make_uint2(k1.x, k1.y), ys);
+          put(cache_row(p.k_cache, r, h), __fdiv_rn(hk, sk), false, false);
+        }
+        if (sv > hv) {
+          decode8<I8>(make_uint2(v0.x, v0.y), xs);
+          decode8<I8>(make_uint2(v1.x, v1.y), ys);
+          put(cache_row(p.v_cache, r, h), __fdiv_rn(hv, sv), false, false);
+        }
       }
       if (ONE) break;
     }
