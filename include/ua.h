@@ -157,8 +157,11 @@ typedef struct {
                           key-major decode tile of code 2 with eight consumer warps (128-key
                           stages, one CTA per SM), for decode grids of at most one CTA per SM;
                           64: the decode tile of code 2 with two kv-heads per CTA (fp8 caches
-                          with per-tensor scales, at most 4 rows per kv-head, an even
-                          num_kv_heads): one page box carries both heads' rows */
+                          with per-tensor scales, or caches with per-block ones, at most 4
+                          rows per kv-head, an even num_kv_heads): one page box carries both
+                          heads' rows; 128: the decode tile of code 2 or 64 for caches with
+                          per-block scales, a CTA walking an even share of all sequences'
+                          keys: grid_x ranges, and n_part the most partitions of one row */
   int32_t block_m;     /* (query token x head) rows per q-block */
   int32_t n_part;      /* key-range partitions (1 on the 2D path) */
   int32_t grid_x;      /* q-block slots: num_seqs when slot_per_seq, else
@@ -357,8 +360,9 @@ size_t ua_workspace_bytes(const ua_shape_t* shape, int block_size, int num_q_hea
 /*
  * ua_device_status -- synchronises `stream`, then stores in *status the device
  * check word the kernels of this library raised since the last reset, mapped to
- * UA_OK, UA_ERR_DEVICE_CHECK (a block id outside the cache, or a q_len
- * above max_seqlen_q in a decode-shaped call) or UA_ERR_TIMEOUT (a
+ * UA_OK, UA_ERR_DEVICE_CHECK (a block id outside the cache, a position outside the
+ * rotation table, or a q_len above max_seqlen_q or kv_len above max_seqlen_k in a
+ * decode-shaped call) or UA_ERR_TIMEOUT (a
  * bounded wait expired).  Returns UA_OK or UA_ERR_CUDA / UA_ERR_INVALID_ARG.
  * The word reports what the kernels refuse to read rather than faulting: a bad block id
  * is never dereferenced (its keys count as zero).  Slots of a sequence's last page at or

@@ -95,14 +95,14 @@ def on_gpu(c):
     return {n: None if x is None else x.cuda() for n, x in c["t"].items()}
 
 
-def run(c, d=None, out_dtype=torch.float32, fn=ua.unified_attention, **kw):
+def run(c, d=None, out_dtype=torch.float32, fn=ua.unified_attention, max_k=None, **kw):
     d = d or on_gpu(c)
     rows, hq, dim = d["q"].shape
     out = torch.full((rows, hq, dim), 7.0, dtype=out_dtype, device="cuda")
     args = (d["q"], d["k_cache"], d["v_cache"], d["cu_seqlens_q"], d["seq_lens_k"],
             d["block_table"])
     got = fn(*args, max_seqlen_q=max(q for q, _ in c["seqs"]),
-             max_seqlen_k=max(kv for _, kv in c["seqs"]), scale=c["scale"], out=out,
+             max_seqlen_k=max_k or max(kv for _, kv in c["seqs"]), scale=c["scale"], out=out,
              **{n: d[n] for n in ("k_scale_blk", "v_scale_blk", "sinks", "alibi_slopes",
                                   "qq_bias")}, **c["opt"], **kw)
     if fn is ua.prepare:
@@ -121,13 +121,13 @@ def check(c, out, kv=None):
     assert (out[total:] == 7.0).all()
 
 
-def planned(c, **kw):
+def planned(c, max_k=None, **kw):
     t = c["t"]
     code = ua._DTYPES[t["k_cache"].dtype]
     nb, bs, hkv, d = t["k_cache"].shape
     return ua.plan(num_seqs=len(c["seqs"]), total_q=t["q"].shape[0],
                    max_seqlen_q=max(q for q, _ in c["seqs"]),
-                   max_seqlen_k=max(kv for _, kv in c["seqs"]), block_size=bs,
+                   max_seqlen_k=max_k or max(kv for _, kv in c["seqs"]), block_size=bs,
                    num_q_heads=t["q"].shape[1], num_kv_heads=hkv, head_dim=d,
                    window_left=c["opt"]["window_left"], kv_dtype=code,
                    q_dtype=ua._DTYPES[t["q"].dtype], max_blocks_per_seq=t["block_table"].shape[1],
@@ -257,6 +257,85 @@ def test_prepared_captured_and_twice_the_same(shape, splits, code):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(step.out, once)
+
+
+RAGGED = {
+    # many sequences of very different lengths, idle slots among them; a batch of 200 short
+    # ones (more than a CTA's threads); one long sequence in many ranges; two heads a CTA, one,
+    # and eight rows a kv-head
+    "ragged": dict(seqs=[(1, 1 + 97 * i * i % 2600) for i in range(37)] + [(0, 0), (0, 9), (1, 0)],
+                   hq=32, hkv=8),
+    "many": dict(seqs=[(int(i % 5 != 0), 1 + i % 130) for i in range(200)], hq=8, hkv=2),
+    "long": dict(seqs=[(1, 3), (1, 9000), (1, 64), (1, 65)] + [(1, 5 + i) for i in range(60)],
+                 hq=4, hkv=2),
+    "rows8": dict(seqs=[(2, 2 + 211 * i % 1000) for i in range(25)], hq=12, hkv=3),
+    "rows5": dict(seqs=[(1, 1 + 211 * i % 1000) for i in range(60)], hq=10, hkv=2),
+}
+
+
+@pytest.mark.parametrize("code", [E4M3, I8], ids=["e4m3", "i8"])
+@pytest.mark.parametrize("feat", FEATURES)
+@pytest.mark.parametrize("shape,d", [(n, d) for n in RAGGED for d in (64, 128)] +
+                         [("rows5", 256), ("rows8", 256)])
+def test_an_even_share_of_ragged_batches(shape, feat, d, code):
+    """Decode batches whose bound on kv_len makes the dispatcher cut all keys into equal ranges."""
+    seed = d + len(shape) + len(feat)
+    c = make(**RAGGED[shape], **FEATURES[feat], d=d, code=code, seed=seed, pad_rows=2,
+             q_dtype=BF if seed % 2 else F16, bs=(16, 32, 64)[seed % 3], scale_spread=3.0)
+    c["opt"]["window_left"] = 1500 if c["opt"]["window_left"] >= 0 else -1
+    max_k = 40000 if c["opt"]["window_left"] < 0 else None
+    if max_k or shape == "ragged":
+        assert planned(c, max_k)["kernel"] == 128
+    ua.device_status_reset()
+    d_ = on_gpu(c)
+    out = run(c, d_, max_k=max_k)
+    check(c, out)
+    assert torch.equal(out, run(c, d_, max_k=max_k))
+    assert ua.device_status() == 0
+
+
+def test_an_even_share_captured_on_a_poisoned_workspace():
+    """The scratch needs no clearing, and a replayed call takes the lengths it finds."""
+    c = make(**RAGGED["ragged"], d=128, code=I8, seed=5, sinks=True)
+    d = on_gpu(c)
+    plan = planned(c, 40000)
+    assert plan["kernel"] == 128
+    ws = torch.full((plan["workspace_bytes"],), 0xFF, dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    step = run(c, d, fn=ua.prepare, max_k=40000, workspace=ws, stream=stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        step()
+    graph.replay()
+    torch.cuda.synchronize()
+    check(c, step.out)
+    # other lengths (all within the first ones' blocks) in the captured tensor
+    c["seqs"] = [(q, kv if kv < 2 else 1 + kv // 3) for q, kv in c["seqs"]]
+    c["t"]["seq_lens_k"] = torch.tensor([kv for _, kv in c["seqs"]], dtype=torch.int32)
+    d["seq_lens_k"].copy_(c["t"]["seq_lens_k"])
+    ws.fill_(0x7F)
+    graph.replay()
+    torch.cuda.synchronize()
+    check(c, step.out)
+    with pytest.raises(ua.UaError):
+        run(c, d, max_k=40000, workspace=ws[:1024])
+
+
+def test_an_even_share_flags_lengths_above_the_bound():
+    """A kv_len far above max_seqlen_k: the scratch has no room for its partitions; the row is
+    left, the others are right and the status word says so."""
+    c = make([(1, 300)] * 239 + [(1, 60000)], hq=8, hkv=1, d=64, code=I8, seed=5)
+    d = on_gpu(c)
+    assert planned(c, 2000)["kernel"] == 128
+    ua.device_status_reset()
+    out = run(c, d, max_k=2000)
+    assert ua.device_status() == ua._lib.UA_ERR_DEVICE_CHECK
+    ua.device_status_reset()
+    want = torch.from_numpy(reference(c))
+    ok = torch.tensor([kv == 300 for _, kv in c["seqs"]])
+    got = out.cpu().double()
+    assert float((got[ok] - want[ok]).abs().max()) <= bar(c)
 
 
 def test_a_bad_block_counts_as_zero():

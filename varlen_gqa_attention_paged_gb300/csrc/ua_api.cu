@@ -234,6 +234,14 @@ int kv_kind(const ua_shape_t* sh, int kv_dtype) {
 // shared memory), two tiles per CTA for head_dim <= 128 when that grid still fills the
 // device; the rest (block sizes not a multiple of 16) take the tile kernel with 64-row
 // q-blocks.  A decode grid of at most one CTA per SM takes the eight-warp decode tile.
+size_t round256(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
+// Scratch of `rows` partial rows: max and sum, then the unnormalised output; each piece rounded
+// to 256 bytes.
+size_t scratch_bytes(size_t rows, int d) {
+  return 2 * round256(rows * sizeof(float)) + round256(rows * d * sizeof(float));
+}
+
 bool is_tc(int kernel) { return kernel == ua::KERNEL_TC128 || kernel == ua::KERNEL_TC256; }
 
 void make_plan(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, int window_left,
@@ -245,12 +253,12 @@ void make_plan(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, int
   const long long rows_max = static_cast<long long>(sh->max_seqlen_q) * group;
   const bool tc = allow_tc && rows_max > 16 && group <= 128 && block_size % 16 == 0;
   // decode with at most 8 rows per kv-head: the key-major decode tile (page boxes)
-  const bool dec = allow_dec && !tc && rows_max <= 8 && d <= 128 && block_size % 16 == 0 &&
+  const bool dec = allow_dec && !tc && rows_max <= 8 && (d <= 128 || blk) && block_size % 16 == 0 &&
                    static_cast<long long>(sh->num_blocks) * block_size + 16 <= INT32_MAX;
   // fp8 decode with at most 4 rows per kv-head and per-tensor scales: two kv-heads a CTA
   // (their q-blocks fill the tile's 8 columns; one page box carries both heads' rows)
-  const bool pair = dec && (kv_dtype == UA_DT_F8E4M3 || blk) && rows_max <= 4 && hkv % 2 == 0 &&
-                    sh->k_scale_tok == nullptr;
+  const bool pair = dec && (kv_dtype == UA_DT_F8E4M3 || blk) && d <= 128 && rows_max <= 4 &&
+                    hkv % 2 == 0 && sh->k_scale_tok == nullptr;
   const int gy = pair ? hkv / 2 : hkv;  // CTAs of one slot (grid y)
   const int wm = dec ? ua::KERNEL_DEC8 : rows_max <= 16 ? 1 : 4;
   const int tq = tc ? 128 / group : 0;               // tokens per 128-row tensor-memory tile
@@ -279,15 +287,27 @@ void make_plan(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, int
        : pair ? ua::decode_pair_ctas_per_sm(d)
        : dec  ? ua::decode_ctas_per_sm(d, kv)
               : ua::tile_ctas_per_sm(d, kv, wm));
-  const long long by_walk = std::max<long long>(1, walk / kMinPartitionKeys);
-  const long long fit = std::max<long long>(2, std::min(wave / base, by_walk));
+  // Block-scaled decode: partitions from one 64-key tile on, up to the 16 of a cluster, which
+  // merges them inside the launch (one sequence of 500 keys 12.7 us in one partition, 5.6 us in
+  // eight; of 8191 keys 17.8 us in 32 and the merge kernel, 12.8 us in 16).  Clusters of more
+  // than eight CTAs spread badly over the device unless it is nearly empty (four sequences of
+  // 8191 keys, 16 slots: 26.2 us in 8, 20.5 us in 12, 28.2 us in 16 partitions).
+  const bool small_parts = blk && !tc && wm != 4;
+  const long long min_keys = small_parts ? 64 : kMinPartitionKeys;
+  const long long by_walk =
+      std::max<long long>(1, small_parts ? (walk + min_keys - 1) / min_keys : walk / min_keys);
+  long long fit = std::max<long long>(2, std::min(wave / base, by_walk));
+  if (small_parts) {
+    fit = std::min<long long>(fit, 16);
+    if (fit > 8) fit = std::max<long long>(8, std::min<long long>(fit, num_sms * 4LL / 3 / base));
+  }
   int n_part = 1;
   bool fitted = false;  // n_part chosen here rather than by the caller
   if (backend == UA_BACKEND_SPLIT) {
     n_part = sh->num_splits > 0 ? sh->num_splits : static_cast<int>(fit);
     fitted = sh->num_splits <= 0;
   } else if (backend == UA_BACKEND_AUTO) {
-    if (base < wave && walk >= 2LL * kMinPartitionKeys) {
+    if (base < wave && walk >= 2 * min_keys) {
       n_part = static_cast<int>(fit);
       fitted = true;
     }
@@ -343,6 +363,45 @@ void make_plan(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, int
       wide = slots * (hkv / cy) <= cap;
     }
   }
+  // Block-scaled decode: an even share of all sequences' keys a CTA (STREAM in ua_decode.cuh)
+  // instead of partitions, where those leave much of the device idle.  In 64-key tiles a CTA
+  // walks (1.2 to 1.6 us each): the partitions take their waves' longest walks, the even share
+  // the mean, but a merge kernel and a schedule more, about 5 tiles' time.  Walks that a window
+  // bounds are all alike, so only their own rounding can be gained; others differ, and the
+  // longest is taken by few.  Measured at 32/8 heads, d128, e4m3, up to 8191 keys: 48 sequences
+  // 120 against 86 us, 24: 80 against 50, 8: 27 against 29; 32 windows of 4096: 51 against 56.
+  const long long stream_tiles = (walk + 15) / 64 + 2;  // of one walk, at most
+  const bool alike = window_left >= 0 && window_left < sh->max_seqlen_k;
+  long long ranges = 0;
+  int scy = 1;
+  if (blk && dec && backend == UA_BACKEND_AUTO) {
+    const long long by_parts =
+        (slots * gy * n_part + wave - 1) / wave * ((stream_tiles + n_part - 1) / n_part);
+    while (scy < 8 && gy % (2 * scy) == 0) scy *= 2;
+    long long cap = query_device ? ua::decode_stream_capacity(d, kv, pair, scy) : -1;
+    if (cap < 0) cap = wave * 9 / 10 / scy;
+    const long long r = cap * scy / gy;
+    const long long by_share = std::max(base * stream_tiles / std::max(1LL, r * gy),
+                                        std::min<long long>(ua::kStreamMinTiles, stream_tiles));
+    if (r > 1 && by_parts - by_share > (alike ? 8 : 5)) ranges = r;
+  }
+  if (ranges > 1) {
+    pl->path = UA_PATH_SPLIT;
+    pl->kernel = ua::KERNEL_DEC8S;
+    pl->block_m = bm;
+    pl->n_part = static_cast<int32_t>(
+        std::min(ranges, std::max<long long>(2, stream_tiles / ua::kStreamMinTiles + 2)));
+    pl->grid_x = static_cast<int32_t>(ranges);
+    pl->grid_y = gy;
+    pl->grid_z = 1;
+    pl->num_sms = num_sms;
+    pl->cluster_y = scy;
+    pl->cluster_z = 1;
+    pl->slot_per_seq = 0;
+    const size_t rows = static_cast<size_t>(sh->total_q) * hq;
+    pl->workspace_bytes = scratch_bytes(rows * pl->n_part, d) + round256(rows * sizeof(int));
+    return;
+  }
   pl->path = n_part > 1 ? UA_PATH_SPLIT : UA_PATH_2D;
   pl->kernel = tc     ? (nq == 2 ? ua::KERNEL_TC256 : ua::KERNEL_TC128)
                : pair ? ua::KERNEL_DEC8P
@@ -361,11 +420,7 @@ void make_plan(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, int
   pl->slot_per_seq = per_seq ? 1 : 0;
   pl->workspace_bytes = 0;
   if (n_part > 1 && cz == 1) {
-    const size_t rows = static_cast<size_t>(sh->total_q) * hq * n_part;
-    // m and l, then acc; each piece rounded to 256 bytes
-    const size_t ml = ((rows * sizeof(float) + 255) / 256) * 256;
-    const size_t acc = ((rows * d * sizeof(float) + 255) / 256) * 256;
-    pl->workspace_bytes = 2 * ml + acc;
+    pl->workspace_bytes = scratch_bytes(static_cast<size_t>(sh->total_q) * hq * n_part, d);
   }
 }
 
@@ -528,14 +583,16 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
   // decode tile needs them, else the call is planned again for the tile kernel.
   bool tma = !is_tc(pl.kernel) && block_size % 16 == 0 &&
              static_cast<long long>(sh->num_blocks) * block_size + 16 <= INT32_MAX;
-  const int hbox = pl.kernel == ua::KERNEL_DEC8P ? 2 : 1;  // kv-heads per page box
+  const int hbox = pl.kernel == ua::KERNEL_DEC8P || (pl.kernel == ua::KERNEL_DEC8S && pl.grid_y < hkv)
+                       ? 2
+                       : 1;  // kv-heads per page box
   if (tma)
     tma = encode_cache_map(&tp.tmap_k, k_cache, kv_dtype, sh->num_blocks, block_size, hkv, d,
                            hbox) &&
           encode_cache_map(&tp.tmap_v, v_cache, kv_dtype, sh->num_blocks, block_size, hkv, d,
                            hbox);
   const bool dec_kernel = pl.kernel == ua::KERNEL_DEC8 || pl.kernel == ua::KERNEL_DEC8W ||
-                          pl.kernel == ua::KERNEL_DEC8P;
+                          pl.kernel == ua::KERNEL_DEC8P || pl.kernel == ua::KERNEL_DEC8S;
   if (dec_kernel && !tma) {
     make_plan(sh, block_size, hq, hkv, d, window_left, kv_dtype, backend, num_sms, false, false,
               true, &pl);
@@ -556,10 +613,11 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
       return rc;
     }
     const size_t rows = static_cast<size_t>(sh->total_q) * hq * pl.n_part;
-    const size_t ml = ((rows * sizeof(float) + 255) / 256) * 256;
+    const size_t ml = round256(rows * sizeof(float));
     p.ws_m = static_cast<float*>(ws);
     p.ws_l = reinterpret_cast<float*>(static_cast<char*>(ws) + ml);
     p.ws_acc = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * ml);
+    p.ws_np = reinterpret_cast<int*>(static_cast<char*>(ws) + scratch_bytes(rows, d));
   }
   const dim3 grid(pl.grid_x, pl.grid_y, pl.grid_z);
   cudaEvent_t* ev = static_cast<cudaEvent_t*>(sh->events);
@@ -579,11 +637,23 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
       default: err = ua::launch_prefill_d256(pp, grid, kv, feat, nq, st); break;
     }
   } else if (blk_scales && dec_kernel && tma) {
-    const bool d64 = d == 64;
-    const auto launch =
-        pl.kernel == ua::KERNEL_DEC8P ? (d64 ? ua::launch_decode_blk_pair_d64 : ua::launch_decode_blk_pair_d128)
-        : pl.kernel == ua::KERNEL_DEC8W ? (d64 ? ua::launch_decode_blk_w8_d64 : ua::launch_decode_blk_w8_d128)
-                                        : (d64 ? ua::launch_decode_blk_w4_d64 : ua::launch_decode_blk_w4_d128);
+    decltype(&ua::launch_decode_blk_w4_d64) launch;
+    if (pl.kernel == ua::KERNEL_DEC8S && hbox == 2)
+      launch = d == 64 ? ua::launch_decode_blk_stream_pair_d64 : ua::launch_decode_blk_stream_pair_d128;
+    else if (pl.kernel == ua::KERNEL_DEC8S)
+      launch = d == 64    ? ua::launch_decode_blk_stream_d64
+               : d == 128 ? ua::launch_decode_blk_stream_d128
+                          : ua::launch_decode_blk_stream_d256;
+    else if (pl.kernel == ua::KERNEL_DEC8P)
+      launch = d == 64 ? ua::launch_decode_blk_pair_d64 : ua::launch_decode_blk_pair_d128;
+    else if (pl.kernel == ua::KERNEL_DEC8W)
+      launch = d == 64    ? ua::launch_decode_blk_w8_d64
+               : d == 128 ? ua::launch_decode_blk_w8_d128
+                          : ua::launch_decode_blk_w8_d256;
+    else
+      launch = d == 64    ? ua::launch_decode_blk_w4_d64
+               : d == 128 ? ua::launch_decode_blk_w4_d128
+                          : ua::launch_decode_blk_w4_d256;
     err = launch(tp, grid, kv, feat, pl.cluster_y, pl.cluster_z, st);
   } else if (pl.kernel == ua::KERNEL_DEC8) {
     err = d == 64 ? ua::launch_decode_w4_d64(tp, grid, kv, feat, pl.cluster_y, pl.cluster_z, st)
@@ -608,6 +678,11 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
   if (ev && cudaEventRecord(ev[1], st) != cudaSuccess) return UA_ERR_CUDA;
   if (pl.n_part > 1 && !p.cluster_merge) {
     ua::MergeParams mp{};
+    if (pl.kernel == ua::KERNEL_DEC8S) {
+      mp.np = p.ws_np;
+      mp.end = cu_seqlens_q + sh->num_seqs;
+      mp.hq = hq;
+    }
     mp.ws_m = p.ws_m;
     mp.ws_l = p.ws_l;
     mp.ws_acc = p.ws_acc;

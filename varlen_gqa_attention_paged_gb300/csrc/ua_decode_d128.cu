@@ -14,6 +14,7 @@ cudaError_t launch_decode_w4_d128(const TileParams& tp, dim3 grid, int kv, bool 
 }
 
 int decode_ctas_per_sm(int head_dim, int kv) {
+  if (head_dim == 256) return DecCfg<256, KV_I8B>::kMinBlocks;  // (block scales only)
   return head_dim == 64 ? decode_ctas_per_sm_d<64>(kv) : decode_ctas_per_sm_d<128>(kv);
 }
 
@@ -37,6 +38,21 @@ int decode_cluster_capacity(int head_dim, int kv, bool wide, bool pair, int clus
   else if (wide) n = decode_cluster_capacity_w8(head_dim, kv, cluster_y, cluster_z);
   else n = head_dim == 64 ? decode_cluster_capacity_d<64, 4>(kv, cluster_y, cluster_z)
                           : decode_cluster_capacity_d<128, 4>(kv, cluster_y, cluster_z);
+  cache.emplace(key, n);
+  return n;
+}
+
+int decode_stream_capacity(int head_dim, int kv, bool pair, int cluster_y) {
+  static std::mutex mu;
+  static std::map<std::array<int, 5>, int> cache;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  const std::array<int, 5> key = {dev, head_dim, kv, pair ? 1 : 0, cluster_y};
+  std::lock_guard<std::mutex> lock(mu);
+  auto it = cache.find(key);
+  if (it != cache.end()) return it->second;
+  const int n = (pair ? decode_cluster_capacity_blk_stream_pair
+                      : decode_cluster_capacity_blk_stream)(head_dim, kv, cluster_y, 1);
   cache.emplace(key, n);
   return n;
 }

@@ -54,6 +54,7 @@ struct AttnParams {
   float* ws_m;                  // [total_q, hq, n_part]     (n_part > 1)
   float* ws_l;                  // [total_q, hq, n_part]
   float* ws_acc;                // [total_q, hq, n_part, D]
+  int* ws_np;                   // [total_q, hq]: an even share's partitions of a row
   unsigned int* status;         // device status word
   int num_seqs, total_q, max_seqlen_q, max_blocks_per_seq, num_blocks, block_size;
   int hq, hkv, group;
@@ -88,6 +89,11 @@ struct PrefillParams {
 
 // The LSE-merge of split partitions (one output row per query token x head).
 struct MergeParams {
+  // an even share's partitions of each row (1: nothing to merge; n_part is the row's stride
+  // then) and the end of the last sequence's tokens, or null: n_part for every row
+  const int* np;
+  const int32_t* end;
+  int hq;
   const float* ws_m;
   const float* ws_l;
   const float* ws_acc;
@@ -139,10 +145,14 @@ cudaError_t launch_decode_blk_w4_d64(const TileParams& tp, dim3 grid, int kv, bo
                                        int cluster_y, int cluster_z, cudaStream_t s);
 cudaError_t launch_decode_blk_w4_d128(const TileParams& tp, dim3 grid, int kv, bool feat,
                                        int cluster_y, int cluster_z, cudaStream_t s);
+cudaError_t launch_decode_blk_w4_d256(const TileParams& tp, dim3 grid, int kv, bool feat,
+                                       int cluster_y, int cluster_z, cudaStream_t s);
 int decode_cluster_capacity_blk_w4(int head_dim, int kv, int cluster_y, int cluster_z);
 cudaError_t launch_decode_blk_w8_d64(const TileParams& tp, dim3 grid, int kv, bool feat,
                                        int cluster_y, int cluster_z, cudaStream_t s);
 cudaError_t launch_decode_blk_w8_d128(const TileParams& tp, dim3 grid, int kv, bool feat,
+                                       int cluster_y, int cluster_z, cudaStream_t s);
+cudaError_t launch_decode_blk_w8_d256(const TileParams& tp, dim3 grid, int kv, bool feat,
                                        int cluster_y, int cluster_z, cudaStream_t s);
 int decode_cluster_capacity_blk_w8(int head_dim, int kv, int cluster_y, int cluster_z);
 cudaError_t launch_decode_blk_pair_d64(const TileParams& tp, dim3 grid, int kv, bool feat,
@@ -150,6 +160,23 @@ cudaError_t launch_decode_blk_pair_d64(const TileParams& tp, dim3 grid, int kv, 
 cudaError_t launch_decode_blk_pair_d128(const TileParams& tp, dim3 grid, int kv, bool feat,
                                        int cluster_y, int cluster_z, cudaStream_t s);
 int decode_cluster_capacity_blk_pair(int head_dim, int kv, int cluster_y, int cluster_z);
+cudaError_t launch_decode_blk_stream_d64(const TileParams& tp, dim3 grid, int kv, bool feat,
+                                       int cluster_y, int cluster_z, cudaStream_t s);
+cudaError_t launch_decode_blk_stream_d128(const TileParams& tp, dim3 grid, int kv, bool feat,
+                                       int cluster_y, int cluster_z, cudaStream_t s);
+cudaError_t launch_decode_blk_stream_d256(const TileParams& tp, dim3 grid, int kv, bool feat,
+                                       int cluster_y, int cluster_z, cudaStream_t s);
+int decode_cluster_capacity_blk_stream(int head_dim, int kv, int cluster_y, int cluster_z);
+cudaError_t launch_decode_blk_stream_pair_d64(const TileParams& tp, dim3 grid, int kv, bool feat,
+                                       int cluster_y, int cluster_z, cudaStream_t s);
+cudaError_t launch_decode_blk_stream_pair_d128(const TileParams& tp, dim3 grid, int kv, bool feat,
+                                       int cluster_y, int cluster_z, cudaStream_t s);
+int decode_cluster_capacity_blk_stream_pair(int head_dim, int kv, int cluster_y, int cluster_z);
+// co-resident clusters of cluster_y CTAs of the even-share kernels (-1: unknown; cached)
+int decode_stream_capacity(int head_dim, int kv, bool pair, int cluster_y);
+// the smallest range of an even share, in 64-key tiles (it bounds the partitions of a sequence,
+// and so the scratch)
+constexpr int kStreamMinTiles = 8;
 // resident CTAs per SM of the four-warp decode tile
 int decode_ctas_per_sm(int head_dim, int kv);
 // co-resident clusters of cluster_y x cluster_z decode CTAs (four or, wide, eight consumer
@@ -175,7 +202,7 @@ cudaError_t launch_prefill_blk_d256(const PrefillParams& pp, dim3 grid, int kv, 
 
 // Plan kernel codes.
 enum : int { KERNEL_TILE16 = 1, KERNEL_DEC8 = 2, KERNEL_TILE64 = 4, KERNEL_TC128 = 8, KERNEL_TC256 = 16,
-             KERNEL_DEC8W = 32, KERNEL_DEC8P = 64 };
+             KERNEL_DEC8W = 32, KERNEL_DEC8P = 64, KERNEL_DEC8S = 128 };
 
 // Resident CTAs per SM of the tile kernel variant for (head_dim, kv dtype, wm).
 int tile_ctas_per_sm(int head_dim, int kv, int wm);

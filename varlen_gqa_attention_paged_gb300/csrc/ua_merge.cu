@@ -23,10 +23,15 @@ __global__ void __launch_bounds__(256) ua_merge_kernel(const __grid_constant__ M
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * 8 + warp;
   if (row >= p.rows) return;
-  const int np = p.n_part;
+  int np = p.n_part;
   const float* m = p.ws_m + static_cast<size_t>(row) * np;
   const float* l = p.ws_l + static_cast<size_t>(row) * np;
   const float* a = p.ws_acc + static_cast<size_t>(row) * np * D + lane * kPer;
+  if (p.np != nullptr) {  // an even share: a row's own partitions, none for rows of no token
+    if (row / p.hq >= *p.end) return;
+    np = min(p.np[row], np);
+    if (np <= 1) return;
+  }
 
   // Partitions go 32 at a time, one per lane: max and sum loads are independent, the
   // row max and sum are warp reductions, and every partition's weight reaches the lanes
