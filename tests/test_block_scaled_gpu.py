@@ -259,6 +259,36 @@ def test_prepared_captured_and_twice_the_same(shape, splits, code):
     assert torch.equal(step.out, once)
 
 
+LONG = {
+    # two q tiles a CTA (at head_dim <= 128), ragged sequence ends, a chunk behind a prefix
+    "prompts": dict(seqs=[(1500, 1500), (1000, 1600), (300, 300), (3, 700)], hq=16, hkv=8),
+    "g3": dict(seqs=[(1400, 1400), (900, 1000), (129, 129)], hq=24, hkv=8),
+}
+HARD = {
+    # scores of a few units; scores whose maximum climbs all along a row's walk, with each feature
+    "plain": dict(),
+    "steep": dict(q_gain=6.0),
+    "steep_window": dict(q_gain=6.0, window=300, sinks=True),
+    "steep_capped": dict(q_gain=6.0, softcap=40.0, alibi=True, sinks=True),
+    "biased": dict(qq_bias=True, window=500),
+}
+
+
+@pytest.mark.parametrize("code", [E4M3, I8], ids=["e4m3", "i8"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("feat", HARD)
+@pytest.mark.parametrize("shape", LONG)
+def test_block_scaled_prompts(shape, feat, d, code):
+    seed = d + len(shape) + len(feat)
+    c = make(**LONG[shape], **HARD[feat], d=d, code=code, seed=seed, pad_rows=1,
+             q_dtype=BF if seed % 2 else F16, bs=(16, 48, 64)[seed % 3], scale_spread=3.0)
+    if d <= 128:
+        assert planned(c)["kernel"] == 16
+    ua.device_status_reset()
+    check(c, run(c))
+    assert ua.device_status() == 0
+
+
 RAGGED = {
     # many sequences of very different lengths, idle slots among them; a batch of 200 short
     # ones (more than a CTA's threads); one long sequence in many ranges; two heads a CTA, one,

@@ -113,18 +113,14 @@ struct BlkRow {
   int ctx, pos, lo, ke;
 };
 
-// 32 raw scores (keys key0 .. key0 + 31, two groups at gs[grp], gs[grp + 1]) in place: with
-// FEAT the transformed score (its K scale in it), and the mask on a boundary tile; returns the
-// larger of mx and their maximum in log2 units with the V scales.  Each feature is a loop of
+// 32 raw scores (keys key0 .. key0 + 31, two groups of K scales kf) in place: with FEAT the
+// transformed score (its K scale in it), and the mask on a boundary tile.  Each feature is a loop of
 // its own behind a branch that the whole grid takes alike: a softcap alone costs two special
 // function operations and 1.5 others a score (as one loop with every feature tested at each
 // score it took over 30: 463 against 261 us for three chunks of up to 1501 tokens at head_dim 256).
 template <bool FEAT>
-__device__ __forceinline__ float blk_scores32(const BlkRow& w, const GroupScales* gs, int grp,
-                                              int key0, bool need_mask, float c, uint32_t (&r)[32],
-                                              float mx) {
-  const float2 kf = *reinterpret_cast<const float2*>(gs->kf + grp);
-  const float2 vl = *reinterpret_cast<const float2*>(gs->vl + grp);
+__device__ __forceinline__ void blk_transform32(const BlkRow& w, float2 kf, int key0,
+                                                bool need_mask, uint32_t (&r)[32]) {
   if constexpr (FEAT) {
     if (w.softcap > 0.f) {
       // sc tanh(s / sc) = sc - 2 sc / (1 + 2^(2 log2(e) s / sc))
@@ -168,6 +164,16 @@ __device__ __forceinline__ float blk_scores32(const BlkRow& w, const GroupScales
     for (int e = 0; e < 32; ++e)
       r[e] = (live & (1u << e)) ? r[e] : __float_as_uint(-INFINITY);
   }
+}
+
+// The same, and the larger of mx and their maximum in log2 units with the V scales.
+template <bool FEAT>
+__device__ __forceinline__ float blk_scores32(const BlkRow& w, const GroupScales* gs, int grp,
+                                              int key0, bool need_mask, float c, uint32_t (&r)[32],
+                                              float mx) {
+  const float2 kf = *reinterpret_cast<const float2*>(gs->kf + grp);
+  const float2 vl = *reinterpret_cast<const float2*>(gs->vl + grp);
+  blk_transform32<FEAT>(w, kf, key0, need_mask, r);
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     float mg = -INFINITY;
@@ -177,6 +183,101 @@ __device__ __forceinline__ float blk_scores32(const BlkRow& w, const GroupScales
     mx = fmaxf(mx, fmaf(mg, FEAT ? c : c * (q ? kf.y : kf.x), q ? vl.y : vl.x));
   }
   return mx;
+}
+
+// One key tile's softmax in one pass, by a warp whose threads own whole rows (S at tS, O at tO):
+// P = 2^(x - M) over S as f16 pairs, 32 keys at a time.  M stays the running max of the tiles
+// before until a 32-key group's scores pass it by more than 2^8 (or see the row's first key);
+// then the row's sums, its O and the P of this tile's earlier groups are brought down to the
+// new one.  That is rare past a row's first group, so the pass for the maxima, with its reads
+// of S and (with features or a mask) its writes back, goes: 791 -> 771 us for two chunks of
+// 4096 tokens behind 4096, e4m3, 32/8 heads, d128.  wait_pv: P.V of the tile before is done.
+template <bool FEAT, int D, typename WaitPv>
+__device__ __forceinline__ bool blk_softmax_tile(const BlkRow& w, const GroupScales* gs,
+                                                 uint32_t tS, uint32_t tO, int k0, bool need_mask,
+                                                 float c, bool have_o, float& m_used, float& l,
+                                                 WaitPv wait_pv) {
+  float lacc = 0.f;
+#pragma unroll 1
+  for (int c0 = 0; c0 < 16 * kTileGroups; c0 += 32) {
+    uint32_t r[32];
+    tmem_ld32(tS + c0, r);
+    const float2 kf = *reinterpret_cast<const float2*>(gs->kf + c0 / 16);
+    const float2 vl = *reinterpret_cast<const float2*>(gs->vl + c0 / 16);
+    const float2 vi = *reinterpret_cast<const float2*>(gs->vi + c0 / 16);
+    tmem_ld_wait();
+    blk_transform32<FEAT>(w, kf, k0 + c0, need_mask, r);
+    const float m_use = m_used == -INFINITY ? 0.f : m_used;
+    float y[32];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float f = FEAT ? c : c * (q ? kf.y : kf.x), o = (q ? vl.y : vl.x) - m_use;
+#pragma unroll
+      for (int e = 16 * q; e < 16 * q + 16; e += 2) {
+        const float2 u =
+            __ffma2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                       make_float2(f, f), make_float2(o, o));
+        y[e] = u.x;
+        y[e + 1] = u.y;
+        mx = fmax3(mx, u.x, u.y);
+      }
+    }
+    const bool grow = mx > (m_used == -INFINITY ? -INFINITY : 8.f);
+    if (__any_sync(0xffffffffu, grow)) {
+      const float alpha = !grow ? 1.f : m_used == -INFINITY ? 0.f : fast_exp2(-mx);
+      const float d = grow ? mx : 0.f;
+      if (grow) m_used = m_use + mx;
+      l *= alpha;
+      lacc *= alpha;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) y[e] -= d;
+      if (have_o) {
+        if (!wait_pv()) return false;
+#pragma unroll 1
+        for (int o0 = 0; o0 < D; o0 += 16) {
+          uint32_t t[16];
+          tmem_ld16(tO + o0, t);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) t[e] = __float_as_uint(__uint_as_float(t[e]) * alpha);
+          tmem_st16(tO + o0, t);
+        }
+      }
+      tmem_st_wait();  // the P groups written above
+#pragma unroll 1
+      for (int p0 = 0; p0 < c0; p0 += 32) {
+        uint32_t t[16];
+        tmem_ld16(tS + p0, t);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&t[e]));
+          t[e] = pack_f16(f.x * alpha, f.y * alpha);
+        }
+        tmem_st16(tS + p0, t);
+      }
+    }
+    uint32_t hw[16];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      float2 a0 = make_float2(0.f, 0.f), a1 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int e = 16 * q; e < 16 * q + 16; e += 4) {
+        const float2 u = make_float2(fast_exp2(y[e]), fast_exp2(y[e + 1]));
+        const float2 v = make_float2(fast_exp2(y[e + 2]), fast_exp2(y[e + 3]));
+        a0 = __fadd2_rn(a0, u);
+        a1 = __fadd2_rn(a1, v);
+        hw[e / 2] = pack_f16(u.x, u.y);
+        hw[e / 2 + 1] = pack_f16(v.x, v.y);
+      }
+      lacc = fmaf((a0.x + a0.y) + (a1.x + a1.y), q ? vi.y : vi.x, lacc);
+    }
+    tmem_st16(tS + c0, hw);
+  }
+  l += lacc;
+  tmem_st_wait();
+  return true;
 }
 
 }  // namespace ua

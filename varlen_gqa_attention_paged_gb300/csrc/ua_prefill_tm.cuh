@@ -92,6 +92,11 @@ struct PrefillTmCfg {
   static_assert(kSmemBytes + 16 <= 227 * 1024, "shared memory budget");
   static_assert(BLK == 0 || F8, "block scales go with 8-bit codes");
   static_assert(sizeof(GroupScales) == 96);
+  // the barriers, flags and row-exchange barriers end before the group scales' barriers (byte 384)
+  static constexpr int kBarsEnd =
+      8 * (2 + 2 * kRingK + 2 * kRingV + (F8 ? 5 : 0) + 3 * NQ + 2) + 4 * (2 * NQ + 2) +
+      (SW > 1 ? NQ * 64 : 0);
+  static_assert(BLK == 0 || kBarsEnd <= 48 * 8, "barrier layout");
   static_assert(kRingK >= 2 && kRingV >= 2, "at least double-buffered K and V");
   static_assert(!F8 || D == 64 || D == 128, "fp8 caches: head_dim 64 or 128");
 };
@@ -667,6 +672,20 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
       }
       const int k0 = ks + (jb + n) * BN;
       const bool need_mask = k0 < lomax || k0 + BN - 1 > pmin || k0 + BN > ke;
+
+      if constexpr (BLK != 0 && SW == 1) {
+        const int slot = (jb + n) % C::kScaleSlots;
+        ok = pf_wait_warp(&sc_full[slot], ((jb + n) / C::kScaleSlots) & 1, abort_flag, p.status);
+        static_assert(!DB, "with one S buffer its commit covers the P.V before");
+        if (ok)
+          blk_softmax_tile<FEAT, D>(brow, scales + slot, tS, tO, k0, need_mask, c, n >= 1, m_used,
+                                    l, [] { return true; });
+        if (!ok) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pf);
+        continue;
+      }
 
       // ---- pass 1: row max (two 32-column loads in flight).  Scores that need a transform
       // or a mask get it here, once, and are written back over S for pass 2.

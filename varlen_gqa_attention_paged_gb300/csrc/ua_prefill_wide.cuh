@@ -570,6 +570,24 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
       const int k0 = ks + j * BN;
       const bool need_mask = k0 < lomax || k0 + BN - 1 > pmin || k0 + BN > ke;
 
+      if constexpr (BLK != 0 && SW == 1) {
+        const int slot = j % C::kScaleSlots;
+        ok = pf_wait_warp(&sc_full[slot], (j / C::kScaleSlots) & 1, abort_flag, p.status) &&
+             blk_softmax_tile<FEAT, D>(brow, scales + slot, tS, tOr, k0, need_mask, c, j >= 1,
+                                       m_used, l, [&]() -> bool {
+                                         if (!pf_wait_warp(pv_done, (j - 1) & 1, abort_flag,
+                                                           p.status))
+                                           return false;
+                                         tc_fence_after();
+                                         return true;
+                                       });
+        if (!ok) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[bb]);
+        continue;
+      }
+
       // ---- pass 1: row max; transformed / masked scores written back over S
       const bool rewrite = FEAT || need_mask;
       float mx0 = -INFINITY, mx1 = -INFINITY;
