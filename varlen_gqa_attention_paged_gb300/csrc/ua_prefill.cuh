@@ -186,52 +186,99 @@ __device__ __forceinline__ float blk_scores32(const BlkRow& w, const GroupScales
 }
 
 // One key tile's softmax in one pass, by a warp whose threads own whole rows (S at tS, O at tO):
-// P = 2^(x - M) over S as f16 pairs, 32 keys at a time.  M stays the running max of the tiles
-// before until a 32-key group's scores pass it by more than 2^8 (or see the row's first key);
-// then the row's sums, its O and the P of this tile's earlier groups are brought down to the
-// new one.  That is rare past a row's first group, so the pass for the maxima, with its reads
-// of S and (with features or a mask) its writes back, goes: 791 -> 771 us for two chunks of
-// 4096 tokens behind 4096, e4m3, 32/8 heads, d128.  wait_pv: P.V of the tile before is done.
+// P = 2^(x - M) over S as f16 pairs, 64 keys at a time.  M stays what it was after the tiles
+// before while no 16 keys' weights add up to more than 2^12 (so no maximum is taken, and every
+// weight is a finite f16); where a row's do, or it sees its first keys, its sums, O and the P of
+// this tile's earlier keys are brought down to the maximum of the 64.  That is rare past a
+// row's first keys.  (Two passes, the first for the row maxima: 791 us for two chunks of 4096
+// tokens behind 4096, e4m3, 32/8 heads, d128; one pass with a maximum every 32 keys 771 us, as
+// a thread's chain of load, maximum, vote and exponentials is what the tile waits for; this
+// one 679 us.)  wait_pv: P.V of the tile before is done.
 template <bool FEAT, int D, typename WaitPv>
 __device__ __forceinline__ bool blk_softmax_tile(const BlkRow& w, const GroupScales* gs,
                                                  uint32_t tS, uint32_t tO, int k0, bool need_mask,
                                                  float c, bool have_o, float& m_used, float& l,
                                                  WaitPv wait_pv) {
+  constexpr float kMostSum = 4096.f;
   float lacc = 0.f;
 #pragma unroll 1
-  for (int c0 = 0; c0 < 16 * kTileGroups; c0 += 32) {
-    uint32_t r[32];
-    tmem_ld32(tS + c0, r);
-    const float2 kf = *reinterpret_cast<const float2*>(gs->kf + c0 / 16);
-    const float2 vl = *reinterpret_cast<const float2*>(gs->vl + c0 / 16);
-    const float2 vi = *reinterpret_cast<const float2*>(gs->vi + c0 / 16);
-    tmem_ld_wait();
-    blk_transform32<FEAT>(w, kf, k0 + c0, need_mask, r);
-    const float m_use = m_used == -INFINITY ? 0.f : m_used;
-    float y[32];
-    float mx = -INFINITY;
+  for (int c0 = 0; c0 < 16 * kTileGroups; c0 += 64) {
+    uint32_t r[2][32];
+    float f[4], o[4], sum[4];
+    // the scores' factors and offsets of the four groups, with the present M in them
+    auto factors = [&]() {
+      const float4 kf = *reinterpret_cast<const float4*>(gs->kf + c0 / 16);
+      const float4 vl = *reinterpret_cast<const float4*>(gs->vl + c0 / 16);
+      const float m = m_used == -INFINITY ? 0.f : m_used;
+      f[0] = FEAT ? c : c * kf.x, f[1] = FEAT ? c : c * kf.y;
+      f[2] = FEAT ? c : c * kf.z, f[3] = FEAT ? c : c * kf.w;
+      o[0] = vl.x - m, o[1] = vl.y - m, o[2] = vl.z - m, o[3] = vl.w - m;
+    };
+    auto scores = [&]() {
+      const float4 kf = *reinterpret_cast<const float4*>(gs->kf + c0 / 16);
+      blk_transform32<FEAT>(w, make_float2(kf.x, kf.y), k0 + c0, need_mask, r[0]);
+      blk_transform32<FEAT>(w, make_float2(kf.z, kf.w), k0 + c0 + 32, need_mask, r[1]);
+    };
+    // weights as packed f16 (the first 16 registers of each half), and the groups' sums
+    auto weights = [&]() {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const float f = FEAT ? c : c * (q ? kf.y : kf.x), o = (q ? vl.y : vl.x) - m_use;
+      for (int q = 0; q < 4; ++q) {
+        uint32_t* const x = r[q / 2] + 16 * (q & 1);
+        float2 a0 = make_float2(0.f, 0.f), a1 = make_float2(0.f, 0.f);
+        uint32_t hw[8];
 #pragma unroll
-      for (int e = 16 * q; e < 16 * q + 16; e += 2) {
-        const float2 u =
-            __ffma2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
-                       make_float2(f, f), make_float2(o, o));
-        y[e] = u.x;
-        y[e + 1] = u.y;
-        mx = fmax3(mx, u.x, u.y);
+        for (int e = 0; e < 16; e += 4) {
+          float2 u = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                                make_float2(f[q], f[q]), make_float2(o[q], o[q]));
+          float2 v = __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])),
+                                make_float2(f[q], f[q]), make_float2(o[q], o[q]));
+          u = make_float2(fast_exp2(u.x), fast_exp2(u.y));
+          v = make_float2(fast_exp2(v.x), fast_exp2(v.y));
+          a0 = __fadd2_rn(a0, u);
+          a1 = __fadd2_rn(a1, v);
+          hw[e / 2] = pack_f16(u.x, u.y);
+          hw[e / 2 + 1] = pack_f16(v.x, v.y);
+        }
+        sum[q] = (a0.x + a0.y) + (a1.x + a1.y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[q / 2][8 * (q & 1) + e] = hw[e];
       }
+    };
+    tmem_ld32(tS + c0, r[0]);
+    tmem_ld32(tS + c0 + 32, r[1]);
+    factors();
+    tmem_ld_wait();
+    scores();
+    bool again = m_used == -INFINITY;  // the row has seen no key
+    const bool fresh = __any_sync(0xffffffffu, again);
+    if (!fresh) {
+      weights();
+      again = fmaxf(fmaxf(sum[0], sum[1]), fmaxf(sum[2], sum[3])) > kMostSum;
     }
-    const bool grow = mx > (m_used == -INFINITY ? -INFINITY : 8.f);
-    if (__any_sync(0xffffffffu, grow)) {
+    if (fresh || __any_sync(0xffffffffu, again)) {
+      if (!fresh) {  // the scores once more: S is still there
+        tmem_ld32(tS + c0, r[0]);
+        tmem_ld32(tS + c0 + 32, r[1]);
+        tmem_ld_wait();
+        scores();
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float mg = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 16; e += 2)
+          mg = fmax3(mg, __uint_as_float(r[q / 2][16 * (q & 1) + e]),
+                     __uint_as_float(r[q / 2][16 * (q & 1) + e + 1]));
+        mx = fmaxf(mx, fmaf(mg, f[q], o[q]));
+      }
+      // (mx is relative to M; a row past the bound on its sum lies at least 2^8 above it)
+      const bool grow = mx > (m_used == -INFINITY ? -INFINITY : 8.f);
       const float alpha = !grow ? 1.f : m_used == -INFINITY ? 0.f : fast_exp2(-mx);
-      const float d = grow ? mx : 0.f;
-      if (grow) m_used = m_use + mx;
+      if (grow) m_used = (m_used == -INFINITY ? 0.f : m_used) + mx;
       l *= alpha;
       lacc *= alpha;
-#pragma unroll
-      for (int e = 0; e < 32; ++e) y[e] -= d;
+      factors();
       if (have_o) {
         if (!wait_pv()) return false;
 #pragma unroll 1
@@ -244,7 +291,7 @@ __device__ __forceinline__ bool blk_softmax_tile(const BlkRow& w, const GroupSca
           tmem_st16(tO + o0, t);
         }
       }
-      tmem_st_wait();  // the P groups written above
+      tmem_st_wait();  // the P written above
 #pragma unroll 1
       for (int p0 = 0; p0 < c0; p0 += 32) {
         uint32_t t[16];
@@ -252,28 +299,17 @@ __device__ __forceinline__ bool blk_softmax_tile(const BlkRow& w, const GroupSca
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&t[e]));
-          t[e] = pack_f16(f.x * alpha, f.y * alpha);
+          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&t[e]));
+          t[e] = pack_f16(v.x * alpha, v.y * alpha);
         }
         tmem_st16(tS + p0, t);
       }
+      weights();
     }
-    uint32_t hw[16];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      float2 a0 = make_float2(0.f, 0.f), a1 = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int e = 16 * q; e < 16 * q + 16; e += 4) {
-        const float2 u = make_float2(fast_exp2(y[e]), fast_exp2(y[e + 1]));
-        const float2 v = make_float2(fast_exp2(y[e + 2]), fast_exp2(y[e + 3]));
-        a0 = __fadd2_rn(a0, u);
-        a1 = __fadd2_rn(a1, v);
-        hw[e / 2] = pack_f16(u.x, u.y);
-        hw[e / 2 + 1] = pack_f16(v.x, v.y);
-      }
-      lacc = fmaf((a0.x + a0.y) + (a1.x + a1.y), q ? vi.y : vi.x, lacc);
-    }
-    tmem_st16(tS + c0, hw);
+    const float4 vi = *reinterpret_cast<const float4*>(gs->vi + c0 / 16);
+    lacc = fmaf(sum[0], vi.x, fmaf(sum[1], vi.y, fmaf(sum[2], vi.z, fmaf(sum[3], vi.w, lacc))));
+    tmem_st16(tS + c0, *reinterpret_cast<uint32_t(*)[16]>(r[0]));
+    tmem_st16(tS + c0 + 32, *reinterpret_cast<uint32_t(*)[16]>(r[1]));
   }
   l += lacc;
   tmem_st_wait();

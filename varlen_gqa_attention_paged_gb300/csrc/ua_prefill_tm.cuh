@@ -628,6 +628,7 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
     // (block-scaled caches, whose running max carries the V scales, add the sink at the end)
     float m_used = sink && BLK == 0 ? __ldg(p.sinks + h) * kLog2e : -INFINITY;
     float l = sink && BLK == 0 && half == 0 ? 1.f : 0.f;  // the sink's share, once per row
+    if (BLK != 0 && !rv) m_used = 0.f;  // (no row: never stored, and nothing waits for its first key)
     // one q tile: S buffers at columns 0 and BN, O at 2 BN; two: tile qt's S then O
     constexpr bool DB = NQ == 1;
     const uint32_t lane_off = (32u * quad) << 16;

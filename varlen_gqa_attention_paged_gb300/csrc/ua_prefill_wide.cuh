@@ -537,6 +537,7 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
     // (block-scaled caches, whose running max carries the V scales, add the sink at the end)
     float m_used = sink && BLK == 0 ? __ldg(p.sinks + h) * kLog2e : -INFINITY;
     float l = sink && BLK == 0 && half == 0 ? 1.f : 0.f;
+    if (BLK != 0 && !rv) m_used = 0.f;  // (no row: never stored, and nothing waits for its first key)
     const uint32_t lane_off = (32u * quad) << 16;
     const uint32_t tOr = tO + lane_off;
     bool ok = true;
