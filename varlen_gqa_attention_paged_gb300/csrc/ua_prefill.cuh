@@ -85,12 +85,16 @@ struct GroupScales {
   float kf[kTileGroups], vl[kTileGroups], vi[kTileGroups];
 };
 
-// The scales of key `key`'s block (both 1 past ke, or for a bad block).
-__device__ __forceinline__ float2 key_block_scales(const AttnParams& p, const int32_t* bt, int g,
-                                                   int key, int ke) {
-  if (key >= ke) return make_float2(1.f, 1.f);
+// A dequant thread's key group: its block (-1 past ke) and then its scales (both 1 without a
+// block, or for a bad one).  The block is loaded two tiles ahead and the scales one, so that
+// neither load, each of which needs the one before, is waited for (in one step a tile ahead
+// the warp stood 800 cycles a tile).
+__device__ __forceinline__ int key_block(const AttnParams& p, const int32_t* bt, int key, int ke) {
+  if (key >= ke) return -1;
   const int col = key / p.block_size;
-  const int blk = col < p.max_blocks_per_seq ? __ldg(bt + col) : -1;
+  return col < p.max_blocks_per_seq ? __ldg(bt + col) : -1;
+}
+__device__ __forceinline__ float2 block_scales(const AttnParams& p, int g, int blk) {
   if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks))
     return make_float2(1.f, 1.f);
   return make_float2(__ldg(p.k_scale_blk + blk * p.k_blk_stride[0] + g * p.k_blk_stride[1]),

@@ -487,9 +487,13 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
     // to f16 (0 for keys past the partition's walk)
     const bool tok = BLK == 0 && p.k_scale_tok != nullptr;
     const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_blocks_per_seq;
-    // block scales, loaded a tile ahead (16 threads a group)
+    // block scales of the next tile's group, block of the one after (16 threads a group)
     float2 bsc = make_float2(1.f, 1.f);
-    if constexpr (BLK != 0) bsc = key_block_scales(p, bt, g, ks + (td & ~15), ke);
+    int next_blk = -1;
+    if constexpr (BLK != 0) {
+      bsc = block_scales(p, g, key_block(p, bt, ks + (td & ~15), ke));
+      next_blk = key_block(p, bt, ks + BN + (td & ~15), ke);
+    }
     auto key_scale = [&](int j, int op) -> float {
       const int key = ks + j * BN + td;
       if (key >= ke) return 0.f;
@@ -541,7 +545,8 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
             if ((td & 15) == 0) put_group_scales(scales + j % C::kScaleSlots, td >> 4, bsc);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sc_full[j % C::kScaleSlots]);
-            bsc = key_block_scales(p, bt, g, ks + (j + 1) * BN + (td & ~15), ke);
+            bsc = block_scales(p, g, next_blk);
+            next_blk = key_block(p, bt, ks + (j + 2) * BN + (td & ~15), ke);
           }
         }
         uint8_t* dst = (op ? sV : sK) + (j % R) * C::kTileBytes + td * 128;

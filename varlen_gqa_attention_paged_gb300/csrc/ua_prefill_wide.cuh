@@ -81,6 +81,11 @@ struct PrefillWideCfg {
   // eight dequant warps: thread = (key, column half); with four (thread = key) each item's
   // conversion took twice as long on the critical path
   static constexpr int kDeqWarps = F8 ? 8 : 0;
+  // dequant warps of one item: all eight (thread = a key's column half), or (block scales) four
+  // (thread = key) with the two halves of the warps on alternate items, so that one item's
+  // waits pass under the other's conversion: 1280 -> 1112 us for two chunks of 4096 behind
+  // 4096, 24/4 heads, e4m3
+  static constexpr int kItemWarps = BLK ? kDeqWarps / 2 : kDeqWarps;
   static constexpr int kThreads = 32 * (kSoft + kProducers + 1 + kDeqWarps);
   static_assert(D == 256, "two half tiles of 128 columns");
   static_assert(2 * kBN + D <= kTmemCols, "tensor memory budget");
@@ -156,14 +161,14 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
       lo_flag[i] = 0;
     }
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&full[i], F8 ? C::kDeqWarps : 1);  // f16 slots: written by the copies or
+      mbar_init(&full[i], F8 ? C::kItemWarps : 1);  // f16 slots: written by the copies or
       mbar_init(&empty[i], 1);                      // (fp8) the dequant warps
     }
     if constexpr (F8) {
       mbar_init(q_ready, C::kDeqWarps);
       for (int i = 0; i < C::kStage; ++i) {
         mbar_init(&s8_full[i], 1);
-        mbar_init(&s8_empty[i], C::kDeqWarps);
+        mbar_init(&s8_empty[i], C::kItemWarps);
       }
     }
     for (int i = 0; i < C::kScaleSlots; ++i) mbar_init(&sc_full[i], C::kDeqWarps / 2);
@@ -418,9 +423,13 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
     if (lane == 0) mbar_arrive(q_ready);
     const bool tok = BLK == 0 && p.k_scale_tok != nullptr;
     const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_blocks_per_seq;
-    // block scales, loaded a tile ahead (16 threads a group)
+    // block scales of the next tile's group, block of the one after (16 threads a group)
     float2 bsc = make_float2(1.f, 1.f);
-    if constexpr (BLK != 0) bsc = key_block_scales(p, bt, g, ks + (td & ~15), ke);
+    int next_blk = -1;
+    if constexpr (BLK != 0) {
+      bsc = block_scales(p, g, key_block(p, bt, ks + (td & ~15), ke));
+      next_blk = key_block(p, bt, ks + BN + (td & ~15), ke);
+    }
     // the per-token scale of this thread's key of tile j (0 past the partition's keys)
     auto key_scale = [&](int j, bool is_k) -> float {
       const int key = ks + j * BN + td;
@@ -435,8 +444,11 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
                           g * p.v_scale_stride[2]);
     };
     const int n_items = 4 * nt;
+    constexpr bool kAlt = C::kItemWarps < C::kDeqWarps;
+    constexpr int kChunks = kAlt ? 8 : 4;  // 16-code chunks of a thread, from chunk ch0 on
+    const int ch0 = kAlt ? 0 : 4 * hc;
 #pragma unroll 1
-    for (int u = 0; ok && u < n_items; ++u) {
+    for (int u = kAlt ? hc : 0; ok && u < n_items; u += kAlt ? 2 : 1) {
       bool is_k;
       int j, h;
       if (u < 2) {
@@ -451,12 +463,12 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
       const int st = u % C::kStage;
       if (!pf_wait_warp(&s8_full[st], (u / C::kStage) & 1, abort_flag, p.status)) { ok = false; break; }
       // take the half row of codes into registers and hand the staging slot back at once
-      uint4 raw[4];
+      uint4 raw[kChunks];
       {
         const uint8_t* src = s8 + st * C::kStageBytes + td * 128;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          raw[c] = *reinterpret_cast<const uint4*>(src + (((4 * hc + c) ^ sw) << 4));
+        for (int c = 0; c < kChunks; ++c)
+          raw[c] = *reinterpret_cast<const uint4*>(src + (((ch0 + c) ^ sw) << 4));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s8_empty[st]);
@@ -466,18 +478,19 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
         break;
       }
       if constexpr (BLK != 0) {
-        if (is_k && h == 0 && hc == 0) {  // uniform for the warp
+        if (is_k && h == 0) {  // even items: the first half of the warps
           if ((td & 15) == 0) put_group_scales(scales + j % C::kScaleSlots, td >> 4, bsc);
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_full[j % C::kScaleSlots]);
-          bsc = key_block_scales(p, bt, g, ks + (j + 1) * BN + (td & ~15), ke);
+          bsc = block_scales(p, g, next_blk);
+          next_blk = key_block(p, bt, ks + (j + 2) * BN + (td & ~15), ke);
         }
       }
       uint8_t* dst = sR + sl * C::kSlotBytes + td * 128;
       const bool zero = !is_k && ks + j * BN + td >= kv_len;
 #pragma unroll
-      for (int c4 = 0; c4 < 4; ++c4) {  // 16 codes of the row -> f16 chunks 2c, 2c + 1
-        const int c = 4 * hc + c4;
+      for (int c4 = 0; c4 < kChunks; ++c4) {  // 16 codes of the row -> f16 chunks 2c, 2c + 1
+        const int c = ch0 + c4;
         const uint4 r = zero ? make_uint4(0, 0, 0, 0) : raw[c4];
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
         uint32_t hh[8];
