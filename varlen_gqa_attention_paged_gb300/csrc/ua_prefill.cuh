@@ -85,10 +85,9 @@ struct GroupScales {
   float kf[kTileGroups], vl[kTileGroups], vi[kTileGroups];
 };
 
-// A dequant thread's key group: its block (-1 past ke) and then its scales (both 1 without a
-// block, or for a bad one).  The block is loaded two tiles ahead and the scales one, so that
-// neither load, each of which needs the one before, is waited for (in one step a tile ahead
-// the warp stood 800 cycles a tile).
+// A key group's block (-1 past ke), and a block's scales (both 1 without one, or for a bad id).
+// The block is loaded two tiles ahead and the scales one, so that neither load, each of which
+// needs the one before, is waited for (in one step a tile ahead a warp stood 800 cycles a tile).
 __device__ __forceinline__ int key_block(const AttnParams& p, const int32_t* bt, int key, int ke) {
   if (key >= ke) return -1;
   const int col = key / p.block_size;

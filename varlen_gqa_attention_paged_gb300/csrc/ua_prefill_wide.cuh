@@ -63,8 +63,12 @@ struct PrefillWideCfg {
   static constexpr int kStage = F8 ? 2 : 0;         // fp8: staging slots of codes
   static constexpr int kStageBytes = kBN * 128;     // one staged half tile of codes
   static constexpr int kBarBytes = 512;
-  // block-scaled caches: a tile's group scales, written once the first half of its K tile has
-  // its slot, which is after Q K^T of tile j - 1 and so after the softmax of tile j - 3
+  // block-scaled caches: a tile's group scales, written by a warp of their own once producer 0
+  // sent off the first half of its K tile, whose staging slot was free: item 4 j - 4 was read
+  // out, so item 4 j - 6 (the first half of K tile j - 1) has its f16 slot, Q K^T of tile j - 2
+  // is done, and so is the softmax of tile j - 4.  (The dequant warps took 700 cycles a tile for
+  // them: 1112 us for two chunks of 4096 behind 4096, 24/4 heads, e4m3, against 1104, and with a
+  // softcap 1444 against 1409; producer 0, whose copies then came late, 1183 us.)
   static constexpr int kScaleSlots = BLK ? 4 : 0;
   // SW > 1: row maxima of the SW halves as bf16 rounded up, two tiles in flight (at the end
   // the same bytes hold the row sums of the halves as fp32)
@@ -86,7 +90,7 @@ struct PrefillWideCfg {
   // waits pass under the other's conversion: 1280 -> 1112 us for two chunks of 4096 behind
   // 4096, 24/4 heads, e4m3
   static constexpr int kItemWarps = BLK ? kDeqWarps / 2 : kDeqWarps;
-  static constexpr int kThreads = 32 * (kSoft + kProducers + 1 + kDeqWarps);
+  static constexpr int kThreads = 32 * (kSoft + kProducers + 1 + kDeqWarps + (BLK ? 1 : 0));
   static_assert(D == 256, "two half tiles of 128 columns");
   static_assert(2 * kBN + D <= kTmemCols, "tensor memory budget");
   static_assert(kSmemBytes + 32 <= 227 * 1024, "shared memory budget (32: static)");
@@ -138,7 +142,9 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
   uint64_t* const sc_full = bars + 40;
   GroupScales* const scales =
       reinterpret_cast<GroupScales*>(reinterpret_cast<uint8_t*>(bars) + C::kBarBytes);
-  uint64_t* const xch_bars = bars + 46;  // [4]: SW > 1, the row-max exchange of a lane quarter
+  uint64_t* const sc_go = sc_full + C::kScaleSlots;  // producer 0 reached the tile
+  static_assert(40 + 2 * C::kScaleSlots <= 50);
+  uint64_t* const xch_bars = bars + 50;  // [4]: SW > 1, the row-max exchange of a lane quarter
   uint16_t* const xch = reinterpret_cast<uint16_t*>(scales + C::kScaleSlots);  // [2][SW][128]
   __shared__ int s_abort;
   __shared__ int s_last[C::kProducers];  // last item each producer warp issued
@@ -171,7 +177,10 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
         mbar_init(&s8_empty[i], C::kItemWarps);
       }
     }
-    for (int i = 0; i < C::kScaleSlots; ++i) mbar_init(&sc_full[i], C::kDeqWarps / 2);
+    for (int i = 0; i < C::kScaleSlots; ++i) {
+      mbar_init(&sc_full[i], 1);
+      mbar_init(&sc_go[i], 1);
+    }
     if constexpr (SW > 1)
       for (int i = 0; i < 4; ++i) mbar_init(&xch_bars[i], 32 * SW);
     s_abort = 0;
@@ -304,6 +313,10 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
           tma_load_3d_pf(sR + sl * C::kSlotBytes + cbl * C::kSlotCBBytes + page * 2048,
                          is_k ? &pp.tmap_k : &pp.tmap_v, 64 * (2 * h + cbl), g, row, f);
       }
+      if constexpr (BLK != 0) {
+        // (producer 0 has the first halves)
+        if (pw == 0 && is_k && lane == 0) mbar_arrive(&sc_go[j % C::kScaleSlots]);
+      }
       last = u;
     }
     // Never leave copies in flight into this CTA's shared memory (even after an abort).
@@ -391,6 +404,25 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
     // nothing may still be in flight on the tensor cores when the memory is freed
     umma_commit_warp(fin);
     mbar_wait_bounded(fin, 0, p.status, DEV_TIMEOUT);
+  } else if (BLK != 0 && warp == kDeq0 + C::kDeqWarps) {
+    // ======================================================== block scales (lane = 16-key group)
+    // those of the next tile in registers, the block of the one after on its way
+    const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_blocks_per_seq;
+    auto block_of = [&](int j) -> int {
+      return lane < kTileGroups ? key_block(p, bt, ks + j * BN + 16 * lane, ke) : -1;
+    };
+    float2 bsc = block_scales(p, g, block_of(0));
+    int next_blk = block_of(1);
+#pragma unroll 1
+    for (int j = 0; j < nt; ++j) {
+      const int slot = j % C::kScaleSlots;
+      if (!pf_wait_warp(&sc_go[slot], (j / C::kScaleSlots) & 1, abort_flag, p.status)) break;
+      if (lane < kTileGroups) put_group_scales(scales + slot, lane, bsc);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sc_full[slot]);
+      bsc = block_scales(p, g, next_blk);
+      next_blk = block_of(j + 2);
+    }
   } else if (F8 && warp >= kDeq0) {
     // ======================================================== fp8 dequant warps
     // Thread (key td, column half hc): Q (bf16) to f16 in place once (row td, column blocks
@@ -423,13 +455,6 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
     if (lane == 0) mbar_arrive(q_ready);
     const bool tok = BLK == 0 && p.k_scale_tok != nullptr;
     const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_blocks_per_seq;
-    // block scales of the next tile's group, block of the one after (16 threads a group)
-    float2 bsc = make_float2(1.f, 1.f);
-    int next_blk = -1;
-    if constexpr (BLK != 0) {
-      bsc = block_scales(p, g, key_block(p, bt, ks + (td & ~15), ke));
-      next_blk = key_block(p, bt, ks + BN + (td & ~15), ke);
-    }
     // the per-token scale of this thread's key of tile j (0 past the partition's keys)
     auto key_scale = [&](int j, bool is_k) -> float {
       const int key = ks + j * BN + td;
@@ -476,15 +501,6 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
       if (u >= NS && !pf_wait_warp(&empty[sl], ((u / NS) - 1) & 1, abort_flag, p.status)) {
         ok = false;
         break;
-      }
-      if constexpr (BLK != 0) {
-        if (is_k && h == 0) {  // even items: the first half of the warps
-          if ((td & 15) == 0) put_group_scales(scales + j % C::kScaleSlots, td >> 4, bsc);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sc_full[j % C::kScaleSlots]);
-          bsc = block_scales(p, g, next_blk);
-          next_blk = key_block(p, bt, ks + (j + 2) * BN + (td & ~15), ke);
-        }
       }
       uint8_t* dst = sR + sl * C::kSlotBytes + td * 128;
       const bool zero = !is_k && ks + j * BN + td >= kv_len;
