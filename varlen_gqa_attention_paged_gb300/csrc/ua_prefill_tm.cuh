@@ -90,7 +90,7 @@ struct PrefillTmCfg {
   static_assert(NQ * kTmemStride <= kTmemCols, "tensor memory budget");
   // (16 bytes of static shared memory beside it)
   static_assert(kSmemBytes + 16 <= 227 * 1024, "shared memory budget");
-  static_assert(BLK == 0 || F8, "block scales go with 8-bit codes");
+  static_assert(BLK == 0 || (F8 && SW == 1), "block scales go with 8-bit codes, whole rows a thread");
   static_assert(sizeof(GroupScales) == 96);
   // the barriers, flags and row-exchange barriers end before the group scales' barriers (byte 384)
   static constexpr int kBarsEnd =
@@ -679,13 +679,18 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
       const int k0 = ks + (jb + n) * BN;
       const bool need_mask = k0 < lomax || k0 + BN - 1 > pmin || k0 + BN > ke;
 
-      if constexpr (BLK != 0 && SW == 1) {
+      if constexpr (BLK != 0) {
         const int slot = (jb + n) % C::kScaleSlots;
         ok = pf_wait_warp(&sc_full[slot], ((jb + n) / C::kScaleSlots) & 1, abort_flag, p.status);
-        static_assert(!DB, "with one S buffer its commit covers the P.V before");
-        if (ok)
-          blk_softmax_tile<FEAT, D>(brow, scales + slot, tS, tO, k0, need_mask, c, n >= 1, m_used,
-                                    l, [] { return true; });
+        // with one S buffer its commit covers the P.V before; with two it covers P.V n - 2
+        ok = ok && blk_softmax_tile<FEAT, D>(
+                       brow, scales + slot, tS, tO, k0, need_mask, c, n >= 1, m_used, l,
+                       [&]() -> bool {
+                         if (DB && !pf_wait_warp(pv_done(0), (n - 1) & 1, abort_flag, p.status))
+                           return false;
+                         if (DB) tc_fence_after();
+                         return true;
+                       });
         if (!ok) break;
         tc_fence_before();
         __syncwarp();
@@ -698,65 +703,40 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
       const bool rewrite = FEAT || need_mask;
       float mx0 = -INFINITY, mx1 = -INFINITY;
       constexpr bool kTwo = kCols >= 64;  // two 32-column loads an iteration
-      const GroupScales* const gs = scales + (jb + n) % (BLK ? C::kScaleSlots : 1);
-      if constexpr (BLK != 0) {
-        if (!pf_wait_warp(&sc_full[(jb + n) % C::kScaleSlots], ((jb + n) / C::kScaleSlots) & 1,
-                          abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
-        constexpr bool k64 = !FEAT && kCols >= 64;
 #pragma unroll 1
-        for (int c0 = half * kCols; c0 < (half + 1) * kCols; c0 += k64 ? 64 : 32) {
-          uint32_t ra[32], rb[32];
-          tmem_ld32(tS + c0, ra);
-          if constexpr (k64) tmem_ld32(tS + c0 + 32, rb);
-          tmem_ld_wait();
-          mx0 = blk_scores32<FEAT>(brow, gs, c0 / 16, k0 + c0, need_mask, c, ra, mx0);
-          if (rewrite) tmem_st32(tS + c0, ra);
-          if constexpr (k64) {
-            mx0 = blk_scores32<FEAT>(brow, gs, c0 / 16 + 2, k0 + c0 + 32, need_mask, c, rb, mx0);
-            if (rewrite) tmem_st32(tS + c0 + 32, rb);
-          }
-        }
-      } else {
-#pragma unroll 1
-        for (int c0 = half * kCols; c0 < (half + 1) * kCols; c0 += kTwo ? 64 : 32) {
-          uint32_t ra[32], rb[32];
-          tmem_ld32(tS + c0, ra);
-          if constexpr (kTwo) tmem_ld32(tS + c0 + 32, rb);
-          tmem_ld_wait();
-          if (rewrite) {
-            const float ab = FEAT ? slope * static_cast<float>(k0 + c0 - ctx) : 0.f;
-            if (need_mask) {
+      for (int c0 = half * kCols; c0 < (half + 1) * kCols; c0 += kTwo ? 64 : 32) {
+        uint32_t ra[32], rb[32];
+        tmem_ld32(tS + c0, ra);
+        if constexpr (kTwo) tmem_ld32(tS + c0 + 32, rb);
+        tmem_ld_wait();
+        if (rewrite) {
+          const float ab = FEAT ? slope * static_cast<float>(k0 + c0 - ctx) : 0.f;
+          if (need_mask) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                ra[e] = __float_as_uint(score(__uint_as_float(ra[e]), k0 + c0 + e, ab, e, std::true_type{}));
-                if constexpr (kTwo)
-                  rb[e] = __float_as_uint(score(__uint_as_float(rb[e]), k0 + c0 + 32 + e, ab, 32 + e, std::true_type{}));
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                ra[e] = __float_as_uint(score(__uint_as_float(ra[e]), k0 + c0 + e, ab, e, std::false_type{}));
-                if constexpr (kTwo)
-                  rb[e] = __float_as_uint(score(__uint_as_float(rb[e]), k0 + c0 + 32 + e, ab, 32 + e, std::false_type{}));
-              }
+            for (int e = 0; e < 32; ++e) {
+              ra[e] = __float_as_uint(score(__uint_as_float(ra[e]), k0 + c0 + e, ab, e, std::true_type{}));
+              if constexpr (kTwo)
+                rb[e] = __float_as_uint(score(__uint_as_float(rb[e]), k0 + c0 + 32 + e, ab, 32 + e, std::true_type{}));
             }
-            tmem_st32(tS + c0, ra);
-            if constexpr (kTwo) tmem_st32(tS + c0 + 32, rb);
-          }
+          } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            mx0 = fmax3(mx0, __uint_as_float(ra[e]), __uint_as_float(ra[e + 1]));
-            if constexpr (kTwo)
-              mx1 = fmax3(mx1, __uint_as_float(rb[e]), __uint_as_float(rb[e + 1]));
+            for (int e = 0; e < 32; ++e) {
+              ra[e] = __float_as_uint(score(__uint_as_float(ra[e]), k0 + c0 + e, ab, e, std::false_type{}));
+              if constexpr (kTwo)
+                rb[e] = __float_as_uint(score(__uint_as_float(rb[e]), k0 + c0 + 32 + e, ab, 32 + e, std::false_type{}));
+            }
           }
+          tmem_st32(tS + c0, ra);
+          if constexpr (kTwo) tmem_st32(tS + c0 + 32, rb);
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          mx0 = fmax3(mx0, __uint_as_float(ra[e]), __uint_as_float(ra[e + 1]));
+          if constexpr (kTwo) mx1 = fmax3(mx1, __uint_as_float(rb[e]), __uint_as_float(rb[e + 1]));
         }
       }
       if (rewrite) tmem_st_wait();
-      // row max in log2 units (-inf stays -inf)
-      float mx = BLK != 0 ? mx0 : fmaxf(mx0, mx1) * c;
+      float mx = fmaxf(mx0, mx1) * c;  // row max in log2 units (-inf stays -inf)
       if constexpr (SW > 1) {
         // the row's other column slices: every lane arrives once its value is written.  Two
         // slots: a warp writes tile n + 2's slot only after its S wait, which follows the
@@ -806,31 +786,15 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
 
       // ---- pass 2: P = 2^(c s - m) over S, 32 keys at a time: 16 columns of high part
       // (bf16 or f16 pairs), then 16 columns of bf16 remainder (zeros when not needed)
-      float2 cc = make_float2(c, c), mm = make_float2(-m_use, -m_use);
+      const float2 cc = make_float2(c, c), mm = make_float2(-m_use, -m_use);
       float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-      float lacc = 0.f;  // block-scaled: the sum of w / vs
       // one 32-key group: P and its remainder over the group's S columns
       auto p_group = [&](int c0, uint32_t* rr) {
         float xv[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) xv[e] = __uint_as_float(rr[e]);
-        float2 kf2, vl2, vi2;  // block-scaled: the two groups' scales
-        if constexpr (BLK != 0) {
-          kf2 = *reinterpret_cast<const float2*>(gs->kf + c0 / 16);
-          vl2 = *reinterpret_cast<const float2*>(gs->vl + c0 / 16);
-          vi2 = *reinterpret_cast<const float2*>(gs->vi + c0 / 16);
-        }
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
-          if constexpr (BLK != 0) {
-            if (e % 16 == 0) {
-              const float f = FEAT ? c : c * (e ? kf2.y : kf2.x);
-              const float o = (e ? vl2.y : vl2.x) - m_use;
-              cc = make_float2(f, f);
-              mm = make_float2(o, o);
-              acc0 = acc1 = make_float2(0.f, 0.f);
-            }
-          }
           const float2 u = __ffma2_rn(make_float2(xv[e], xv[e + 1]), cc, mm);
           const float2 w = __ffma2_rn(make_float2(xv[e + 2], xv[e + 3]), cc, mm);
           xv[e] = fast_exp2(u.x);
@@ -839,10 +803,6 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
           xv[e + 3] = fast_exp2(w.y);
           acc0 = __fadd2_rn(acc0, make_float2(xv[e], xv[e + 1]));
           acc1 = __fadd2_rn(acc1, make_float2(xv[e + 2], xv[e + 3]));
-          if constexpr (BLK != 0) {
-            if (e % 16 == 12)
-              lacc = fmaf((acc0.x + acc0.y) + (acc1.x + acc1.y), e > 16 ? vi2.y : vi2.x, lacc);
-          }
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -865,7 +825,7 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
         tmem_ld_wait();
         p_group(c0, rr);
       }
-      l = l * alpha + (BLK != 0 ? lacc : (acc0.x + acc0.y) + (acc1.x + acc1.y));
+      l = l * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y));
       tmem_st_wait();
       if (warp_lo && lane == 0) lo_flag[2 * qt + (n & 1)] = n + 1;
       tc_fence_before();
@@ -875,6 +835,8 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
 
     // ---- epilogue: O / l for one partition, or the partition's max / sum / O
     // the last P.V (two S buffers: the tile's last pv_done phase; one: its only phase)
+    if (BLK != 0 && DB && ok && n_tiles > 1 && active)  // (not waited for in the walk)
+      ok = pf_wait_warp(pv_done(qt), n_tiles & 1, abort_flag, p.status);
     if (ok && n_tiles > 0 && active)
       ok = pf_wait_warp(pv_done(qt), DB ? (n_tiles - 1) & 1 : 0, abort_flag, p.status);
     tc_fence_after();
@@ -1001,6 +963,10 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
   if (warp == kMma) tmem_dealloc(tmem, C::kTmemCols);
 }
 
+// Block-scaled caches: one softmax warp per lane quarter and one pass over the scores
+// (blk_softmax_tile); with two, which have to agree on every tile's maxima, one-tile CTAs took
+// 34.2 against 31.5 us for a prompt of 1000 tokens and two-tile CTAs 841 against 791 us for two
+// chunks of 4096 behind 4096 (both in two passes).  Other caches:
 // One q tile a CTA: four softmax warps per lane quarter at head_dim 128 with a 16-bit cache
 // (32 key columns a warp: the per-tile chain of a thread shortens; the mixed batch went
 // from 24.5 to 22 us against two), two at head_dim 64 (O's 64 columns) and for fp8 caches
@@ -1009,7 +975,7 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
 // softmax too measured slower on GB300 (the d128 long prefill went from 1.12 to 1.19 ms).
 template <int D, int NQ, bool BF16, bool FEAT, bool F8 = false, int BLK = 0>
 cudaError_t launch_prefill_tm_t(const PrefillParams& pp, dim3 grid, cudaStream_t stream) {
-  constexpr int SW = NQ == 1 ? (D == 128 && !F8 ? 4 : 2) : 1;
+  constexpr int SW = NQ == 1 && BLK == 0 ? (D == 128 && !F8 ? 4 : 2) : 1;
   using C = PrefillTmCfg<D, NQ, F8, SW, BLK>;
   auto kern = ua_prefill_tm_kernel<D, NQ, BF16, FEAT, F8, SW, BLK>;
   static std::atomic<unsigned long long> configured{0};  // one bit per device
