@@ -324,7 +324,8 @@ typedef struct {
  *
  * Asynchronous on `stream`, capturable, no workspace, no allocation.  Returns UA_OK or
  * UA_ERR_INVALID_ARG (a missing or misaligned pointer, a size, stride or enum value that is
- * not accepted, scales that do not fit the cache's type), UA_ERR_UNSUPPORTED (a 16-bit cache
+ * not accepted, strides by which q_out or a scale array overlaps itself, scales that do not fit
+ * the cache's type), UA_ERR_UNSUPPORTED (a 16-bit cache
  * of another type than k and v), UA_ERR_CUDA.
  */
 int ua_append_kv(const ua_append_t* call, void* stream);
@@ -361,9 +362,8 @@ size_t ua_workspace_bytes(const ua_shape_t* shape, int block_size, int num_q_hea
  * ua_device_status -- synchronises `stream`, then stores in *status the device
  * check word the kernels of this library raised since the last reset, mapped to
  * UA_OK, UA_ERR_DEVICE_CHECK (a block id outside the cache, a position outside the
- * rotation table, or a q_len above max_seqlen_q or kv_len above max_seqlen_k in a
- * decode-shaped call) or UA_ERR_TIMEOUT (a
- * bounded wait expired).  Returns UA_OK or UA_ERR_CUDA / UA_ERR_INVALID_ARG.
+ * rotation table, or a q_len above max_seqlen_q in a decode-shaped call) or
+ * UA_ERR_TIMEOUT (a bounded wait expired).  Returns UA_OK or UA_ERR_CUDA / UA_ERR_INVALID_ARG.
  * The word reports what the kernels refuse to read rather than faulting: a bad block id
  * is never dereferenced (its keys count as zero).  Slots of a sequence's last page at or
  * past kv_len are never an input either: whatever they hold (NaN included) gets weight

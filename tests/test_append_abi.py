@@ -69,6 +69,12 @@ AXES = (ctypes.c_uint8 * 32)(*([0] * 31 + [2]))
     (dict(cos_sin=None), INVALID),
     (dict(k_stride=(ctypes.c_int64 * 2)(512, 60)), INVALID),
     (dict(q_out_stride=(ctypes.c_int64 * 2)(-512, 64)), INVALID),
+    (dict(q_out_stride=(ctypes.c_int64 * 2)(0, 64)), INVALID),  # overlapping outputs
+    (dict(q_out_stride=(ctypes.c_int64 * 2)(248, 64)), INVALID),
+    (dict(q_out_stride=(ctypes.c_int64 * 2)(64, 376)), INVALID),
+    (dict(total_q=2 ** 31 - 1, block_size=1, kv_dtype=4, k_scale_blk=FAKE, v_scale_blk=FAKE,
+          k_scale_blk_stride=(ctypes.c_int64 * 2)(2, 1),
+          v_scale_blk_stride=(ctypes.c_int64 * 2)(2, 0)), INVALID),
     (dict(head_dim=96), INVALID),
     (dict(num_kv_heads=0), INVALID),
     (dict(block_size=0), INVALID),
@@ -89,6 +95,9 @@ AXES = (ctypes.c_uint8 * 32)(*([0] * 31 + [2]))
     (dict(kv_dtype=2), INVALID),                               # e4m3 without scales
     (dict(kv_dtype=2, kv_scale=FAKE, k_scale_blk=FAKE, v_scale_blk=FAKE), INVALID),
     (dict(kv_dtype=2, k_scale_tok=FAKE), INVALID),
+    (dict(kv_dtype=2, k_scale_tok=FAKE, v_scale_tok=FAKE,
+          k_scale_tok_stride=(ctypes.c_int64 * 3)(32, 2, 1),
+          v_scale_tok_stride=(ctypes.c_int64 * 3)(16, 2, 1)), INVALID),
     (dict(kv_dtype=2, k_scale_blk=FAKE), INVALID),
     (dict(kv_dtype=2, k_scale_blk=FAKE + 2, v_scale_blk=FAKE), INVALID),
     (dict(kv_dtype=4), INVALID),                               # int8 without scales

@@ -319,4 +319,10 @@ def test_refusals():
     call(ua.UaError, k_scale_blk=None, v_scale_blk=None, **f16)  # bf16 k, f16 cache
     call(ValueError, q=None, q_out=d["q"])
     call(ValueError, q_out=d["q"][:, :1])
+    # outputs that overlap themselves: one row for all tokens, one scale for all heads
+    call(ua.UaError, q_out=torch.empty_like(d["q"][:1]).expand_as(d["q"]))
+    call(ua.UaError, q_out=torch.empty_like(d["q"][:, :1]).expand_as(d["q"]))
+    for n in ("k_scale_blk", "v_scale_blk"):
+        call(ua.UaError, **{n: d[n][:, :1].contiguous().expand(-1, d[n].shape[1])})
+        call(ua.UaError, **{n: d[n][:1].contiguous().expand_as(d[n])})
     assert ua.device_status() == 0

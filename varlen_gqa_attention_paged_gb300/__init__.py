@@ -177,12 +177,10 @@ class PreparedAttention:
                         ("block_table", block_table), ("out", out)):
             if t is None:
                 continue
-            if t is not self._keep[name]:
-                if (tuple(t.shape), t.dtype, t.device) != self._meta[name] or \
-                        not t.is_contiguous():
-                    raise ValueError(f"{name}: shape, dtype, device or layout differs from the "
-                                     "prepared call")
-                self._keep[name] = t
+            if (t.shape, t.dtype, t.device) != self._meta[name] or not t.is_contiguous():
+                raise ValueError(f"{name}: shape, dtype, device or layout differs from the "
+                                 "prepared call")
+            self._keep[name] = t
             args[self._POS[name]] = t.data_ptr()
         if stream is not None:
             args[-2] = ctypes.c_void_p(stream.cuda_stream)
@@ -404,11 +402,13 @@ class PreparedAppend:
                         ("block_table", block_table), ("positions", positions)):
             if t is None:
                 continue
-            if t is not keep[name]:
-                if (t.shape, t.stride(), t.dtype, t.device) != self._meta.get(name):
-                    raise ValueError(f"{name}: shape, strides, dtype or device differs from the "
-                                     "prepared call")
-                keep[name] = t
+            # (the prepared tensor itself may have been resized in place)
+            meta = self._meta.get(name)
+            if (t.shape, t.stride()) != meta[:2] if t is keep[name] else \
+                    (t.shape, t.stride(), t.dtype, t.device) != meta:
+                raise ValueError(f"{name}: shape, strides, dtype or device differs from the "
+                                 "prepared call")
+            keep[name] = t
             ptr = t.data_ptr()
             if ptr != ptrs[name]:
                 setattr(self._call, name, ptr)

@@ -242,6 +242,13 @@ size_t scratch_bytes(size_t rows, int d) {
   return 2 * round256(rows * sizeof(float)) + round256(rows * d * sizeof(float));
 }
 
+// An even share's partial rows: tokens of a sequence that the decode tile holds, and the rows of
+// all tokens and ranges (see STREAM in ua_decode.cuh).
+int share_step(int group, bool pair) { return ((pair ? 4 : 8) + group - 1) / group; }
+size_t share_rows(int total_q, int hq, long long ranges, int step) {
+  return (static_cast<size_t>(total_q) + static_cast<size_t>(ranges) * step) * hq;
+}
+
 bool is_tc(int kernel) { return kernel == ua::KERNEL_TC128 || kernel == ua::KERNEL_TC256; }
 
 void make_plan(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, int window_left,
@@ -398,8 +405,8 @@ void make_plan(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, int
     pl->cluster_y = scy;
     pl->cluster_z = 1;
     pl->slot_per_seq = 0;
-    const size_t rows = static_cast<size_t>(sh->total_q) * hq;
-    pl->workspace_bytes = scratch_bytes(rows * pl->n_part, d) + round256(rows * sizeof(int));
+    pl->workspace_bytes = scratch_bytes(share_rows(sh->total_q, hq, ranges, share_step(hq / hkv, pair)), d) +
+                          round256(static_cast<size_t>(sh->total_q) * hq * sizeof(int2));
     return;
   }
   pl->path = n_part > 1 ? UA_PATH_SPLIT : UA_PATH_2D;
@@ -478,7 +485,9 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
   const int kv = kv_kind(sh, kv_dtype);
   const bool blk_scales = kv == ua::KV_E4M3B || kv == ua::KV_I8B;
   const bool tok_scales = kv_dtype == UA_DT_F8E4M3 && sh->k_scale_tok != nullptr;
-  if (kv_dtype == UA_DT_F8E4M3 || kv_dtype == UA_DT_I8) {
+  if (kv_dtype != UA_DT_F8E4M3 && kv_dtype != UA_DT_I8) {
+    if (sh->k_scale_blk || sh->v_scale_blk) return UA_ERR_INVALID_ARG;
+  } else {
     if ((sh->k_scale_blk == nullptr) != (sh->v_scale_blk == nullptr)) return UA_ERR_INVALID_ARG;
     if (kv_dtype == UA_DT_I8 && !sh->k_scale_blk) return UA_ERR_INVALID_ARG;
     if (blk_scales) {
@@ -612,12 +621,15 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
     } else if ((rc = library_workspace(stream, pl.workspace_bytes, &ws)) != UA_OK) {
       return rc;
     }
-    const size_t rows = static_cast<size_t>(sh->total_q) * hq * pl.n_part;
+    const bool share = pl.kernel == ua::KERNEL_DEC8S;
+    p.share_step = share_step(hq / hkv, pl.grid_y < hkv);
+    const size_t rows = share ? share_rows(sh->total_q, hq, pl.grid_x, p.share_step)
+                              : static_cast<size_t>(sh->total_q) * hq * pl.n_part;
     const size_t ml = round256(rows * sizeof(float));
     p.ws_m = static_cast<float*>(ws);
     p.ws_l = reinterpret_cast<float*>(static_cast<char*>(ws) + ml);
     p.ws_acc = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * ml);
-    p.ws_np = reinterpret_cast<int*>(static_cast<char*>(ws) + scratch_bytes(rows, d));
+    if (share) p.ws_np = reinterpret_cast<int2*>(static_cast<char*>(ws) + scratch_bytes(rows, d));
   }
   const dim3 grid(pl.grid_x, pl.grid_y, pl.grid_z);
   cudaEvent_t* ev = static_cast<cudaEvent_t*>(sh->events);
@@ -682,13 +694,14 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
       mp.np = p.ws_np;
       mp.end = cu_seqlens_q + sh->num_seqs;
       mp.hq = hq;
+      mp.share_step = p.share_step;
     }
     mp.ws_m = p.ws_m;
     mp.ws_l = p.ws_l;
     mp.ws_acc = p.ws_acc;
     mp.out = out;
     mp.rows = sh->total_q * hq;
-    mp.n_part = pl.n_part;
+    mp.n_part = pl.kernel == ua::KERNEL_DEC8S ? pl.grid_x : pl.n_part;
     mp.head_dim = d;
     mp.out_dtype = sh->out_dtype;
     if (ua::launch_merge(mp, st) != cudaSuccess) return UA_ERR_CUDA;

@@ -14,6 +14,22 @@ bool row_strides(const int64_t* s) {
   return s[0] >= 0 && s[1] >= 0 && s[0] % 8 == 0 && s[1] % 8 == 0;
 }
 
+// No two elements of a written array [s0][s1](..[inner contiguous]) share memory: each stride,
+// from the smallest, clears what lies under it.  (Sizes of one have no stride.)
+template <int N>
+bool disjoint(const int64_t* stride, const int64_t (&size)[N], int64_t inner) {
+  int order[N];
+  for (int i = 0; i < N; ++i) order[i] = i;
+  std::sort(order, order + N, [&](int a, int b) { return stride[a] < stride[b]; });
+  __int128 reach = inner;
+  for (int i : order) {
+    if (size[i] <= 1) continue;
+    if (stride[i] < reach) return false;
+    reach = static_cast<__int128>(stride[i]) * size[i];
+  }
+  return true;
+}
+
 int check(const ua_append_t& a) {
   if (a.num_seqs < 0 || a.total_q < 0 || a.max_seqlen_q < 0 || a.max_blocks_per_seq < 0 ||
       a.num_blocks < 0 || a.block_size < 1 || a.num_kv_heads < 1 || a.num_q_heads < 0)
@@ -49,7 +65,7 @@ int check(const ua_append_t& a) {
 
 template <int D, bool BF, bool I8>
 cudaError_t launch_blk(const ua::AppendParams& p, dim3 g, dim3 t, bool filled, cudaStream_t st) {
-  const bool one = (D / 16) * p.block_size <= static_cast<int>(t.x);
+  const bool one = p.block_size <= static_cast<int>(t.x) / (D / 16);
   const auto kern = !one     ? ua::ua_append_blk_kernel<D, BF, I8, false, 3>
                     : filled ? ua::ua_append_blk_kernel<D, BF, I8, true, 4>
                              : ua::ua_append_blk_kernel<D, BF, I8, true, 3>;
@@ -96,6 +112,17 @@ int append(const ua_append_t& a, cudaStream_t st) {
   for (int i = 0; i < 2; ++i)
     if (a.k_scale_blk && (a.k_scale_blk_stride[i] < 0 || a.v_scale_blk_stride[i] < 0))
       return UA_ERR_INVALID_ARG;
+  // what is written may not overlap itself
+  const int64_t rows[2] = {a.total_q, a.num_q_heads};
+  const int64_t tok[3] = {a.num_blocks, a.block_size, a.num_kv_heads};
+  const int64_t blocks[2] = {a.num_blocks, a.num_kv_heads};
+  if (a.q && !disjoint(a.q_out_stride, rows, a.head_dim)) return UA_ERR_INVALID_ARG;
+  if (a.k_scale_tok &&
+      !(disjoint(a.k_scale_tok_stride, tok, 1) && disjoint(a.v_scale_tok_stride, tok, 1)))
+    return UA_ERR_INVALID_ARG;
+  if (a.k_scale_blk &&
+      !(disjoint(a.k_scale_blk_stride, blocks, 1) && disjoint(a.v_scale_blk_stride, blocks, 1)))
+    return UA_ERR_INVALID_ARG;
   if (a.max_blocks_per_seq < 1 || a.num_blocks < 1) return UA_ERR_INVALID_ARG;
 
   int sms = 0;
@@ -187,10 +214,12 @@ int append(const ua_append_t& a, cudaStream_t st) {
   bool filled = false;
   if (blk) {
     const int bs = a.block_size;
-    threads = std::min(ua::kBlkThreads, ((a.head_dim / 16) * bs + 31) / 32 * 32);
+    threads = std::min(ua::kBlkThreads, ((a.head_dim / 16) * std::min(bs, ua::kBlkThreads) + 31) / 32 * 32);
     threads = std::max(threads, 64);
     p.slot_per_seq = a.max_seqlen_q <= 1;
-    p.slots = p.slot_per_seq ? a.num_seqs : a.total_q / bs + 2 * a.num_seqs;
+    const long long slots = p.slot_per_seq ? a.num_seqs : a.total_q / bs + 2LL * a.num_seqs;
+    if (slots > INT_MAX) return UA_ERR_INVALID_ARG;
+    p.slots = static_cast<int>(slots);
     // a CTA walks kv-heads (its rows' cosines and sines stay in registers) while the grid
     // still has three CTAs an SM
     auto hgroups = [&] { return (p.hkv + p.heads_per_cta - 1) / p.heads_per_cta; };

@@ -119,9 +119,12 @@ struct DecCfg {
 // into gridDim.x equal ranges (at least kStreamMinTiles tiles each), and CTA x walks range x,
 // which may begin and end inside a sequence and hold several: ragged batches load every SM
 // alike, where a partition count for all leaves the SMs of short sequences idle.  A sequence
-// inside one range is written as output; one cut into np > 1 leaves a partial row a range in
-// the scratch, and np in ws_np for the merge kernel (1: nothing to merge).  The copies of the
-// next sequence follow the last one's without a pause.
+// inside one range is written as output; one cut into several leaves a partial row a range in
+// the scratch, and in ws_np the first of them and their number for the merge kernel.  Token t's
+// partial rows of range x are number t + x * share_step (share_step: the most tokens of a
+// sequence that the tile holds), which no two (t, x) share: a later sequence's ranges never lie
+// before an earlier one's.  So the scratch grows with the tokens and the ranges, not with their
+// product.  The copies of the next sequence follow the last one's without a pause.
 template <int D, int KV, bool FEAT, int QT, int W, int HP = 1, bool STREAM = false>
 __global__ void __launch_bounds__(DecCfg<D, KV, W, HP, STREAM>::kThreads,
                                   (DecCfg<D, KV, W, HP, STREAM>::kMinBlocks))
@@ -1062,7 +1065,8 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP, STREAM>::kThreads,
           if (!rv[e]) continue;
           // row 2cq + e: this lane's 16-column runs gq D/8 .. of it
           const size_t row = static_cast<size_t>(q0 + ri[e]) * p.hq + rh[e];
-          if (np > p.n_part) continue;  // kv_len above max_seqlen_k: the scratch has no room
+          const size_t part = (static_cast<size_t>(q0 + ri[e]) +
+                               static_cast<size_t>(blockIdx.x) * p.share_step) * p.hq + rh[e];
           if (np == 1) mul = l > 0.f ? mul / l : 0.f;
           float x[2 * C::kMT];
 #pragma unroll
@@ -1072,7 +1076,7 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP, STREAM>::kThreads,
           }
           const int c0 = gq * (D / 8);
           if (np > 1 || p.out_dtype == UA_DT_F32) {
-            float* const dst = np > 1 ? p.ws_acc + (row * p.n_part + z) * D + c0
+            float* const dst = np > 1 ? p.ws_acc + part * D + c0
                                       : static_cast<float*>(p.out) + row * D + c0;
 #pragma unroll
             for (int i = 0; i < 2 * C::kMT; i += 4)
@@ -1087,21 +1091,22 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP, STREAM>::kThreads,
                              bf ? pack_bf16(x[i + 2], x[i + 3]) : pack_f16(x[i + 2], x[i + 3]));
           }
           if (gq == 0 && np > 1) {
-            p.ws_m[row * p.n_part + z] = m_run[e];
-            p.ws_l[row * p.n_part + z] = l;
+            p.ws_m[part] = m_run[e];
+            p.ws_l[part] = l;
           }
         }
-        // partitions of the sequence's rows, for the merge (rows past RH: left as they are)
+        // the sequence's first range (this one) and their number (1: nothing to merge; rows past
+        // RH too, which stay as they are), for the merge
         if (z == 0) {
           const int n = HP * rows_b;
           for (int i = lane; i < n; i += 32) {
             const int hh = i / rows_b, r = i % rows_b;
             const size_t t = static_cast<size_t>(q0 + r / G);
             if (t < static_cast<size_t>(p.total_q))
-              p.ws_np[t * p.hq + (g + hh) * G + r % G] = r < RH && np <= p.n_part ? np : 1;
+              p.ws_np[t * p.hq + (g + hh) * G + r % G] =
+                  make_int2(static_cast<int>(blockIdx.x), r < RH ? np : 1);
           }
-          if ((rows_b > RH || np > p.n_part) && lane == 0 && g == 0)
-            atomicOr(p.status, DEV_BAD_SHAPE);
+          if (rows_b > RH && lane == 0 && g == 0) atomicOr(p.status, DEV_BAD_SHAPE);
         }
       }
       tb += ntiles;

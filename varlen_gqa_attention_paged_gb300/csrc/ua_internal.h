@@ -54,7 +54,10 @@ struct AttnParams {
   float* ws_m;                  // [total_q, hq, n_part]     (n_part > 1)
   float* ws_l;                  // [total_q, hq, n_part]
   float* ws_acc;                // [total_q, hq, n_part, D]
-  int* ws_np;                   // [total_q, hq]: an even share's partitions of a row
+  // an even share (the decode tile's STREAM): [total_q, hq] a row's first range and ranges, and
+  // partial rows [tokens, hq] with share_step tokens from one range to the next
+  int2* ws_np;
+  int share_step;
   unsigned int* status;         // device status word
   int num_seqs, total_q, max_seqlen_q, max_blocks_per_seq, num_blocks, block_size;
   int hq, hkv, group;
@@ -89,11 +92,12 @@ struct PrefillParams {
 
 // The LSE-merge of split partitions (one output row per query token x head).
 struct MergeParams {
-  // an even share's partitions of each row (1: nothing to merge; n_part is the row's stride
-  // then) and the end of the last sequence's tokens, or null: n_part for every row
-  const int* np;
+  // an even share's first range and ranges of each row (1: nothing to merge), the tokens from one
+  // range's partial rows to the next's and the end of the last sequence's tokens, n_part ranges; or
+  // null: n_part partial rows of every row, one after the other
+  const int2* np;
   const int32_t* end;
-  int hq;
+  int hq, share_step;
   const float* ws_m;
   const float* ws_l;
   const float* ws_acc;
@@ -174,8 +178,7 @@ cudaError_t launch_decode_blk_stream_pair_d128(const TileParams& tp, dim3 grid, 
 int decode_cluster_capacity_blk_stream_pair(int head_dim, int kv, int cluster_y, int cluster_z);
 // co-resident clusters of cluster_y CTAs of the even-share kernels (-1: unknown; cached)
 int decode_stream_capacity(int head_dim, int kv, bool pair, int cluster_y);
-// the smallest range of an even share, in 64-key tiles (it bounds the partitions of a sequence,
-// and so the scratch)
+// the smallest range of an even share, in 64-key tiles
 constexpr int kStreamMinTiles = 8;
 // resident CTAs per SM of the four-warp decode tile
 int decode_ctas_per_sm(int head_dim, int kv);

@@ -14,7 +14,7 @@
 
 namespace ua {
 
-template <int D>
+template <int D, bool SHARE>
 __global__ void __launch_bounds__(256) ua_merge_kernel(const __grid_constant__ MergeParams p) {
   constexpr int kPer = D / 32;  // output elements per lane
   grid_dependency_wait();        // the partition kernel's scratch is complete
@@ -24,14 +24,18 @@ __global__ void __launch_bounds__(256) ua_merge_kernel(const __grid_constant__ M
   const int row = blockIdx.x * 8 + warp;
   if (row >= p.rows) return;
   int np = p.n_part;
-  const float* m = p.ws_m + static_cast<size_t>(row) * np;
-  const float* l = p.ws_l + static_cast<size_t>(row) * np;
-  const float* a = p.ws_acc + static_cast<size_t>(row) * np * D + lane * kPer;
-  if (p.np != nullptr) {  // an even share: a row's own partitions, none for rows of no token
+  size_t first = static_cast<size_t>(row) * np, step = 1;  // of the row's partial rows
+  if constexpr (SHARE) {  // its own ranges, none for rows of no token
     if (row / p.hq >= *p.end) return;
-    np = min(p.np[row], np);
-    if (np <= 1) return;
+    const int2 own = p.np[row];
+    np = own.y;  // (an aborted partition kernel may have left anything)
+    if (np <= 1 || own.x < 0 || own.x > p.n_part - np) return;
+    step = static_cast<size_t>(p.share_step) * p.hq;
+    first = row + own.x * step;
   }
+  const float* m = p.ws_m + first;
+  const float* l = p.ws_l + first;
+  const float* a = p.ws_acc + first * D + lane * kPer;
 
   // Partitions go 32 at a time, one per lane: max and sum loads are independent, the
   // row max and sum are warp reductions, and every partition's weight reaches the lanes
@@ -40,7 +44,7 @@ __global__ void __launch_bounds__(256) ua_merge_kernel(const __grid_constant__ M
   float M = -INFINITY;
   for (int z0 = 0; z0 < np; z0 += 32) {
     const int z = z0 + lane;
-    if (z < np && l[z] > 0.f) M = fmaxf(M, m[z]);
+    if (z < np && l[z * step] > 0.f) M = fmaxf(M, m[z * step]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -52,14 +56,14 @@ __global__ void __launch_bounds__(256) ua_merge_kernel(const __grid_constant__ M
   if (M != -INFINITY) {
     for (int z0 = 0; z0 < np; z0 += 32) {
       const int z = z0 + lane;
-      const float lz = z < np ? l[z] : 0.f;
-      const float wz = lz > 0.f ? fast_exp2(m[z] - M) : 0.f;
+      const float lz = z < np ? l[z * step] : 0.f;
+      const float wz = lz > 0.f ? fast_exp2(m[z * step] - M) : 0.f;
       L += lz * wz;
       const int nz = min(32, np - z0);
 #pragma unroll 8
       for (int k = 0; k < nz; ++k) {
         const float wt = __shfl_sync(0xffffffffu, wz, k);
-        const float* az = a + static_cast<size_t>(z0 + k) * D;
+        const float* az = a + static_cast<size_t>(z0 + k) * step * D;
 #pragma unroll
         for (int e = 0; e < kPer; e += 2) {
           const float2 v = *reinterpret_cast<const float2*>(az + e);
@@ -88,10 +92,11 @@ __global__ void __launch_bounds__(256) ua_merge_kernel(const __grid_constant__ M
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t s) {
   if (p.rows <= 0) return cudaSuccess;
   const dim3 grid((p.rows + 7) / 8);
+  const bool share = p.np != nullptr;
   switch (p.head_dim) {
-    case 64: return launch_pdl(ua_merge_kernel<64>, grid, dim3(256), 0, s, 1, p);
-    case 128: return launch_pdl(ua_merge_kernel<128>, grid, dim3(256), 0, s, 1, p);
-    case 256: return launch_pdl(ua_merge_kernel<256>, grid, dim3(256), 0, s, 1, p);
+    case 64: return launch_pdl(share ? ua_merge_kernel<64, true> : ua_merge_kernel<64, false>, grid, dim3(256), 0, s, 1, p);
+    case 128: return launch_pdl(share ? ua_merge_kernel<128, true> : ua_merge_kernel<128, false>, grid, dim3(256), 0, s, 1, p);
+    case 256: return launch_pdl(share ? ua_merge_kernel<256, true> : ua_merge_kernel<256, false>, grid, dim3(256), 0, s, 1, p);
     default: return cudaErrorInvalidValue;
   }
 }
