@@ -210,6 +210,36 @@ int ua_unified_attention(const void* q, const void* k_cache, const void* v_cache
                          void* stream, const ua_shape_t* shape);
 
 /*
+ * ua_unified_attention_call -- the same call with its arguments in one struct, for bindings that
+ * pay for every argument and make one call again and again (Python's ctypes takes 2.0 us for the
+ * 22 arguments above and 0.4 us for two).  NULL: UA_ERR_INVALID_ARG.
+ */
+typedef struct {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  void* out;
+  const int32_t* cu_seqlens_q;
+  const int32_t* seq_lens_k;
+  const int32_t* block_table;
+  const float* alibi_slopes;
+  const float* qq_bias;
+  const float* sinks;
+  const float* kv_scale;
+  const ua_shape_t* shape;
+  int32_t block_size;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  float scale;
+  float softcap;
+  int32_t window_left;
+  int32_t kv_dtype;
+  int32_t backend;
+} ua_attention_t;
+int ua_unified_attention_call(const ua_attention_t* call, void* stream);
+
+/*
  * ua_unified_attention_noalloc -- ua_unified_attention for callers that may not
  * allocate device memory (the pages have no counterpart: this is a library service).
  *

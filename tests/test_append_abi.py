@@ -13,12 +13,14 @@ from varlen_gqa_attention_paged_gb300 import _lib
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
-def test_append_struct_matches_the_header(tmp_path):
+@pytest.mark.parametrize("name,struct", [("ua_append_t", _lib.UaAppend),
+                                         ("ua_attention_t", _lib.UaAttention)])
+def test_struct_matches_the_header(name, struct, tmp_path):
     lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "ua.h"', "int main(void) {",
-             'printf("sizeof %zu 0\\n", sizeof(ua_append_t));']
-    for f, _ in _lib.UaAppend._fields_:
-        lines.append(f'printf("{f} %zu %zu\\n", offsetof(ua_append_t, {f}), '
-                     f"sizeof(((ua_append_t*)0)->{f}));")
+             f'printf("sizeof %zu 0\\n", sizeof({name}));']
+    for f, _ in struct._fields_:
+        lines.append(f'printf("{f} %zu %zu\\n", offsetof({name}, {f}), '
+                     f"sizeof((({name}*)0)->{f}));")
     src, exe = tmp_path / "a.c", tmp_path / "a"
     src.write_text("\n".join(lines + ["return 0;", "}"]) + "\n")
     subprocess.run(["gcc", "-std=c11", "-I", os.path.join(ROOT, "include"), "-o", str(exe),
@@ -28,10 +30,16 @@ def test_append_struct_matches_the_header(tmp_path):
                              text=True).stdout.splitlines():
         n, a, b = ln.split()
         got[n] = (int(a), int(b))
-    assert got.pop("sizeof")[0] == ctypes.sizeof(_lib.UaAppend)
-    for f, _ in _lib.UaAppend._fields_:
-        desc = getattr(_lib.UaAppend, f)
+    assert got.pop("sizeof")[0] == ctypes.sizeof(struct)
+    for f, _ in struct._fields_:
+        desc = getattr(struct, f)
         assert got[f] == (desc.offset, desc.size), f
+
+
+def test_the_struct_call_without_a_struct():
+    assert _lib.load().ua_unified_attention_call(None, None) == _lib.UA_ERR_INVALID_ARG
+    assert _lib.load().ua_unified_attention_call(_lib.UaAttention(), None) == \
+        _lib.UA_ERR_INVALID_ARG
 
 
 FAKE = 0x7f0000001000  # aligned, never dereferenced: every case fails validation first

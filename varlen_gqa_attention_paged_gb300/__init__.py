@@ -158,36 +158,38 @@ class PreparedAttention:
     stay as prepared.  Returns ``out``.
     """
 
-    _STEP = ("q", "cu_seqlens_q", "seq_lens_k", "block_table", "out")
-    _POS = {"q": 0, "out": 3, "cu_seqlens_q": 4, "seq_lens_k": 5, "block_table": 6}
-
-    def __init__(self, lib, args, shape, tensors, stream):
+    def __init__(self, lib, call, tensors, stream):
         self._lib = lib
-        self._args = args
-        self._shape = shape
-        self._meta = {n: (tuple(t.shape), t.dtype, t.device) for n, t in tensors.items()}
-        self._keep = dict(tensors)
+        self._call = call
+        self._ref = ctypes.byref(call)
+        self._meta = {n: (t.shape, t.dtype, t.device) for n, t in tensors.items()}
+        self._now = {n: (t, t.data_ptr(), t.shape) for n, t in tensors.items()}
         self._stream = stream
         self.out = tensors["out"]
 
+    def _take(self, name, t):
+        if (t.shape, t.dtype, t.device) != self._meta[name] or not t.is_contiguous():
+            raise ValueError(f"{name}: shape, dtype, device or layout differs from the "
+                             "prepared call")
+        setattr(self._call, name, t.data_ptr())
+        self._now[name] = (t, t.data_ptr(), t.shape)
+
     def __call__(self, q=None, cu_seqlens_q=None, seq_lens_k=None, block_table=None, out=None,
                  stream=None):
-        args = self._args
+        now = self._now
         for name, t in (("q", q), ("cu_seqlens_q", cu_seqlens_q), ("seq_lens_k", seq_lens_k),
                         ("block_table", block_table), ("out", out)):
             if t is None:
                 continue
-            if (t.shape, t.dtype, t.device) != self._meta[name] or not t.is_contiguous():
-                raise ValueError(f"{name}: shape, dtype, device or layout differs from the "
-                                 "prepared call")
-            self._keep[name] = t
-            args[self._POS[name]] = t.data_ptr()
+            kept, ptr, shape = now[name]
+            if t is not kept or t.data_ptr() != ptr or t.shape != shape or not t.is_contiguous():
+                self._take(name, t)
         if stream is not None:
-            args[-2] = ctypes.c_void_p(stream.cuda_stream)
-        rc = self._lib.ua_unified_attention(*args)
+            self._stream = stream
+        rc = self._lib.ua_unified_attention_call(self._ref, self._stream.cuda_stream)
         if rc != 0:
             raise UaError(rc, "ua_unified_attention")
-        return self._keep["out"]
+        return now["out"][0]
 
 
 def prepare(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *, max_seqlen_q: int,
@@ -219,14 +221,16 @@ def prepare(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *, max_s
     sh = _shape(q, k_cache, block_table, cu_seqlens_q, max_seqlen_q, max_seqlen_k, qq_bias,
                 _dtype_code(out), num_splits, workspace, None, k_scale_tok, v_scale_tok,
                 k_scale_blk, v_scale_blk)
-    args = [_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(cu_seqlens_q),
-            _ptr(seq_lens_k), _ptr(block_table), block_size, hq, hkv, d, float(scale),
-            float(softcap or 0.0), int(window_left if window_left is not None else -1),
-            _ptr(alibi_slopes), _ptr(qq_bias), _ptr(sinks), _dtype_code(k_cache), _ptr(kv_scale),
-            BACKENDS[backend], ctypes.c_void_p(stream.cuda_stream), ctypes.byref(sh)]
+    call = _lib.UaAttention(
+        *(0 if t is None else t.data_ptr()
+          for t in (q, k_cache, v_cache, out, cu_seqlens_q, seq_lens_k, block_table, alibi_slopes,
+                    qq_bias, sinks, kv_scale)),
+        ctypes.pointer(sh), block_size, hq, hkv, d, float(scale), float(softcap or 0.0),
+        int(window_left if window_left is not None else -1), _dtype_code(k_cache),
+        BACKENDS[backend])
     tensors = {"q": q, "cu_seqlens_q": cu_seqlens_q, "seq_lens_k": seq_lens_k,
                "block_table": block_table, "out": out}
-    prep = PreparedAttention(lib, args, sh, tensors, stream)
+    prep = PreparedAttention(lib, call, tensors, stream)
     # the caches, score features and scales the prepared call points at stay alive with it
     prep._static = (k_cache, v_cache, alibi_slopes, qq_bias, sinks, kv_scale, k_scale_tok,
                     v_scale_tok, k_scale_blk, v_scale_blk, workspace)
@@ -386,33 +390,33 @@ class PreparedAppend:
         self._lib = lib
         self._call = call
         self._ref = ctypes.byref(call)
-        self._keep = keep
         self._static = static
         self._meta = {n: (t.shape, t.stride(), t.dtype, t.device)
                       for n, t in keep.items() if t is not None}
-        self._ptr = {n: t.data_ptr() for n, t in keep.items() if t is not None}
+        # the tensors passed last: one passed again, as most are, costs three comparisons
+        self._now = {n: (None, 0, None) if t is None else (t, t.data_ptr(), t.shape)
+                     for n, t in keep.items()}
         self._device = keep["k"].device.index
         self._stream = stream
 
+    def _take(self, name, t):
+        if (t.shape, t.stride(), t.dtype, t.device) != self._meta.get(name):
+            raise ValueError(f"{name}: shape, strides, dtype or device differs from the "
+                             "prepared call")
+        setattr(self._call, name, t.data_ptr())
+        self._now[name] = (t, t.data_ptr(), t.shape)
+
     def __call__(self, k=None, v=None, q=None, q_out=None, cu_seqlens_q=None, seq_lens_k=None,
                  block_table=None, positions=None, stream=None):
-        keep, ptrs = self._keep, self._ptr
+        now = self._now
         for name, t in (("k", k), ("v", v), ("q", q), ("q_out", q_out),
                         ("cu_seqlens_q", cu_seqlens_q), ("seq_lens_k", seq_lens_k),
                         ("block_table", block_table), ("positions", positions)):
             if t is None:
                 continue
-            # (the prepared tensor itself may have been resized in place)
-            meta = self._meta.get(name)
-            if (t.shape, t.stride()) != meta[:2] if t is keep[name] else \
-                    (t.shape, t.stride(), t.dtype, t.device) != meta:
-                raise ValueError(f"{name}: shape, strides, dtype or device differs from the "
-                                 "prepared call")
-            keep[name] = t
-            ptr = t.data_ptr()
-            if ptr != ptrs[name]:
-                setattr(self._call, name, ptr)
-                ptrs[name] = ptr
+            kept, ptr, shape = now[name]
+            if t is not kept or t.data_ptr() != ptr or t.shape != shape:
+                self._take(name, t)
         handle = (self._stream if stream is None else stream).cuda_stream
         if torch.cuda.current_device() == self._device:
             rc = self._lib.ua_append_kv(self._ref, handle)
@@ -421,7 +425,7 @@ class PreparedAppend:
                 rc = self._lib.ua_append_kv(self._ref, handle)
         if rc != 0:
             raise UaError(rc, "ua_append_kv")
-        return keep["q_out"]
+        return now["q_out"][0]
 
 
 def prepare_append(k, v, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *,

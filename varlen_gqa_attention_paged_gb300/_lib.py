@@ -19,8 +19,8 @@ UA_BACKEND_AUTO, UA_BACKEND_2D, UA_BACKEND_SPLIT = 0, 1, 2
 UA_PATH_2D, UA_PATH_SPLIT = 1, 2
 
 # every symbol include/ua.h declares
-EXPORTS = ("ua_unified_attention", "ua_unified_attention_noalloc", "ua_append_kv", "ua_plan",
-           "ua_workspace_bytes", "ua_device_status", "ua_device_status_reset",
+EXPORTS = ("ua_unified_attention", "ua_unified_attention_call",
+           "ua_unified_attention_noalloc", "ua_append_kv", "ua_plan", "ua_workspace_bytes", "ua_device_status", "ua_device_status_reset",
            "ua_status_string", "ua_version")
 
 
@@ -48,6 +48,17 @@ class UaShape(ctypes.Structure):
         ("k_scale_blk_stride", ctypes.c_int64 * 2),
         ("v_scale_blk_stride", ctypes.c_int64 * 2),
     ]
+
+
+class UaAttention(ctypes.Structure):
+    _fields_ = (
+        [(n, ctypes.c_void_p) for n in (
+            "q", "k_cache", "v_cache", "out", "cu_seqlens_q", "seq_lens_k", "block_table",
+            "alibi_slopes", "qq_bias", "sinks", "kv_scale")] +
+        [("shape", ctypes.POINTER(UaShape))] +
+        [(n, ctypes.c_int32) for n in ("block_size", "num_q_heads", "num_kv_heads", "head_dim")] +
+        [("scale", ctypes.c_float), ("softcap", ctypes.c_float)] +
+        [(n, ctypes.c_int32) for n in ("window_left", "kv_dtype", "backend")])
 
 
 class UaAppend(ctypes.Structure):
@@ -106,6 +117,8 @@ def load():
         lib.ua_unified_attention.restype = ctypes.c_int
         lib.ua_unified_attention_noalloc.argtypes = lib.ua_unified_attention.argtypes
         lib.ua_unified_attention_noalloc.restype = ctypes.c_int
+        lib.ua_unified_attention_call.argtypes = [ctypes.POINTER(UaAttention), vp]
+        lib.ua_unified_attention_call.restype = ctypes.c_int
         lib.ua_append_kv.argtypes = [ctypes.POINTER(UaAppend), vp]
         lib.ua_append_kv.restype = ctypes.c_int
         lib.ua_plan.argtypes = [ctypes.POINTER(UaShape), i32, i32, i32, i32, i32, i32, i32, i32,

@@ -735,6 +735,16 @@ int ua_unified_attention(const void* q, const void* k_cache, const void* v_cache
   }
 }
 
+int ua_unified_attention_call(const ua_attention_t* call, void* stream) {
+  if (call == nullptr) return UA_ERR_INVALID_ARG;
+  const ua_attention_t& c = *call;
+  return ua_unified_attention(c.q, c.k_cache, c.v_cache, c.out, c.cu_seqlens_q, c.seq_lens_k,
+                              c.block_table, c.block_size, c.num_q_heads, c.num_kv_heads,
+                              c.head_dim, c.scale, c.softcap, c.window_left, c.alibi_slopes,
+                              c.qq_bias, c.sinks, c.kv_dtype, c.kv_scale, c.backend, stream,
+                              c.shape);
+}
+
 int ua_plan(const ua_shape_t* shape, int block_size, int num_q_heads, int num_kv_heads,
             int head_dim, int window_left, int kv_dtype, int backend, int num_sms,
             ua_plan_t* plan) {
