@@ -64,9 +64,11 @@ struct DecCfg {
   // SM's issue rate where three CTAs share an SM: measured 18.7 against 20.0 us for the
   // sliding-window decode); eight consumer warps: one CTA per SM
   // STREAM: a CTA walks several sequences' keys and its ring never drains between them, so the
-  // warps' states meet in two fragment buffers of their own ([kMT][32] float4) and two
-  // exchanges of maxima and sums ([W][8])
-  static constexpr int kSegBytes = STREAM ? 2 * kMT * 512 + 2 * kConsumerWarps * kRows * 4 : 0;
+  // warps' states meet in two fragment buffers of their own ([kSegMT][32] float4) and two
+  // exchanges of maxima and sums ([W][8]); at head_dim 256 half the fragments at a time, which
+  // leaves room for a third stage
+  static constexpr int kSegMT = D == 256 ? kMT / 2 : kMT;
+  static constexpr int kSegBytes = STREAM ? 2 * kSegMT * 512 + 2 * kConsumerWarps * kRows * 4 : 0;
   static constexpr int kBudget =
       (W != 4 ? 200 : HP == 2 || D == 256 ? (STREAM ? 108 : 100) : 72) * 1024 - kSegBytes;
   static constexpr int kStagesFit = kBudget / kStageBytes;
@@ -1006,8 +1008,8 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP, STREAM>::kThreads,
       // The four warps' states of the part just walked: rescaled to the rows' max, then added up
       // in two steps (1 to 0 and 3 to 2, then 2 to 0) as MMA fragments; warp 0 writes the rows.
       if (s_abort) return;  // uniform for the consumers; the producer gives up on its waits
-      float4* const red = reinterpret_cast<float4*>(svs + S * C::kScales);  // [2][kMT][32]
-      float* const xm = reinterpret_cast<float*>(red + 2 * C::kMT * 32);    // [W][8] maxima
+      float4* const red = reinterpret_cast<float4*>(svs + S * C::kScales);  // [2][kSegMT][32]
+      float* const xm = reinterpret_cast<float*>(red + 2 * C::kSegMT * 32);  // [W][8] maxima
       float* const xl = xm + W * NR;                                        // [W][8] sums
       if (gq == 0) {
         xm[warp * NR + 2 * cq] = m_run[0];
@@ -1028,32 +1030,39 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP, STREAM>::kThreads,
           ot[m][e + 2] *= wt;
         }
       }
-      auto give = [&](int at) {
-#pragma unroll
-        for (int m = 0; m < C::kMT; ++m)
-          red[(at * C::kMT + m) * 32 + lane] = make_float4(ot[m][0], ot[m][1], ot[m][2], ot[m][3]);
-      };
-      auto get = [&](int at) {
-#pragma unroll
-        for (int m = 0; m < C::kMT; ++m) {
-          const float4 o4 = red[(at * C::kMT + m) * 32 + lane];
-          ot[m][0] += o4.x;
-          ot[m][1] += o4.y;
-          ot[m][2] += o4.z;
-          ot[m][3] += o4.w;
-        }
-      };
       if (gq == 0) {
         xl[warp * NR + 2 * cq] = l_run[0];
         xl[warp * NR + 2 * cq + 1] = l_run[1];
       }
-      if (warp & 1) give(warp >> 1);
-      named_bar_sync(1, 32 * W);
-      if (!(warp & 1)) get(warp >> 1);
-      if (warp == 2) give(1);  // (its own buffer, read just above by this warp alone)
-      named_bar_sync(1, 32 * W);
+#pragma unroll
+      for (int m0 = 0; m0 < C::kMT; m0 += C::kSegMT) {
+        auto give = [&](int at) {
+#pragma unroll
+          for (int m = 0; m < C::kSegMT; ++m) {
+            const float(&o)[4] = ot[m0 + m];
+            red[(at * C::kSegMT + m) * 32 + lane] = make_float4(o[0], o[1], o[2], o[3]);
+          }
+        };
+        auto get = [&](int at) {
+#pragma unroll
+          for (int m = 0; m < C::kSegMT; ++m) {
+            const float4 o4 = red[(at * C::kSegMT + m) * 32 + lane];
+            float(&o)[4] = ot[m0 + m];
+            o[0] += o4.x;
+            o[1] += o4.y;
+            o[2] += o4.z;
+            o[3] += o4.w;
+          }
+        };
+        if (m0 > 0) named_bar_sync(1, 32 * W);  // warp 0 has read buffer 1
+        if (warp & 1) give(warp >> 1);
+        named_bar_sync(1, 32 * W);
+        if (!(warp & 1)) get(warp >> 1);
+        if (warp == 2) give(1);  // (its own buffer, read just above by this warp alone)
+        named_bar_sync(1, 32 * W);
+        if (warp == 0) get(1);
+      }
       if (warp == 0) {
-        get(1);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float l = 0.f;
@@ -1276,8 +1285,12 @@ cudaError_t launch_decode_t(const TileParams& tp, dim3 grid, int cluster_y, int 
     if (err != cudaSuccess) return err;
     configured.fetch_or(bit);
   }
-  return launch_pdl_cluster(kern, grid, dim3(C::kThreads), C::kSmemBytes, stream, cluster_y,
-                            cluster_z, tp);
+  // An even share's grid takes every slot of the device, and follows the merge kernel of the
+  // call before in a decode loop.  Started while that one still runs, its clusters are placed
+  // unevenly around it: 106 against 83 us a call, back to back, for 48 sequences of up to 8191
+  // keys (int8, 32/8 heads, d128), 297 against 179 us at d256.  So it waits for a whole device.
+  return launch_cluster(!STREAM, kern, grid, dim3(C::kThreads), C::kSmemBytes, stream, cluster_y,
+                        cluster_z, tp);
 }
 
 template <int D, int W>

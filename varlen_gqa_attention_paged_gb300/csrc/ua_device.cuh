@@ -124,33 +124,42 @@ __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Launch with programmatic stream serialisation (the kernel must call
+// Launch, if `pdl` with programmatic stream serialisation (the kernel must call
 // grid_dependency_wait() before it touches memory the previous kernel writes), and,
 // with cluster_y or cluster_z > 1, as clusters of cluster_y x cluster_z CTAs along grid
 // y and z that the hardware schedules together.
 template <typename... Args, typename... Act>
-inline cudaError_t launch_pdl_cluster(void (*kern)(Args...), dim3 grid, dim3 block, size_t smem,
-                                      cudaStream_t stream, int cluster_y, int cluster_z,
-                                      Act&&... args) {
+inline cudaError_t launch_cluster(bool pdl, void (*kern)(Args...), dim3 grid, dim3 block,
+                                  size_t smem, cudaStream_t stream, int cluster_y, int cluster_z,
+                                  Act&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  int n = 1;
+  int n = 0;
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
   if (cluster_y > 1 || cluster_z > 1) {
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 1;
-    attr[1].val.clusterDim.y = static_cast<unsigned>(cluster_y);
-    attr[1].val.clusterDim.z = static_cast<unsigned>(cluster_z);
-    n = 2;
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 1;
+    attr[n].val.clusterDim.y = static_cast<unsigned>(cluster_y);
+    attr[n++].val.clusterDim.z = static_cast<unsigned>(cluster_z);
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Act>(args)...);
+}
+
+template <typename... Args, typename... Act>
+inline cudaError_t launch_pdl_cluster(void (*kern)(Args...), dim3 grid, dim3 block, size_t smem,
+                                      cudaStream_t stream, int cluster_y, int cluster_z,
+                                      Act&&... args) {
+  return launch_cluster(true, kern, grid, block, smem, stream, cluster_y, cluster_z,
+                        std::forward<Act>(args)...);
 }
 
 template <typename... Args, typename... Act>
