@@ -48,8 +48,8 @@ namespace ua {
 // write it into its f16 slot, exactly (every e4m3 value is an f16), so the f16 MMAs and the softmax run
 // unchanged; k_scale joins the score scale and v_scale the output (per-token scales:
 // folded into each key's f16 row instead).
-// Block-scaled caches: 24/4 heads, two chunks of 4096 behind 4096, e4m3: 1104 us; three chunks
-// of 1501 to 2999 tokens with a softcap, int8: 251 us (628 TFLOP/s; 199 without the softcap),
+// Block-scaled caches: 24/4 heads, two chunks of 4096 behind 4096, e4m3: 1104 us; three ragged
+// chunks of up to 1501 tokens (2999 keys) with a softcap, int8: 251 us (628 TFLOP/s; 199 without the softcap),
 // bound by the dequant warps' and the softmax warps' instructions (issue slots 54 %, tensor 32 %).
 // SW: softmax warps per tensor-memory lane quarter (2: each takes half the key columns of S
 // and half the columns of O, and the row maxima meet in shared memory once a tile).
