@@ -138,6 +138,16 @@ def test_append_lengths(lens, cache, form):
     check(c, d, run(c, d))
 
 
+@pytest.mark.parametrize("cache,form", [(None, ""), (I8, "blk")])
+def test_append_thousands_of_sequences(cache, form):
+    """The search for a token's and a page's sequence in several rounds, empty ones between."""
+    lens = [((3 * i * i) % 4 if i % 7 else 0, 1 + i % 23) for i in range(2100)]
+    lens = [(min(q, kv), kv) for q, kv in lens] + [(0, 5)] * 40
+    c = R.make(R.Case(lens, hq=2, hkv=1, d=64, bs=16, cache=cache, form=form, rot=64, seed=4))
+    d = to_dev(c)
+    check(c, d, run(c, d))
+
+
 @pytest.mark.parametrize("cache,form", [(None, ""), (E4M3, "tok"), (I8, "blk")])
 def test_tokens_before_the_cache_are_skipped(cache, form):
     """kv_len < q_len (a padded slot): the tokens at negative positions write nothing."""
