@@ -467,3 +467,22 @@ def test_two_even_shares_at_once():
     torch.cuda.synchronize()
     for c, step in zip(cs, steps):
         check(c, step.out)
+
+
+@pytest.mark.parametrize("bs", [64, 24])
+@pytest.mark.parametrize("shape,max_k", [("decode4", None), ("chunks", None), ("ragged", 40000)])
+def test_blocks_past_32_bits_of_a_large_cache(shape, max_k, bs):
+    """Blocks that lie past 2^32 bytes of the cache, with the scales of all its blocks."""
+    c = make(**{**(RAGGED if shape == "ragged" else SHAPES)[shape], "bs": bs}, d=128, code=I8,
+             seed=2)
+    d = on_gpu(c)
+    nb, _, hkv, dim = d["k_cache"].shape
+    first = 2 ** 32 // (bs * hkv * dim) + 1
+    for n in ("k", "v"):
+        cache = torch.zeros((first + nb, bs, hkv, dim), dtype=I8, device="cuda")
+        cache[first:] = d[f"{n}_cache"]
+        scales = torch.full((first + nb, hkv), float("nan"), device="cuda")
+        scales[first:] = d[f"{n}_scale_blk"]
+        d[f"{n}_cache"], d[f"{n}_scale_blk"] = cache, scales
+    d["block_table"] += first
+    check(c, run(c, d, max_k=max_k))
