@@ -3,8 +3,8 @@
 Python binding of the C ABI in ``include/ua.h``: it only turns torch tensors into
 device pointers, the current CUDA stream and host-side sizes, and calls
 ``ua_append_kv`` (new keys and values into the paged cache, rotated by position) and
-``ua_unified_attention`` (attention over it) in ``libua.so``.  Every step of the computation runs in the
-library's CUDA kernels; without the built library this module raises.
+``ua_unified_attention`` (attention over it) in ``libua.so``.  Every step of the computation
+runs in the library's CUDA kernels; without the built library this module raises.
 """
 from __future__ import annotations
 
@@ -18,7 +18,8 @@ from ._lib import (UA_BACKEND_2D, UA_BACKEND_AUTO, UA_BACKEND_SPLIT, UA_DT_BF16,
                    UA_DT_F16, UA_DT_F32, UA_DT_I8, UA_PATH_2D, UA_PATH_SPLIT)
 
 __all__ = ["unified_attention", "prepare", "PreparedAttention", "append_kv", "prepare_append",
-           "PreparedAppend", "rope_table", "plan", "device_status", "device_status_reset", "UaError", "BACKENDS", "library_path"]
+           "PreparedAppend", "rope_table", "plan", "device_status", "device_status_reset",
+           "UaError", "BACKENDS", "library_path"]
 
 BACKENDS = {"auto": UA_BACKEND_AUTO, "2d": UA_BACKEND_2D, "split": UA_BACKEND_SPLIT}
 _DTYPES = {torch.float16: UA_DT_F16, torch.bfloat16: UA_DT_BF16,
@@ -101,8 +102,8 @@ def unified_attention(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table
                       softcap: float = 0.0, window_left: int = -1, alibi_slopes=None,
                       qq_bias=None, sinks=None, kv_scale=None, k_scale_tok=None,
                       v_scale_tok=None, k_scale_blk=None, v_scale_blk=None, out=None,
-                      out_dtype=None, backend: str = "auto", num_splits: int = 0, workspace=None, stream=None,
-                      events=None):
+                      out_dtype=None, backend: str = "auto", num_splits: int = 0, workspace=None,
+                      stream=None, events=None):
     """Paged varlen GQA attention on the GPU; returns ``out`` [total_q, H_q, D].
 
     q [total_q, H_q, D] f16/bf16; k_cache, v_cache [num_blocks, block_size, H_kv, D]
@@ -196,7 +197,8 @@ def prepare(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *, max_s
             max_seqlen_k: int, scale: float | None = None, softcap: float = 0.0,
             window_left: int = -1, alibi_slopes=None, qq_bias=None, sinks=None, kv_scale=None,
             k_scale_tok=None, v_scale_tok=None, k_scale_blk=None, v_scale_blk=None, out=None,
-            out_dtype=None, backend: str = "auto", num_splits: int = 0, workspace=None, stream=None) -> PreparedAttention:
+            out_dtype=None, backend: str = "auto", num_splits: int = 0, workspace=None,
+            stream=None) -> PreparedAttention:
     """Validate and marshal a ``unified_attention`` call once (same arguments); the
     returned :class:`PreparedAttention` makes the call with new per-step tensors."""
     lib = _lib.load()

@@ -98,7 +98,8 @@ int append(const ua_append_t& a, cudaStream_t st) {
   for (const void* x : {a.k, a.v, a.q, static_cast<const void*>(a.q_out),
                         static_cast<const void*>(a.k_cache), static_cast<const void*>(a.v_cache)})
     if (!aligned(x, 16)) return UA_ERR_INVALID_ARG;
-  for (const void* x : {static_cast<const void*>(a.kv_scale), static_cast<const void*>(a.k_scale_tok),
+  for (const void* x : {static_cast<const void*>(a.kv_scale),
+                        static_cast<const void*>(a.k_scale_tok),
                         static_cast<const void*>(a.v_scale_tok),
                         static_cast<const void*>(a.k_scale_blk),
                         static_cast<const void*>(a.v_scale_blk),
@@ -214,8 +215,8 @@ int append(const ua_append_t& a, cudaStream_t st) {
   bool filled = false;
   if (blk) {
     const int bs = a.block_size;
-    threads = std::min(ua::kBlkThreads, ((a.head_dim / 16) * std::min(bs, ua::kBlkThreads) + 31) / 32 * 32);
-    threads = std::max(threads, 64);
+    const int lanes = (a.head_dim / 16) * std::min(bs, ua::kBlkThreads);
+    threads = std::max(64, std::min(ua::kBlkThreads, (lanes + 31) / 32 * 32));
     p.slot_per_seq = a.max_seqlen_q <= 1;
     const long long slots = p.slot_per_seq ? a.num_seqs : a.total_q / bs + 2LL * a.num_seqs;
     if (slots > INT_MAX) return UA_ERR_INVALID_ARG;
@@ -235,12 +236,13 @@ int append(const ua_append_t& a, cudaStream_t st) {
   if (grid > INT_MAX) return UA_ERR_INVALID_ARG;
   const unsigned gx = static_cast<unsigned>(grid);
   const bool bf = a.dtype == UA_DT_BF16;
-  cudaError_t err;
+  decltype(&launch<64, true>) run;
   switch (a.head_dim) {
-    case 64: err = bf ? launch<64, true>(p, kind, gx, threads, filled, st) : launch<64, false>(p, kind, gx, threads, filled, st); break;
-    case 128: err = bf ? launch<128, true>(p, kind, gx, threads, filled, st) : launch<128, false>(p, kind, gx, threads, filled, st); break;
-    default: err = bf ? launch<256, true>(p, kind, gx, threads, filled, st) : launch<256, false>(p, kind, gx, threads, filled, st); break;
+    case 64: run = bf ? launch<64, true> : launch<64, false>; break;
+    case 128: run = bf ? launch<128, true> : launch<128, false>; break;
+    default: run = bf ? launch<256, true> : launch<256, false>; break;
   }
+  const cudaError_t err = run(p, kind, gx, threads, filled, st);
   return err == cudaSuccess ? UA_OK : UA_ERR_CUDA;
 }
 

@@ -454,7 +454,8 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int t, int p0
       if (!ONLY_Q) {
         at.in_cache = static_cast<unsigned>(at.blk) < static_cast<unsigned>(p.num_blocks);
         if (!at.in_cache && lane == 0) atomicOr(p.status, DEV_BAD_BLOCK);
-        at.cache_row = (static_cast<size_t>(at.in_cache ? at.blk : 0) * p.block_size + at.slot) * p.hkv;
+        at.cache_row =
+            (static_cast<size_t>(at.in_cache ? at.blk : 0) * p.block_size + at.slot) * p.hkv;
       }
     }
     if (r == 0) {
@@ -473,7 +474,8 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int t, int p0
 // 4096 tokens, 76.7 against 67.4 us for 16384 video tokens into e4m3 with token scales).
 constexpr int kRowsMinBlocks = 6, kRowsPasses = 2;
 template <int D, bool BF, int KIND>
-__global__ void __launch_bounds__(128, kRowsMinBlocks) ua_append_rows_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(128, kRowsMinBlocks)
+    ua_append_rows_kernel(const __grid_constant__ AppendParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int groups = (p.passes + p.pass_group - 1) / p.pass_group;
@@ -481,7 +483,8 @@ __global__ void __launch_bounds__(128, kRowsMinBlocks) ua_append_rows_kernel(con
   const long long t = w / groups;
   if (t >= p.total_q) return;
   const int p0 = static_cast<int>(w % groups) * p.pass_group;
-  append_rows<D, BF, KIND, false, kRowsPasses>(p, static_cast<int>(t), p0, min(p0 + p.pass_group, p.passes));
+  append_rows<D, BF, KIND, false, kRowsPasses>(p, static_cast<int>(t), p0,
+                                               min(p0 + p.pass_group, p.passes));
 }
 
 // Block-scaled caches.  CTA x < slots * (hkv / heads_per_cta) owns one page that new tokens
@@ -525,7 +528,8 @@ __global__ void __launch_bounds__(kBlkThreads, MINB)
   const int bs = p.block_size;
   SeqOf sq;
   if (p.slot_per_seq)
-    sq = SeqOf{x, __ldg(p.cu_seqlens_q + x), __ldg(p.cu_seqlens_q + x + 1), __ldg(p.seq_lens_k + x)};
+    sq = SeqOf{x, __ldg(p.cu_seqlens_q + x), __ldg(p.cu_seqlens_q + x + 1),
+               __ldg(p.seq_lens_k + x)};
   else
     sq = seq_of(p.cu_seqlens_q, p.seq_lens_k, p.num_seqs, x,
                 [bs](int c0, int i) -> long long { return c0 / bs + 2LL * i; });

@@ -1,5 +1,5 @@
-// ua_decode_blk_pair.cu -- instantiations of the key-major decode tile kernel for block-scaled caches,
-// two kv-heads a CTA.
+// ua_decode_blk_pair.cu -- instantiations of the key-major decode tile kernel for block-scaled
+// caches, two kv-heads a CTA.
 #include "ua_decode.cuh"
 
 namespace ua {

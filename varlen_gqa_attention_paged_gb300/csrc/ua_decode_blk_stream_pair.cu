@@ -1,6 +1,5 @@
-// ua_decode_blk_stream_pair.cu -- instantiations of the key-major decode tile kernel for block-scaled
-// caches, an even share of
-// the keys of two kv-heads a CTA.
+// ua_decode_blk_stream_pair.cu -- instantiations of the key-major decode tile kernel for
+// block-scaled caches, an even share of the keys of two kv-heads a CTA.
 #include "ua_decode.cuh"
 
 namespace ua {

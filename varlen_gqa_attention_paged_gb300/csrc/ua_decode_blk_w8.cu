@@ -1,5 +1,5 @@
-// ua_decode_blk_w8.cu -- instantiations of the key-major decode tile kernel for block-scaled caches,
-// eight consumer warps.
+// ua_decode_blk_w8.cu -- instantiations of the key-major decode tile kernel for block-scaled
+// caches, eight consumer warps.
 #include "ua_decode.cuh"
 
 namespace ua {
