@@ -682,7 +682,8 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
       if constexpr (BLK != 0) {
         const int slot = (jb + n) % C::kScaleSlots;
         ok = pf_wait_warp(&sc_full[slot], ((jb + n) / C::kScaleSlots) & 1, abort_flag, p.status);
-        // with one S buffer its commit covers the P.V before; with two it covers P.V n - 2
+        // with one S buffer its commit covers the P.V before; with two it covers P.V n - 2, so
+        // that pv_done is in phase n - 1 or n where the wait for phase n - 1 is reached
         ok = ok && blk_softmax_tile<FEAT, D>(
                        brow, scales + slot, tS, tO, k0, need_mask, c, n >= 1, m_used, l,
                        [&]() -> bool {
@@ -834,11 +835,16 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
     }
 
     // ---- epilogue: O / l for one partition, or the partition's max / sum / O
-    // the last P.V (two S buffers: the tile's last pv_done phase; one: its only phase)
-    if (BLK != 0 && DB && ok && n_tiles > 1 && active)  // (not waited for in the walk)
-      ok = pf_wait_warp(pv_done(qt), n_tiles & 1, abort_flag, p.status);
-    if (ok && n_tiles > 0 && active)
-      ok = pf_wait_warp(pv_done(qt), DB ? (n_tiles - 1) & 1 : 0, abort_flag, p.status);
+    // the last P.V (two S buffers: the tile's last pv_done phase; one: its only phase).
+    // Block-scaled caches, which wait for P.V in the walk only where they rescale O, take the
+    // CTA's last commit: behind the last hand-over pv_done may already be two phases past the
+    // last one waited for, where its parity reads as not done.
+    if (ok && n_tiles > 0 && active) {
+      if (BLK != 0 && DB)
+        ok = pf_wait_warp(fin, 0, abort_flag, p.status) && !*abort_flag;
+      else
+        ok = pf_wait_warp(pv_done(qt), DB ? (n_tiles - 1) & 1 : 0, abort_flag, p.status);
+    }
     tc_fence_after();
     if constexpr (SW > 1) {
       if (ok && active) {  // the row sum over every column slice, through tensor memory

@@ -18,7 +18,8 @@
 // compute the next S and the previous P.V while the softmax warps work on tile j; S_{j+2}
 // overwrites P_j only after P.V_j, in issue order.  Each commit covers every earlier MMA
 // of the thread, so when S_j is ready P.V_{j-2} is done; the softmax rescales O (only
-// when a row's max grows by more than 2^8) after also waiting for P.V_{j-1}.
+// when a row's max grows by more than 2^8) after also waiting for P.V_{j-1} (its barrier is
+// then in phase j - 1 or j, so the parity names the phase).
 //
 // Shared memory: Q (64 KB) and a ring of five 32 KB slots.  A slot holds half of a K or V
 // tile (128 keys x 128 of the 256 columns); slots are filled in the order the MMA warp
@@ -796,9 +797,11 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
       if (lane == 0) mbar_arrive(&p_full[bb]);
     }
 
-    // ---- epilogue: P.V_{nt-2} and P.V_{nt-1} done, then O / l or the partition's state
-    if (ok && nt >= 2) ok = pf_wait_warp(pv_done, (nt - 2) & 1, abort_flag, p.status);
-    if (ok && nt >= 1) ok = pf_wait_warp(pv_done, (nt - 1) & 1, abort_flag, p.status);
+    // ---- epilogue: every P.V done, then O / l or the partition's state.  (The walk waits for a
+    // phase of pv_done only where it rescales O; behind the last hand-over the barrier may
+    // already be two phases past the last one waited for, where its parity reads as not done.
+    // The CTA's last commit has a barrier of its own.)
+    if (nt > 0) ok = ok && pf_wait_warp(fin, 0, abort_flag, p.status) && !*abort_flag;
     tc_fence_after();
     if constexpr (SW > 1) {  // the row sum over both halves (also after an abort)
       float* const lx = reinterpret_cast<float*>(xch);  // [SW][128]
