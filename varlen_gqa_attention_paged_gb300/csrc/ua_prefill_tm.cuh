@@ -65,9 +65,11 @@ struct PrefillTmCfg {
   static constexpr int kF8Tile = kBN * D;
   static constexpr int kF8Bytes = F8 ? 2 * kF8Tile : 0;
   static constexpr int kDeqWarps = F8 ? 4 : 0;
-  // SW > 1: each tile's row maxima of the SW warps of a row, exchanged through shared
-  // memory as bf16 values rounded up
-  static constexpr int kXchBytes = SW > 1 ? NQ * SW * 2 * 128 * 2 : 0;  // two tiles in flight
+  // SW > 1: a tile's row maxima of the SW warps of a row, exchanged through shared memory
+  // (as fp32: they may lie in the thousands, where a coarser type is off by whole units of the
+  // exponent, and f16 weights of 2^-16 and less lose their bits)
+  // Four warps: two tiles in flight; two warps swap places every tile instead.
+  static constexpr int kXchBytes = SW == 4 ? 2 * SW * 128 * 4 : SW == 2 ? SW * 128 * 4 : 0;
   // K and V ring depths: as many tiles as fit beside Q (K gets the odd one, at most 4 each)
   static constexpr int kSlots =
       (227 * 1024 - 1024 - kBarBytes - NQ * kQBytes - kF8Bytes - kXchBytes) / kTileBytes;
@@ -88,6 +90,7 @@ struct PrefillTmCfg {
   static constexpr int kThreads = 32 * kSoftmaxWarps + 96 + 32 * kDeqWarps;
   static_assert(D <= 128, "two 128-key K/V rings must fit");
   static_assert(NQ * kTmemStride <= kTmemCols, "tensor memory budget");
+  static_assert(SW == 1 || NQ == 1, "the row-max exchange goes with the two S buffers of one tile");
   // (16 bytes of static shared memory beside it)
   static_assert(kSmemBytes + 16 <= 227 * 1024, "shared memory budget");
   static_assert(BLK == 0 || (F8 && SW == 1), "block scales go with 8-bit codes, whole rows a thread");
@@ -95,7 +98,7 @@ struct PrefillTmCfg {
   // the barriers, flags and row-exchange barriers end before the group scales' barriers (byte 384)
   static constexpr int kBarsEnd =
       8 * (2 + 2 * kRingK + 2 * kRingV + (F8 ? 5 : 0) + 3 * NQ + 2) + 4 * (2 * NQ + 2) +
-      (SW > 1 ? NQ * 64 : 0);
+      (SW > 1 ? 64 : 0);
   static_assert(BLK == 0 || kBarsEnd <= 48 * 8, "barrier layout");
   static_assert(kRingK >= 2 && kRingV >= 2, "at least double-buffered K and V");
   static_assert(!F8 || D == 64 || D == 128, "fp8 caches: head_dim 64 or 128");
@@ -144,10 +147,10 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(tile_bars + 3 * NQ + 2);
   // [NQ][2]: walk step + 1 of the tile's P when its low part matters
   int* const lo_flag = reinterpret_cast<int*>(tmem_holder + 1);
-  // SW > 1: per (q tile, lane quarter) a barrier for the tile's row-max exchange and one for
-  // the final row-sum exchange ([NQ][4][2]), and the exchanged maxima
+  // SW > 1: per lane quarter a barrier for the tile's row-max exchange and one for the final
+  // row-sum exchange ([4][2]), and the exchanged maxima
   uint64_t* const xch_bars = reinterpret_cast<uint64_t*>(lo_flag + 2 * NQ + 1);  // 8-byte aligned
-  uint16_t* const xch = reinterpret_cast<uint16_t*>(bars) + C::kBarBytes / 2;  // [NQ][2][SW][128]
+  float* const xch = reinterpret_cast<float*>(bars) + C::kBarBytes / 4;  // [2][4][128], or [2][128]
   // block-scaled caches: the group scales of a tile (slot j mod kScaleSlots) and their barriers
   uint64_t* const sc_full = bars + 48;
   static_assert(C::kScaleSlots <= 8 && 56 * 8 <= C::kBarBytes);
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
       mbar_init(v8_empty, C::kDeqWarps);
     }
     if constexpr (SW > 1)
-      for (int i = 0; i < NQ * 4 * 2; ++i) mbar_init(&xch_bars[i], 32 * SW);
+      for (int i = 0; i < 4 * 2; ++i) mbar_init(&xch_bars[i], 32 * SW);
     for (int i = 0; i < C::kScaleSlots; ++i) mbar_init(&sc_full[i], C::kDeqWarps);
     mbar_init(s_full_b(1), 1);
     mbar_init(p_full_b(1), 4 * SW);
@@ -582,16 +585,15 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
     // SW warps share a tensor-memory lane quarter: warp `half` takes S columns
     // [half BN / SW, (half + 1) BN / SW) of every key tile and O columns
     // [half D / SW, (half + 1) D / SW).  Once per tile their row maxima meet in shared
-    // memory, each rounded up to bf16, and every warp of the row takes the largest: the
-    // same running max in every warp, never below the true one.  Their row sums meet at
+    // memory, and every warp of the row takes the largest.  Their row sums meet at
     // the end through SW columns of the tile's S/P region, free after its last P.V.
     constexpr int kCols = BN / SW, kOCols = D / SW;
     const int qt = warp / (4 * SW);                        // q tile of this warp
     const int quad = warp & 3;                             // its tensor-memory lane quarter
     const int half = (warp % (4 * SW)) >> 2;               // its column slice
     const int r = 32 * quad + lane;                        // row within the q tile
-    uint64_t* const xbar = xch_bars + 2 * (4 * qt + quad);  // [0]: row max, [1]: row sum
-    uint16_t* const xrow = xch + (qt * 2 * SW) * 128 + r;   // + (slot * SW + h) * 128
+    uint64_t* const xbar = xch_bars + 2 * quad;  // [0]: row max, [1]: row sum
+    float* const xrow = xch + r;                 // + (slot * SW + half) * 128
     int jb, je;
     tile_walk(qt, jb, je);
     const int n_tiles = je - jb;
@@ -739,19 +741,24 @@ __global__ void __launch_bounds__(PrefillTmCfg<D, NQ, F8, SW, BLK>::kThreads, 1)
       if (rewrite) tmem_st_wait();
       float mx = fmaxf(mx0, mx1) * c;  // row max in log2 units (-inf stays -inf)
       if constexpr (SW > 1) {
-        // the row's other column slices: every lane arrives once its value is written.  Two
-        // slots: a warp writes tile n + 2's slot only after its S wait, which follows the
-        // P.V of tile n, which waited for every warp's P of tile n, written after the reads.
-        const uint32_t u = __float_as_uint(mx);
-        uint16_t* const slot = xrow + (n & 1) * SW * 128;
-        slot[half * 128] = static_cast<uint16_t>(
-            ((u & 0xFFFFu) == 0u || (u >> 31)) ? (u >> 16) : (u >> 16) + 1u);  // round up
-        mbar_arrive(&xbar[0]);
-        if (!pf_wait_warp(&xbar[0], n & 1, abort_flag, p.status)) { ok = false; break; }
-        mx = -INFINITY;
+        // the row's other column slices: every lane arrives once its value is written
+        if constexpr (SW == 2) {
+          // the slices swap places every tile, so that a warp writes over the value that it
+          // alone read
+          xrow[((half ^ n) & 1) * 128] = mx;
+          mbar_arrive(&xbar[0]);
+          if (!pf_wait_warp(&xbar[0], n & 1, abort_flag, p.status)) { ok = false; break; }
+          mx = fmaxf(mx, xrow[((half ^ n ^ 1) & 1) * 128]);
+        } else {
+          // two slots: a warp writes tile n + 2's slot only after its S wait, which follows the
+          // P.V of tile n, which waited for every warp's P of tile n, written after the reads
+          float* const slot = xrow + (n & 1) * SW * 128;
+          slot[half * 128] = mx;
+          mbar_arrive(&xbar[0]);
+          if (!pf_wait_warp(&xbar[0], n & 1, abort_flag, p.status)) { ok = false; break; }
 #pragma unroll
-        for (int hh = 0; hh < SW; ++hh)
-          mx = fmaxf(mx, __uint_as_float(static_cast<uint32_t>(slot[hh * 128]) << 16));
+          for (int hh = 1; hh < SW; ++hh) mx = fmaxf(mx, slot[(half + hh) % SW * 128]);
+        }
       }
       // ---- running max, used lazily: O and l are rescaled only when the max grows by
       // more than 8 in log2 units (P stays <= 256, far inside the fp32 and P ranges)

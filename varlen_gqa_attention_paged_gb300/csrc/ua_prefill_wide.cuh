@@ -74,9 +74,8 @@ struct PrefillWideCfg {
   // them: 1112 us for two chunks of 4096 behind 4096, 24/4 heads, e4m3, against 1104, and with a
   // softcap 1444 against 1409; producer 0, whose copies then came late, 1183 us.)
   static constexpr int kScaleSlots = BLK ? 4 : 0;
-  // SW > 1: row maxima of the SW halves as bf16 rounded up, two tiles in flight (at the end
-  // the same bytes hold the row sums of the halves as fp32)
-  static constexpr int kXchBytes = SW > 1 ? 2 * SW * 128 * 2 : 0;
+  // SW > 1: a tile's row maxima of the SW halves (at the end the row sums), fp32
+  static constexpr int kXchBytes = SW > 1 ? SW * 128 * 4 : 0;
   static constexpr int kSoft = 4 * SW;              // softmax warps
   static constexpr int kSmemBytes = 1024 + kQBytes + kSlots * kSlotBytes + kStage * kStageBytes +
                                     kBarBytes + kScaleSlots * 96 + kXchBytes;
@@ -149,7 +148,7 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
   uint64_t* const sc_go = sc_full + C::kScaleSlots;  // producer 0 reached the tile
   static_assert(40 + 2 * C::kScaleSlots <= 50);
   uint64_t* const xch_bars = bars + 50;  // [4]: SW > 1, the row-max exchange of a lane quarter
-  uint16_t* const xch = reinterpret_cast<uint16_t*>(scales + C::kScaleSlots);  // [2][SW][128]
+  float* const xch = reinterpret_cast<float*>(scales + C::kScaleSlots);  // [SW][128]
   __shared__ int s_abort;
   __shared__ int s_last[C::kProducers];  // last item each producer warp issued
 
@@ -539,7 +538,7 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
     constexpr int kCols = BN / SW, kOCols = D / SW;
     const int quad = warp & 3, half = warp >> 2;  // lane quarter, column slice
     const int r = 32 * quad + lane;
-    uint16_t* const xrow = xch + r;  // + (slot * SW + half) * 128
+    float* const xrow = xch + r;  // + half * 128
     // the row's token within the tile and head within the group (rows token * G + head)
     const int tl = r / G;
     const bool rv = r < TQ * G && tl <= t_last - t_first && q0 + t_first + tl < p.total_q;
@@ -681,17 +680,12 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
       if (rewrite) tmem_st_wait();
       float mx = BLK != 0 ? mx0 : fmaxf(mx0, mx1) * c;
       if constexpr (SW > 1) {
-        // the row's other half: every lane arrives once its value is written.  Two slots: a
-        // warp writes tile j + 2's slot only after its S wait, which follows the P.V of tile
-        // j, which waited for every warp's P of tile j, written after the reads.
-        const uint32_t u = __float_as_uint(mx);
-        uint16_t* const slot = xrow + bb * SW * 128;
-        slot[half * 128] = static_cast<uint16_t>(
-            ((u & 0xFFFFu) == 0u || (u >> 31)) ? (u >> 16) : (u >> 16) + 1u);  // round up
+        // the row's other half: every lane arrives once its value is written.  The halves swap
+        // places every tile, so that a warp writes over the value that it alone read.
+        xrow[((half ^ j) & 1) * 128] = mx;
         mbar_arrive(&xch_bars[quad]);
         if (!pf_wait_warp(&xch_bars[quad], j & 1, abort_flag, p.status)) { ok = false; break; }
-        mx = fmaxf(__uint_as_float(static_cast<uint32_t>(slot[0]) << 16),
-                   __uint_as_float(static_cast<uint32_t>(slot[128]) << 16));
+        mx = fmaxf(mx, xrow[((half ^ j ^ 1) & 1) * 128]);
       }
       float alpha = 1.f;
       const bool grow = mx > m_used + 8.f || (m_used == -INFINITY && mx > -INFINITY);
@@ -804,11 +798,10 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
     if (nt > 0) ok = ok && pf_wait_warp(fin, 0, abort_flag, p.status) && !*abort_flag;
     tc_fence_after();
     if constexpr (SW > 1) {  // the row sum over both halves (also after an abort)
-      float* const lx = reinterpret_cast<float*>(xch);  // [SW][128]
-      named_bar_sync(3, 32 * C::kSoft);                 // the maxima in these bytes are read
-      lx[half * 128 + r] = l;
+      named_bar_sync(3, 32 * C::kSoft);  // the last tile's maxima are read
+      xrow[half * 128] = l;
       named_bar_sync(3, 32 * C::kSoft);
-      l = lx[r] + lx[128 + r];
+      l = xrow[0] + xrow[128];
     }
     if (BLK != 0 && sink) v_mul = late_sink(__ldg(p.sinks + h) * kLog2e, m_used, l);
     if (ok) {
