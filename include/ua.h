@@ -348,7 +348,7 @@ typedef struct {
  * reached by two sequences of one call, or twice by one, is the caller's error.
  *
  * A token whose cache position is negative (kv_len < q_len) is skipped, as are rows of k, v
- * and q past cu_seqlens_q[num_seqs].  A block id outside [0, num_blocks) or past the table's
+ * and q past cu_seqlens_q[num_seqs], and a sequence's tokens from total_q on.  A block id outside [0, num_blocks) or past the table's
  * row is not written; a position outside [0, max_position) skips its token, queries included;
  * both raise UA_ERR_DEVICE_CHECK in the device status word.
  *

@@ -542,11 +542,13 @@ __global__ void __launch_bounds__(kBlkThreads, MINB)
   const int pg = max(ctx, 0) / bs + seg;
   if (static_cast<long long>(pg) * bs >= sq.kv_len) return;  // idle slot
   const int base = pg * bs;
+  const int t0 = sq.q0 + base - ctx;         // token of the page's slot 0
   const int s0 = max(ctx - base, 0);        // tokens the page held before
-  const int s1 = min(sq.kv_len - base, bs);  // its slots in use now
+  // its slots in use now (never a token past the inputs, should cu_seqlens_q end behind them)
+  const int s1 = min(min(sq.kv_len - base, bs), p.total_q - t0);
+  if (s1 <= s0) return;
   const int row0 = threadIdx.x / LPR, rows = blockDim.x / LPR;
   const LaneChunks<D> ch(threadIdx.x % LPR, p.rot_dim);
-  const int t0 = sq.q0 + base - ctx;         // token of the page's slot 0
   uint4 k0, k1, v0, v1;  // a new row's chunks as read; codes held before in .x, .y
   auto fetch_new = [&](int r, int h) {
     const long long t = t0 + r;
