@@ -606,12 +606,26 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP, STREAM>::kThreads,
       m_run[e] = sink ? __ldg(p.sinks + rh[e]) * kLog2e : -INFINITY;
       l_run[e] = (sink && gq == 0) ? 1.f : 0.f;
     }
-    float vbias[4] = {0.f, 0.f, 0.f, 0.f};  // int8: 128 2^-24 sum(w) of the rows
+    float vbias[4] = {0.f, 0.f, 0.f, 0.f};  // int8: 128 2^-24 sum(w) still in the rows' O
     float ot[C::kMT][4];
 #pragma unroll
     for (int m = 0; m < C::kMT; ++m)
 #pragma unroll
       for (int e = 0; e < 4; ++e) ot[m][e] = 0.f;
+
+    // The codes' offset comes off O every kI8Tiles tiles (64 keys of a warp).  The sums of weights
+    // times 128 grow with the walk, O itself as its root, and the tensor cores cut what they add
+    // to off at a sum's last bit: taken off once at the end, O was off by 3 % of its rms after
+    // 131072 keys and by 1e-3 after 8192; so, by less than the weights' rounding to f16.
+    constexpr int kI8Tiles = 4;
+    auto take_bias = [&]() {
+#pragma unroll
+      for (int m = 0; m < C::kMT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ot[m][e] -= vbias[e & 1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) vbias[e] = 0.f;
+    };
 
     // Cache slots at or past kv_len in the sequence's last page hold no key and may hold
     // anything (NaN included): their P is 0, and their V values are zeroed before P.V so
@@ -983,13 +997,15 @@ __global__ void __launch_bounds__(DecCfg<D, KV, W, HP, STREAM>::kThreads,
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
+      if (kI8 && (t % kI8Tiles) == kI8Tiles - 1) take_bias();
     }
 
     if constexpr (kI8) {  // V's operands were (code + 128) 2^-24
+      take_bias();
 #pragma unroll
       for (int m = 0; m < C::kMT; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ot[m][e] = (ot[m][e] - vbias[e & 1]) * (1.f / kI8Unit);
+        for (int e = 0; e < 4; ++e) ot[m][e] *= 1.f / kI8Unit;
     }
 
     // Row sums: add up the lanes of a row (gq = 0..7).
