@@ -563,8 +563,6 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
   p.group = hq / hkv;
   p.qq_stride = sh->qq_bias_stride;
   p.window_left = window_left < 0 ? -1 : window_left;
-  p.n_part = pl.n_part;
-  p.slot_per_seq = pl.slot_per_seq;
   p.q_dtype = sh->q_dtype;
   p.out_dtype = sh->out_dtype;
   p.scale = scale;
@@ -585,7 +583,6 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
     if (!maps) {
       make_plan(sh, block_size, hq, hkv, d, window_left, kv_dtype, backend, num_sms, false, true,
                 true, &pl);
-      p.n_part = pl.n_part;
     }
     pp.tq = 128 / group;
   }
@@ -606,8 +603,10 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
   if (dec_kernel && !tma) {
     make_plan(sh, block_size, hq, hkv, d, window_left, kv_dtype, backend, num_sms, false, false,
               true, &pl);
-    p.n_part = pl.n_part;
   }
+  // what the kernels take from the plan, now that it is the last one
+  p.n_part = pl.n_part;
+  p.slot_per_seq = pl.slot_per_seq;
   // per-token fp8 scales: the decode tile and the tensor-memory kernels read them (the tile
   // kernel, for decode batches of 9 to 16 rows a kv-head or head_dim 256, and for pages
   // not a multiple of 16, does not)
