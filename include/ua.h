@@ -405,6 +405,14 @@ int ua_device_status(void* stream, int* status);
 /* Clears the device check word (enqueued on `stream`). */
 int ua_device_status_reset(void* stream);
 
+/*
+ * sizeof(ua_shape_t) in the loaded library.  The struct grows as calls learn new options (its
+ * per-block scales are such), and a call reads all of it: a caller built against another header
+ * compares this with its own sizeof(ua_shape_t) before its first call, and makes none when they
+ * differ.  UA_VERSION stays as long as every older member keeps its place and meaning.
+ */
+size_t ua_shape_bytes(void);
+
 /* Static text for a ua_status_t code. */
 const char* ua_status_string(int status);
 

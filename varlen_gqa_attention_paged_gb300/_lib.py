@@ -19,9 +19,9 @@ UA_BACKEND_AUTO, UA_BACKEND_2D, UA_BACKEND_SPLIT = 0, 1, 2
 UA_PATH_2D, UA_PATH_SPLIT = 1, 2
 
 # every symbol include/ua.h declares
-EXPORTS = ("ua_unified_attention", "ua_unified_attention_call",
-           "ua_unified_attention_noalloc", "ua_append_kv", "ua_plan", "ua_workspace_bytes", "ua_device_status", "ua_device_status_reset",
-           "ua_status_string", "ua_version")
+EXPORTS = ("ua_unified_attention", "ua_unified_attention_call", "ua_unified_attention_noalloc",
+           "ua_append_kv", "ua_plan", "ua_workspace_bytes", "ua_device_status",
+           "ua_device_status_reset", "ua_shape_bytes", "ua_status_string", "ua_version")
 
 
 class UaShape(ctypes.Structure):
@@ -135,5 +135,19 @@ def load():
         lib.ua_status_string.restype = ctypes.c_char_p
         lib.ua_version.argtypes = []
         lib.ua_version.restype = ctypes.c_int
+        _check_layout(lib)
         _LIB = lib
         return lib
+
+
+def _check_layout(lib):
+    """Raises if the library was built from another include/ua.h than these declarations."""
+    try:
+        size = lib.ua_shape_bytes
+    except AttributeError:
+        size = None
+    if size is not None:
+        size.argtypes, size.restype = [], ctypes.c_size_t
+    if size is None or size() != ctypes.sizeof(UaShape):
+        raise RuntimeError(f"{LIB_PATH} was built from another version of include/ua.h: build it "
+                           "again (varlen_gqa_attention_paged_gb300.build.build())")

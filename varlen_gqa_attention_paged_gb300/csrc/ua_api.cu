@@ -800,7 +800,9 @@ const char* ua_status_string(int status) {
     case UA_ERR_UNSUPPORTED: return "unsupported combination";
     case UA_ERR_CUDA: return "CUDA runtime error";
     case UA_ERR_WORKSPACE: return "workspace too small";
-    case UA_ERR_DEVICE_CHECK: return "device check failed: block id outside the cache";
+    case UA_ERR_DEVICE_CHECK:
+      return "device check failed: block id outside the cache, position outside the rotation "
+             "table, or q_len above max_seqlen_q";
     case UA_ERR_TIMEOUT: return "device wait timed out";
     case UA_ERR_SCRATCH_LIMIT:
       return "call needs more scratch than the fixed array of ua_unified_attention_noalloc";
@@ -809,5 +811,7 @@ const char* ua_status_string(int status) {
 }
 
 int ua_version(void) { return UA_VERSION; }
+
+size_t ua_shape_bytes(void) { return sizeof(ua_shape_t); }
 
 }  // extern "C"
