@@ -154,9 +154,9 @@ class PreparedAttention:
 
     Built by :func:`prepare`.  Calling it passes new per-step tensors -- ``q``,
     ``cu_seqlens_q``, ``seq_lens_k``, ``block_table``, ``out`` -- each of the prepared one's
-    shape, dtype and device (checked); any left out keeps the prepared tensor.  The caches,
-    the score features, the scales and the host sizes (``max_seqlen_q``/``max_seqlen_k``)
-    stay as prepared.  Returns ``out``.
+    shape, dtype and device (checked; if one is refused, none is taken); any left out, and
+    ``stream``, keeps what was passed last.  The caches, the score features, the scales and the
+    host sizes (``max_seqlen_q``/``max_seqlen_k``) stay as prepared.  Returns ``out``.
     """
 
     def __init__(self, lib, call, tensors, stream):
@@ -168,23 +168,29 @@ class PreparedAttention:
         self._stream = stream
         self.out = tensors["out"]
 
-    def _take(self, name, t):
-        if (t.shape, t.dtype, t.device) != self._meta[name] or not t.is_contiguous():
-            raise ValueError(f"{name}: shape, dtype, device or layout differs from the "
-                             "prepared call")
-        setattr(self._call, name, t.data_ptr())
-        self._now[name] = (t, t.data_ptr(), t.shape)
+    def _take(self, new):
+        for name, t in new:
+            if (t.shape, t.dtype, t.device) != self._meta[name] or not t.is_contiguous():
+                raise ValueError(f"{name}: shape, dtype, device or layout differs from the "
+                                 "prepared call")
+        for name, t in new:
+            setattr(self._call, name, t.data_ptr())
+            self._now[name] = (t, t.data_ptr(), t.shape)
 
     def __call__(self, q=None, cu_seqlens_q=None, seq_lens_k=None, block_table=None, out=None,
                  stream=None):
         now = self._now
+        new = None
         for name, t in (("q", q), ("cu_seqlens_q", cu_seqlens_q), ("seq_lens_k", seq_lens_k),
                         ("block_table", block_table), ("out", out)):
             if t is None:
                 continue
             kept, ptr, shape = now[name]
             if t is not kept or t.data_ptr() != ptr or t.shape != shape or not t.is_contiguous():
-                self._take(name, t)
+                new = new or []
+                new.append((name, t))
+        if new:
+            self._take(new)
         if stream is not None:
             self._stream = stream
         rc = self._lib.ua_unified_attention_call(self._ref, self._stream.cuda_stream)
@@ -384,8 +390,9 @@ class PreparedAppend:
 
     Built by :func:`prepare_append`.  Calling it passes the step's tensors -- ``k``, ``v``,
     ``q``, ``q_out``, ``cu_seqlens_q``, ``seq_lens_k``, ``block_table``, ``positions`` -- each
-    of the prepared one's shape, strides, dtype and device (checked); any left out keeps the
-    prepared tensor.  The caches, the table and the scales stay as prepared.  Returns ``q_out``.
+    of the prepared one's shape, strides, dtype and device (checked; if one is refused, none is
+    taken); any left out, and ``stream``, keeps what was passed last.  The caches, the table and
+    the scales stay as prepared.  Returns ``q_out``.
     """
 
     def __init__(self, lib, call, keep, static, stream):
@@ -395,31 +402,39 @@ class PreparedAppend:
         self._static = static
         self._meta = {n: (t.shape, t.stride(), t.dtype, t.device)
                       for n, t in keep.items() if t is not None}
-        # the tensors passed last: one passed again, as most are, costs three comparisons
-        self._now = {n: (None, 0, None) if t is None else (t, t.data_ptr(), t.shape)
-                     for n, t in keep.items()}
+        # the tensors passed last: one passed again, as most are, costs four comparisons
+        self._now = {n: (None, 0, None, None) if t is None else
+                     (t, t.data_ptr(), t.shape, t.stride()) for n, t in keep.items()}
         self._device = keep["k"].device.index
         self._stream = stream
 
-    def _take(self, name, t):
-        if (t.shape, t.stride(), t.dtype, t.device) != self._meta.get(name):
-            raise ValueError(f"{name}: shape, strides, dtype or device differs from the "
-                             "prepared call")
-        setattr(self._call, name, t.data_ptr())
-        self._now[name] = (t, t.data_ptr(), t.shape)
+    def _take(self, new):
+        for name, t in new:
+            if (t.shape, t.stride(), t.dtype, t.device) != self._meta.get(name):
+                raise ValueError(f"{name}: shape, strides, dtype or device differs from the "
+                                 "prepared call")
+        for name, t in new:
+            setattr(self._call, name, t.data_ptr())
+            self._now[name] = (t, t.data_ptr(), t.shape, t.stride())
 
     def __call__(self, k=None, v=None, q=None, q_out=None, cu_seqlens_q=None, seq_lens_k=None,
                  block_table=None, positions=None, stream=None):
         now = self._now
+        new = None
         for name, t in (("k", k), ("v", v), ("q", q), ("q_out", q_out),
                         ("cu_seqlens_q", cu_seqlens_q), ("seq_lens_k", seq_lens_k),
                         ("block_table", block_table), ("positions", positions)):
             if t is None:
                 continue
-            kept, ptr, shape = now[name]
-            if t is not kept or t.data_ptr() != ptr or t.shape != shape:
-                self._take(name, t)
-        handle = (self._stream if stream is None else stream).cuda_stream
+            kept, ptr, shape, stride = now[name]
+            if t is not kept or t.data_ptr() != ptr or t.shape != shape or t.stride() != stride:
+                new = new or []
+                new.append((name, t))
+        if new:
+            self._take(new)
+        if stream is not None:
+            self._stream = stream
+        handle = self._stream.cuda_stream
         if torch.cuda.current_device() == self._device:
             rc = self._lib.ua_append_kv(self._ref, handle)
         else:
