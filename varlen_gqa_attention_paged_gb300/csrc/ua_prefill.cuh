@@ -173,21 +173,21 @@ __device__ __forceinline__ void blk_transform32(const BlkRow& w, float2 kf, int 
   }
 }
 
-// The same, and the larger of mx and their maximum in log2 units with the V scales.
-template <bool FEAT>
+// The same with score features, and the larger of mx and their maximum in log2 units with the V
+// scales.
 __device__ __forceinline__ float blk_scores32(const BlkRow& w, const GroupScales* gs, int grp,
-                                              int key0, bool need_mask, float c, uint32_t (&r)[32],
+                                              int key0, bool need_mask, uint32_t (&r)[32],
                                               float mx) {
   const float2 kf = *reinterpret_cast<const float2*>(gs->kf + grp);
   const float2 vl = *reinterpret_cast<const float2*>(gs->vl + grp);
-  blk_transform32<FEAT>(w, kf, key0, need_mask, r);
+  blk_transform32<true>(w, kf, key0, need_mask, r);
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     float mg = -INFINITY;
 #pragma unroll
     for (int e = 16 * q; e < 16 * q + 16; e += 2)
       mg = fmax3(mg, __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
-    mx = fmaxf(mx, fmaf(mg, FEAT ? c : c * (q ? kf.y : kf.x), q ? vl.y : vl.x));
+    mx = fmaxf(mx, fmaf(mg, kLog2e, q ? vl.y : vl.x));
   }
   return mx;
 }

@@ -113,6 +113,7 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
     ua_prefill_wide_kernel(const __grid_constant__ PrefillParams pp) {
   using C = PrefillWideCfg<D, F8, BLK, SW>;
   static_assert(SW == 1 || !BF16, "P's low part is agreed on by four warps");
+  static_assert(SW == 1 || (BLK != 0 && FEAT), "two warps a row: block scales, score features");
   constexpr int BN = C::kBN;
   constexpr int NS = C::kSlots;
   constexpr int kMma = C::kSoft + C::kProducers;
@@ -625,25 +626,19 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
       const bool rewrite = FEAT || need_mask;
       float mx0 = -INFINITY, mx1 = -INFINITY;
       const GroupScales* const gs = scales + j % (BLK ? C::kScaleSlots : 1);
-      if constexpr (BLK != 0) {
+      if constexpr (BLK != 0) {  // (two warps a row, with score features: every tile rewrites)
         if (!pf_wait_warp(&sc_full[j % C::kScaleSlots], (j / C::kScaleSlots) & 1, abort_flag,
                           p.status)) {
           ok = false;
           break;
         }
-        constexpr bool k64 = !FEAT && kCols >= 64;
 #pragma unroll 1
-        for (int c0 = half * kCols; c0 < (half + 1) * kCols; c0 += k64 ? 64 : 32) {
-          uint32_t ra[32], rb[32];
+        for (int c0 = half * kCols; c0 < (half + 1) * kCols; c0 += 32) {
+          uint32_t ra[32];
           tmem_ld32(tS + c0, ra);
-          if constexpr (k64) tmem_ld32(tS + c0 + 32, rb);
           tmem_ld_wait();
-          mx0 = blk_scores32<FEAT>(brow, gs, c0 / 16, k0 + c0, need_mask, c, ra, mx0);
-          if (rewrite) tmem_st32(tS + c0, ra);
-          if constexpr (k64) {
-            mx0 = blk_scores32<FEAT>(brow, gs, c0 / 16 + 2, k0 + c0 + 32, need_mask, c, rb, mx0);
-            if (rewrite) tmem_st32(tS + c0 + 32, rb);
-          }
+          mx0 = blk_scores32(brow, gs, c0 / 16, k0 + c0, need_mask, ra, mx0);
+          tmem_st32(tS + c0, ra);
         }
       } else {
 #pragma unroll 1
@@ -725,7 +720,8 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
 
       // ---- pass 2: P = 2^(c s - m) over S, 32 keys at a time (16 columns of high part,
       // then, when the tile needs it, 16 of bf16 remainder)
-      float2 cc = make_float2(c, c), mm = make_float2(-m_use, -m_use);
+      const float2 cc = make_float2(c, c);
+      float2 mm = make_float2(-m_use, -m_use);
       float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
       float lacc = 0.f;  // block-scaled: the sum of w / vs
 #pragma unroll 1
@@ -736,9 +732,8 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
         float xv[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) xv[e] = __uint_as_float(rr[e]);
-        float2 kf2, vl2, vi2;  // block-scaled: the two groups' scales
+        float2 vl2, vi2;  // block-scaled: the two groups' V scales (K's are in the scores)
         if constexpr (BLK != 0) {
-          kf2 = *reinterpret_cast<const float2*>(gs->kf + c0 / 16);
           vl2 = *reinterpret_cast<const float2*>(gs->vl + c0 / 16);
           vi2 = *reinterpret_cast<const float2*>(gs->vi + c0 / 16);
         }
@@ -746,9 +741,7 @@ __global__ void __launch_bounds__(PrefillWideCfg<D, F8, BLK, SW>::kThreads, 1)
         for (int e = 0; e < 32; e += 4) {
           if constexpr (BLK != 0) {
             if (e % 16 == 0) {
-              const float f = FEAT ? c : c * (e ? kf2.y : kf2.x);
               const float o = (e ? vl2.y : vl2.x) - m_use;
-              cc = make_float2(f, f);
               mm = make_float2(o, o);
               acc0 = acc1 = make_float2(0.f, 0.f);
             }
