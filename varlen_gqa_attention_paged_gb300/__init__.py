@@ -406,6 +406,7 @@ class PreparedAppend:
         self._now = {n: (None, 0, None, None) if t is None else
                      (t, t.data_ptr(), t.shape, t.stride()) for n, t in keep.items()}
         self._device = keep["k"].device.index
+        self._one_device = torch.cuda.device_count() == 1
         self._stream = stream
 
     def _take(self, new):
@@ -435,7 +436,7 @@ class PreparedAppend:
         if stream is not None:
             self._stream = stream
         handle = self._stream.cuda_stream
-        if torch.cuda.current_device() == self._device:
+        if self._one_device or torch.cuda.current_device() == self._device:
             rc = self._lib.ua_append_kv(self._ref, handle)
         else:
             with torch.cuda.device(self._device):
