@@ -49,6 +49,17 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _new(shape, dtype, device, stream):
+    """A result for a call on `stream` to write: the current stream's, as any new tensor, and (if
+    `stream` is another) not handed out again before that is done with it."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None and stream.cuda_stream != torch.cuda.current_stream(device).cuda_stream:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+        t.record_stream(stream)
+    return t
+
+
 def _shape(q, k_cache, block_table, cu_seqlens_q, max_seqlen_q, max_seqlen_k, qq_bias,
            out_dtype_code, num_splits, workspace, events, k_scale_tok=None, v_scale_tok=None,
            k_scale_blk=None, v_scale_blk=None):
@@ -131,7 +142,7 @@ def unified_attention(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((total_q, hq, d), dtype=out_dtype or q.dtype, device=q.device)
+        out = _new((total_q, hq, d), out_dtype or q.dtype, q.device, stream)
     if stream is None:
         stream = torch.cuda.current_stream(q.device)
     sh = _shape(q, k_cache, block_table, cu_seqlens_q, max_seqlen_q, max_seqlen_k, qq_bias,
@@ -223,7 +234,7 @@ def prepare(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *, max_s
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((total_q, hq, d), dtype=out_dtype or q.dtype, device=q.device)
+        out = _new((total_q, hq, d), out_dtype or q.dtype, q.device, stream)
     if stream is None:
         stream = torch.cuda.current_stream(q.device)
     sh = _shape(q, k_cache, block_table, cu_seqlens_q, max_seqlen_q, max_seqlen_k, qq_bias,
@@ -276,7 +287,7 @@ def _rows3(name, t, total_q, d, dtype, device):
 
 def _append_call(k, v, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, max_seqlen_q,
                  q, q_out, cos_sin, positions, axis_of, interleaved, kv_scale, k_scale_tok,
-                 v_scale_tok, k_scale_blk, v_scale_blk):
+                 v_scale_tok, k_scale_blk, v_scale_blk, stream):
     """Checks the tensors of an append_kv call; returns its UaAppend and what it points at."""
     if k.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("k must be [total_q, H_kv, D] and k_cache [blocks, block_size, H_kv, D]")
@@ -307,7 +318,7 @@ def _append_call(k, v, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, 
     if q is not None:
         _rows3("q", q, total_q, d, k.dtype, dev)
         if q_out is None:
-            q_out = torch.empty(tuple(q.shape), dtype=q.dtype, device=dev)
+            q_out = _new(tuple(q.shape), q.dtype, dev, stream)
         _rows3("q_out", q_out, total_q, d, k.dtype, dev)
         if q_out.shape != q.shape:
             raise ValueError("q and q_out disagree on shape")
@@ -457,7 +468,7 @@ def prepare_append(k, v, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table
     call, keep, static = _append_call(
         k, v, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, max_seqlen_q, q, q_out,
         cos_sin, positions, axis_of, interleaved, kv_scale, k_scale_tok, v_scale_tok,
-        k_scale_blk, v_scale_blk)
+        k_scale_blk, v_scale_blk, stream)
     if stream is None:
         stream = torch.cuda.current_stream(k.device)
     return PreparedAppend(lib, call, keep, static, stream)
@@ -492,7 +503,7 @@ def append_kv(k, v, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *,
     call, keep, _static = _append_call(
         k, v, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, max_seqlen_q, q, q_out,
         cos_sin, positions, axis_of, interleaved, kv_scale, k_scale_tok, v_scale_tok,
-        k_scale_blk, v_scale_blk)
+        k_scale_blk, v_scale_blk, stream)
     if stream is None:
         stream = torch.cuda.current_stream(k.device)
     with torch.cuda.device(k.device):
