@@ -282,7 +282,8 @@ typedef struct {
   const void* k;       /* [total_q, num_kv_heads, head_dim] of `dtype`, strides k_stride */
   const void* v;       /* likewise, v_stride */
   const void* q;       /* [total_q, num_q_heads, head_dim] to rotate, or NULL */
-  void* q_out;         /* the rotated queries, q_out_stride (may be q itself) */
+  void* q_out;         /* the rotated queries, q_out_stride: q itself, or memory that overlaps
+                          none of q, k and v */
   void* k_cache;       /* [num_blocks, block_size, num_kv_heads, head_dim] kv_dtype, contiguous */
   void* v_cache;
   const int32_t* cu_seqlens_q;  /* [num_seqs + 1] */
@@ -348,9 +349,10 @@ typedef struct {
  * reached by two sequences of one call, or twice by one, is the caller's error.
  *
  * A token whose cache position is negative (kv_len < q_len) is skipped, as are rows of k, v
- * and q past cu_seqlens_q[num_seqs], and a sequence's tokens from total_q on.  A block id outside [0, num_blocks) or past the table's
- * row is not written; a position outside [0, max_position) skips its token, queries included;
- * both raise UA_ERR_DEVICE_CHECK in the device status word.
+ * and q past cu_seqlens_q[num_seqs], and a sequence's tokens from total_q on.  A block id
+ * outside [0, num_blocks) or past the table's row is not written; a position outside [0,
+ * max_position) skips its token, queries included; both raise UA_ERR_DEVICE_CHECK in the
+ * device status word.
  *
  * Asynchronous on `stream`, capturable, no workspace, no allocation.  Returns UA_OK or
  * UA_ERR_INVALID_ARG (a missing or misaligned pointer, a size, stride or enum value that is

@@ -491,7 +491,7 @@ def append_kv(k, v, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *,
     ``positions`` int32 [total_q], or, with several axes (time, height, width), at positions
     [axes, total_q] with ``axis_of``: the axis of each of the rot_dim / 2 frequencies, e.g.
     [0] * 16 + [1] * 24 + [2] * 24.  ``q`` [total_q, H_q, D] is rotated into ``q_out`` (new
-    unless given; may be q itself), which is returned.
+    unless given; may be q itself, else overlaps none of q, k and v), which is returned.
 
     Scales of an 8-bit cache, one form: ``kv_scale`` float32 [2] (e4m3, per tensor, read);
     k_scale_tok / v_scale_tok float32 [blocks, block_size, H_kv] (e4m3, per token, written);

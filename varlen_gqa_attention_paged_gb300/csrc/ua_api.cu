@@ -376,7 +376,7 @@ void make_plan(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, int
   // the mean, but a merge kernel and a schedule more, about 5 tiles' time.  Walks that a window
   // bounds are all alike, so only their own rounding can be gained; others differ, and the
   // longest is taken by few.  Measured at 32/8 heads, d128, int8, up to 8191 keys: 48 sequences
-  // 116 against 82 us, 24: 75 against 48, 12: 36 against 32, 8: 25 against 27; d256, 24: 120
+  // 116 against 83 us, 24: 75 against 48, 12: 36 against 32, 8: 25 against 27; d256, 24: 120
   // against 98; 32 windows of 4096: 50 against 54, 24: 49 against 44.
   const long long stream_tiles = (walk + 15) / 64 + 2;  // of one walk, at most
   const bool alike = window_left >= 0 && window_left < sh->max_seqlen_k;

@@ -20,7 +20,7 @@
 // warp reads beside the stage; they join the score's factor and its exponent as in the tile
 // kernel (weights w = 2^(x + log2 vs - M), row sums of w / vs; the weights are rounded to f16
 // for P.V, half a step of 2^-11, and summed unrounded).  Bound by HBM where the batch is long
-// enough: 48 sequences of up to 8191 keys, 32/8 heads, d128, 82 us (int8) and 86 us (e4m3), 6.0
+// enough: 48 sequences of up to 8191 keys, 32/8 heads, d128, 83 us (int8) and 86 us (e4m3), 6.0
 // and 5.8 TB/s; by the chain of each tile (copy, scores, softmax, P.V) and by a call's fixed
 // cost, about 5 us, where it is not (8 windows of 4096 keys: 18.3 us, 3.7 TB/s).  The q-block's
 // rows leave a CTA as one partial per row in shared memory: written out (one partition), merged with the other
@@ -1302,7 +1302,7 @@ cudaError_t launch_decode_t(const TileParams& tp, dim3 grid, int cluster_y, int 
   // An even share's grid takes every slot of the device, and follows the merge kernel of the
   // call before in a decode loop.  Started while that one still runs, its clusters are placed
   // unevenly around it: 106 against 83 us a call, back to back, for 48 sequences of up to 8191
-  // keys (int8, 32/8 heads, d128), 297 against 179 us at d256.  So it waits for a whole device.
+  // keys (int8, 32/8 heads, d128), 297 against 180 us at d256.  So it waits for a whole device.
   return launch_cluster(!STREAM, kern, grid, dim3(C::kThreads), C::kSmemBytes, stream, cluster_y,
                         cluster_z, tp);
 }

@@ -5,7 +5,7 @@
 namespace ua {
 
 // With score features two softmax warps share a lane quarter: softcap, 24/4 heads, two chunks of
-// 4096 behind 4096 (e4m3) 1406 us against 1598 with one, three ragged ones of up to 1501 (int8)
+// 4096 behind 4096 (e4m3) 1384 us against 1598 with one, three ragged ones of up to 1501 (int8)
 // 250 against 302.  Without them one does, in one pass; the halves' exchange of row maxima cost
 // 3 % there (1.32 against 1.36 ms, both in two passes).
 cudaError_t launch_prefill_blk_d256(const PrefillParams& pp, dim3 grid, int kv, bool feat, int nq,

@@ -50,8 +50,8 @@ namespace ua {
 // unchanged; k_scale joins the score scale and v_scale the output (per-token scales:
 // folded into each key's f16 row instead).
 // Block-scaled caches: 24/4 heads, two chunks of 4096 behind 4096, e4m3: 1104 us; three ragged
-// chunks of up to 1501 tokens (2999 keys) with a softcap, int8: 251 us (628 TFLOP/s; 199 without the softcap),
-// bound by the dequant warps' and the softmax warps' instructions (issue slots 54 %, tensor 32 %).
+// chunks of up to 1501 tokens (2999 keys) with a softcap, int8: 250 us (634 TFLOP/s; 204 without
+// the softcap), bound by the dequant warps' and the softmax warps' instructions (issue slots 54 %, tensor 32 %).
 // SW: softmax warps per tensor-memory lane quarter (2: each takes half the key columns of S
 // and half the columns of O, and the row maxima meet in shared memory once a tile).
 template <int D, bool F8 = false, int BLK = 0, int SW = 1>
