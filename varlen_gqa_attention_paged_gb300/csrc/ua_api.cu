@@ -692,10 +692,10 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
     ua::MergeParams mp{};
     if (pl.kernel == ua::KERNEL_DEC8S) {
       mp.np = p.ws_np;
-      mp.end = cu_seqlens_q + sh->num_seqs;
-      mp.hq = hq;
       mp.share_step = p.share_step;
     }
+    mp.end = cu_seqlens_q + sh->num_seqs;
+    mp.hq = hq;
     mp.ws_m = p.ws_m;
     mp.ws_l = p.ws_l;
     mp.ws_acc = p.ws_acc;

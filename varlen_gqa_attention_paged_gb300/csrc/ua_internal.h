@@ -92,11 +92,11 @@ struct PrefillParams {
 
 // The LSE-merge of split partitions (one output row per query token x head).
 struct MergeParams {
-  // an even share's first range and ranges of each row (1: nothing to merge), the tokens from one
-  // range's partial rows to the next's and the end of the last sequence's tokens, n_part ranges; or
-  // null: n_part partial rows of every row, one after the other
+  // an even share's first range and ranges of each row (1: nothing to merge) and the tokens from
+  // one range's partial rows to the next's, n_part ranges; or null: n_part partial rows of every
+  // row, one after the other
   const int2* np;
-  const int32_t* end;
+  const int32_t* end;  // the end of the last sequence's tokens
   int hq, share_step;
   const float* ws_m;
   const float* ws_l;

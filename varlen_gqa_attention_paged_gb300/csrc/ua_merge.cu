@@ -17,7 +17,11 @@ namespace ua {
 template <int D, bool SHARE>
 __global__ void __launch_bounds__(256) ua_merge_kernel(const __grid_constant__ MergeParams p) {
   constexpr int kPer = D / 32;  // output elements per lane
-  grid_dependency_wait();        // the partition kernel's scratch is complete
+  // rows behind the last sequence have no partial rows, and stay as they are.  (The lengths may
+  // be read before the wait: what wrote them had ended when the partition kernel, which waits for
+  // it first, let this one start.)
+  const long long end = static_cast<long long>(__ldg(p.end)) * p.hq;
+  grid_dependency_wait();  // the partition kernel's scratch is complete
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -25,8 +29,8 @@ __global__ void __launch_bounds__(256) ua_merge_kernel(const __grid_constant__ M
   if (row >= p.rows) return;
   int np = p.n_part;
   size_t first = static_cast<size_t>(row) * np, step = 1;  // of the row's partial rows
-  if constexpr (SHARE) {  // its own ranges, none for rows of no token
-    if (row / p.hq >= *p.end) return;
+  if constexpr (SHARE) {  // its own ranges
+    if (row >= end) return;
     const int2 own = p.np[row];
     np = own.y;  // (an aborted partition kernel may have left anything)
     if (np <= 1 || own.x < 0 || own.x > p.n_part - np) return;
@@ -75,6 +79,7 @@ __global__ void __launch_bounds__(256) ua_merge_kernel(const __grid_constant__ M
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   }
+  if (!SHARE && row >= end) return;
   const float inv = L > 0.f ? 1.f / L : 0.f;
   const size_t base = static_cast<size_t>(row) * D + lane * kPer;
 #pragma unroll
