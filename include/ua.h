@@ -110,8 +110,9 @@ typedef struct {
   int32_t out_dtype;          /* ua_dtype_t: F16, BF16 or F32 */
   int32_t num_splits;         /* 0: the dispatcher decides; > 0: partitions for the split path */
   void* workspace;            /* device scratch for the split path, or NULL: the library keeps
-                                 a grow-only buffer per (device, stream) and never frees a
-                                 replaced one while the process lives */
+                                 a grow-only buffer per (device, stream), and one for each
+                                 capture on a stream, and never frees them (nor a replaced one)
+                                 while the process lives */
   size_t workspace_bytes;     /* bytes at `workspace` */
   void* events;               /* NULL, or cudaEvent_t[3] recorded on `stream` before the
                                  attention kernel, after it, and after the merge kernel */
@@ -382,8 +383,9 @@ int ua_plan(const ua_shape_t* shape, int block_size, int num_q_heads, int num_kv
  * unnormalised partial output rows, each piece 256-byte aligned.  The scratch rules follow
  * the author's follow-up on the review of aiter PR #3962 ("split-K long-context decode for
  * shuffled fp8 SWA"): the partition count is capped, the scratch belongs to one stream at a
- * time (a caller workspace, or the library's own buffer per device and stream), and every
- * entry the merge reads is written by the same call, so the scratch needs no clearing.
+ * time (a caller workspace, or the library's own buffer per device and stream or per
+ * capture), and every entry the merge reads is written by the same call, so the scratch needs
+ * no clearing.
  * Returns 0 on an invalid argument too.
  */
 size_t ua_workspace_bytes(const ua_shape_t* shape, int block_size, int num_q_heads,

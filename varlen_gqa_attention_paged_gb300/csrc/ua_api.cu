@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <map>
 #include <mutex>
+#include <tuple>
 #include <utility>
 #include <vector>
 
@@ -432,12 +433,21 @@ void make_plan(const ua_shape_t* sh, int block_size, int hq, int hkv, int d, int
   }
 }
 
-// Library-owned split workspace: one grow-only buffer per (device, stream).  A buffer
-// that is replaced stays allocated, because earlier work (or a captured graph) on that
-// stream may still use it.
+// Library-owned split workspace: one grow-only buffer per (device, stream), and one for each
+// capture on a stream: graphs captured on one stream may be replayed at the same time, on others
+// than the one that they were captured on.  A buffer that is replaced stays allocated, because
+// earlier work on that stream may still use it, and so do the captures'.
+struct WorkspaceKey {
+  int dev;
+  void* stream;
+  unsigned long long capture;  // 0: none
+  bool operator<(const WorkspaceKey& o) const {
+    return std::tie(dev, stream, capture) < std::tie(o.dev, o.stream, o.capture);
+  }
+};
 struct WorkspacePool {
   std::mutex mu;
-  std::map<std::pair<int, void*>, std::pair<void*, size_t>> live;
+  std::map<WorkspaceKey, std::pair<void*, size_t>> live;
   std::vector<void*> retired;
 };
 
@@ -446,12 +456,16 @@ WorkspacePool& pool() {
   return *p;
 }
 
-int library_workspace(void* stream, size_t bytes, void** out) {
+int library_workspace(cudaStream_t stream, size_t bytes, void** out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return UA_ERR_CUDA;
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  unsigned long long capture = 0;
+  if (cudaStreamGetCaptureInfo(stream, &capturing, &capture) != cudaSuccess) return UA_ERR_CUDA;
+  if (capturing == cudaStreamCaptureStatusNone) capture = 0;
   WorkspacePool& wp = pool();
   std::lock_guard<std::mutex> lock(wp.mu);
-  auto key = std::make_pair(dev, stream);
+  const WorkspaceKey key = {dev, stream, capture};
   auto it = wp.live.find(key);
   if (it != wp.live.end() && it->second.second >= bytes) {
     *out = it->second.first;
@@ -459,8 +473,13 @@ int library_workspace(void* stream, size_t bytes, void** out) {
   }
   size_t grow = 1 << 20;
   while (grow < bytes) grow <<= 1;
+  // (an allocation is no part of a capture, and allowed beside one in this mode)
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return UA_ERR_CUDA;
   void* ptr = nullptr;
-  if (cudaMalloc(&ptr, grow) != cudaSuccess) return UA_ERR_CUDA;
+  const cudaError_t err = cudaMalloc(&ptr, grow);
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess || err != cudaSuccess)
+    return UA_ERR_CUDA;
   if (it != wp.live.end()) {
     wp.retired.push_back(it->second.first);
     it->second = std::make_pair(ptr, grow);
@@ -618,7 +637,7 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
     void* ws = sh->workspace;
     if (ws != nullptr) {
       if (sh->workspace_bytes < pl.workspace_bytes || !aligned16(ws)) return UA_ERR_WORKSPACE;
-    } else if ((rc = library_workspace(stream, pl.workspace_bytes, &ws)) != UA_OK) {
+    } else if ((rc = library_workspace(st, pl.workspace_bytes, &ws)) != UA_OK) {
       return rc;
     }
     const bool share = pl.kernel == ua::KERNEL_DEC8S;
