@@ -89,8 +89,9 @@ def _shape(q, k_cache, block_table, cu_seqlens_q, max_seqlen_q, max_seqlen_k, qq
     if k_scale_tok is not None:
         for t, ptr, strides in ((k_scale_tok, "k_scale_tok", "k_scale_stride"),
                                 (v_scale_tok, "v_scale_tok", "v_scale_stride")):
-            if t.dtype != torch.float32 or not t.is_cuda or t.dim() != 3:
-                raise ValueError("per-token scales are float32 CUDA tensors [blocks, slots, H_kv]")
+            if t.dtype != torch.float32 or t.device != k_cache.device or t.dim() != 3:
+                raise ValueError("per-token scales are float32 tensors [blocks, slots, H_kv] on "
+                                 "the caches' device")
             if tuple(t.shape) != tuple(k_cache.shape[:3]):
                 raise ValueError("per-token scales must be [num_blocks, block_size, H_kv]")
             setattr(sh, ptr, t.data_ptr())
@@ -106,6 +107,44 @@ def _shape(q, k_cache, block_table, cu_seqlens_q, max_seqlen_q, max_seqlen_k, qq
             setattr(sh, ptr, t.data_ptr())
             setattr(sh, ptr + "_stride", (ctypes.c_int64 * 2)(*t.stride()))
     return sh
+
+
+def _check_attention(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, max_seqlen_q,
+                     alibi_slopes, qq_bias, sinks, kv_scale, out, workspace):
+    """What the library cannot see from the pointers of an attention call's tensors."""
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [total_q, H_q, D] and k_cache [blocks, block_size, H_kv, D]")
+    dev, num_seqs = q.device, cu_seqlens_q.numel() - 1
+    if k_cache.shape[3] != q.shape[2] or v_cache.shape != k_cache.shape:
+        raise ValueError("q, k_cache and v_cache disagree on shape")
+    if v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache disagree on dtype")
+    for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache)):
+        if not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{name} must be contiguous and on q's device")
+    for name, t in (("cu_seqlens_q", cu_seqlens_q), ("seq_lens_k", seq_lens_k),
+                    ("block_table", block_table)):
+        if t.dtype != torch.int32 or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{name} must be a contiguous int32 tensor on q's device")
+    if num_seqs < 0 or seq_lens_k.numel() < num_seqs or block_table.dim() < 1 or \
+            block_table.numel() < num_seqs * block_table.shape[-1]:
+        raise ValueError("seq_lens_k [S] and block_table [S, blocks] hold fewer sequences than "
+                         "cu_seqlens_q [S + 1]")
+    if qq_bias is not None and qq_bias.shape[0] < max_seqlen_q:
+        raise ValueError("qq_bias needs at least max_seqlen_q rows")
+    for name, t, n in (("alibi_slopes", alibi_slopes, q.shape[1]), ("sinks", sinks, q.shape[1]),
+                       ("kv_scale", kv_scale, 2), ("qq_bias", qq_bias, 0)):
+        if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or
+                              t.device != dev or t.numel() < n):
+            raise ValueError(f"{name} must be contiguous float32 on q's device"
+                             + (f", {n} values" if n else ""))
+    if out is not None and (out.numel() < q.numel() or not out.is_contiguous() or
+                            out.device != dev):
+        raise ValueError("out must be contiguous, on q's device and hold q's elements")
+    if workspace is not None and (not workspace.is_contiguous() or workspace.device != dev):
+        raise ValueError("workspace must be contiguous and on q's device")
+    if not q.is_cuda:
+        raise ValueError("q, k_cache and v_cache must be CUDA tensors")
 
 
 def unified_attention(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *,
@@ -124,21 +163,14 @@ def unified_attention(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table
     block_size, H_kv] (any strides) for per-token fp8 scales, or k_scale_blk / v_scale_blk
     float32 [num_blocks, H_kv] (any strides) for an fp8 or int8 cache with a scale for each
     block and kv-head (what :func:`append_kv` writes).  max_seqlen_q / max_seqlen_k are host
-    ints.
+    ints.  All other tensors are contiguous (a q that :func:`append_kv` rotated in place inside
+    a fused projection is not), on one device.
     """
     lib = _lib.load()
+    _check_attention(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, max_seqlen_q,
+                     alibi_slopes, qq_bias, sinks, kv_scale, out, workspace)
     total_q, hq, d = q.shape
-    num_blocks, block_size, hkv, dk = k_cache.shape
-    if dk != d or v_cache.shape != k_cache.shape:
-        raise ValueError("q, k_cache and v_cache disagree on shape")
-    if qq_bias is not None and qq_bias.shape[0] < max_seqlen_q:
-        raise ValueError("qq_bias needs at least max_seqlen_q rows")
-    for name, t in (("cu_seqlens_q", cu_seqlens_q), ("seq_lens_k", seq_lens_k),
-                    ("block_table", block_table)):
-        if t.dtype != torch.int32 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor")
-    if not (q.is_cuda and k_cache.is_cuda and v_cache.is_cuda):
-        raise ValueError("q, k_cache and v_cache must be CUDA tensors")
+    _, block_size, hkv, _ = k_cache.shape
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
@@ -219,18 +251,10 @@ def prepare(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *, max_s
     """Validate and marshal a ``unified_attention`` call once (same arguments); the
     returned :class:`PreparedAttention` makes the call with new per-step tensors."""
     lib = _lib.load()
+    _check_attention(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, max_seqlen_q,
+                     alibi_slopes, qq_bias, sinks, kv_scale, out, workspace)
     total_q, hq, d = q.shape
-    num_blocks, block_size, hkv, dk = k_cache.shape
-    if dk != d or v_cache.shape != k_cache.shape:
-        raise ValueError("q, k_cache and v_cache disagree on shape")
-    if qq_bias is not None and qq_bias.shape[0] < max_seqlen_q:
-        raise ValueError("qq_bias needs at least max_seqlen_q rows")
-    for name, t in (("cu_seqlens_q", cu_seqlens_q), ("seq_lens_k", seq_lens_k),
-                    ("block_table", block_table)):
-        if t.dtype != torch.int32 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor")
-    if not (q.is_cuda and k_cache.is_cuda and v_cache.is_cuda):
-        raise ValueError("q, k_cache and v_cache must be CUDA tensors")
+    _, block_size, hkv, _ = k_cache.shape
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
