@@ -198,10 +198,10 @@ __device__ __forceinline__ float blk_scores32(const BlkRow& w, const GroupScales
 // weight is a finite f16); where a row's do, or it sees its first keys, its sums, O and the P of
 // this tile's earlier keys are brought down to the maximum of the 64 (the last rounded to f16
 // once more, half a step of 2^-11: S is gone, and keys that a later one outweighs by 2^8 count
-// for little).  That is rare past a row's first keys.  (Two passes, the first for the row maxima: 791 us for two chunks of 4096
-// tokens behind 4096, e4m3, 32/8 heads, d128; one pass with a maximum every 32 keys 771 us, as
-// a thread's chain of load, maximum, vote and exponentials is what the tile waits for; this
-// one 674 us.)  wait_pv: P.V of the tile before is done.
+// for little).  That is rare past a row's first keys.  (Two passes, the first for the row maxima:
+// 791 us for two chunks of 4096 tokens behind 4096, e4m3, 32/8 heads, d128; one pass with a
+// maximum every 32 keys 771 us, as a thread's chain of load, maximum, vote and exponentials is
+// what the tile waits for; this one 674 us.)  wait_pv: P.V of the tile before is done.
 template <bool FEAT, int D, typename WaitPv>
 __device__ __forceinline__ bool blk_softmax_tile(const BlkRow& w, const GroupScales* gs,
                                                  uint32_t tS, uint32_t tO, int k0, bool need_mask,
