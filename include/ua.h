@@ -364,6 +364,170 @@ typedef struct {
 int ua_append_kv(const ua_append_t* call, void* stream);
 
 /*
+ * Latent caches: one vector a token, shared by all heads, instead of keys and values a kv-head
+ * (the pages have no counterpart).  Row t of a cache [num_blocks, block_size, latent_dim +
+ * rope_dim] is [c_t | r_t]: c_t, the normalised latent, is a key and a value at once; r_t, the
+ * rotated rope key, is a part of the key only.  latent_dim is 128, 256 or 512, rope_dim a multiple
+ * of 16 up to 64, elements are F16 or BF16.  Caches, block tables, lengths and the device status
+ * word are used as by ua_unified_attention; every call below is asynchronous on `stream`,
+ * capturable, and returns a ua_status_t.
+ */
+
+/* One ua_append_latent call.  Strides are in elements; the last dim of each tensor has stride 1. */
+typedef struct {
+  const void* latent;           /* [total_q, latent_dim] of `dtype`, row stride latent_stride */
+  const void* k_rope;           /* [total_q, rope_dim], k_rope_stride */
+  const void* q_rope;           /* [total_q, num_heads, rope_dim] to rotate, or NULL */
+  void* q_rope_out;             /* the rotated queries: q_rope itself (with its strides), or memory
+                                   that overlaps none of the inputs */
+  void* cache;                  /* [num_blocks, block_size, latent_dim + rope_dim], contiguous */
+  const int32_t* cu_seqlens_q;  /* [num_seqs + 1] */
+  const int32_t* seq_lens_k;    /* [num_seqs]: lengths with the new tokens */
+  const int32_t* block_table;   /* [num_seqs, max_blocks_per_seq] */
+  const void* norm_weight;      /* [latent_dim] of norm_dtype, or NULL: latents are stored as they are */
+  const float* cos_sin;         /* [max_position, rope_dim]: a row's rope_dim / 2 cosines, then its
+                                   sines; 16-byte aligned; NULL: no rotation */
+  const int32_t* positions;     /* [total_q], or NULL: a token's place in the cache */
+  int64_t latent_stride;        /* token strides and q_rope's head strides: multiples of 8 */
+  int64_t k_rope_stride;
+  int64_t q_rope_stride[2];     /* token, head */
+  int64_t q_rope_out_stride[2];
+  int32_t num_seqs;
+  int32_t total_q;
+  int32_t max_blocks_per_seq;
+  int32_t num_blocks;
+  int32_t block_size;
+  int32_t num_heads;            /* of q_rope; 0 without it */
+  int32_t latent_dim;
+  int32_t rope_dim;
+  int32_t dtype;                /* of every tensor but norm_weight: F16 or BF16 */
+  int32_t norm_dtype;           /* `dtype` or F32 */
+  int32_t max_position;         /* rows of cos_sin */
+  int32_t interleaved;          /* pairs: 0: (f, f + rope_dim / 2); 1: (2 f, 2 f + 1) */
+  float norm_eps;
+} ua_append_latent_t;
+
+/*
+ * ua_append_latent -- appends the batch's new tokens to a latent cache, in one launch:
+ *   c_j = x_j * (mean_j(x_j^2) + norm_eps)^(-1/2) * norm_weight_j     (fp32, rounded once)
+ *   r   = k_rope rotated as ua_append_kv rotates keys, over its whole rope_dim
+ * and rotates q_rope beside it.  Token i of sequence b goes to cache position seq_lens_k[b] - q_len
+ * + i.  What ua_append_kv skips (tokens at negative positions, rows past cu_seqlens_q[num_seqs])
+ * and refuses on the device (block ids outside the cache: not written; positions outside the table:
+ * the token is skipped, its queries included) holds here too.
+ */
+int ua_append_latent(const ua_append_latent_t* call, void* stream);
+
+/* One ua_tree_mask call. */
+typedef struct {
+  const int32_t* parents;       /* [total_q]: the parent's index among its sequence's new tokens, below
+                                   the token's own; -1: none */
+  const int32_t* cu_seqlens_q;
+  const int32_t* seq_lens_k;    /* lengths with the new tokens */
+  int32_t* mask;                /* [total_q, mask_words] out, or NULL */
+  int32_t* positions;           /* [total_q] out, or NULL */
+  int64_t mask_stride;          /* words from one row of mask to the next, >= mask_words */
+  int32_t num_seqs;
+  int32_t total_q;
+  int32_t max_seqlen_q;         /* >= every q_len; at most 4096 */
+  int32_t mask_words;           /* 32 mask_words >= max_seqlen_q */
+} ua_tree_t;
+
+/*
+ * ua_tree_mask -- what the tokens of drafted trees see, from their parents: bit j of token i's mask
+ * (word j / 32) says that new token j of the sequence is i itself or an ancestor of i.  positions
+ * receives kv_len - q_len + the token's depth (its rotary position: siblings share one).  A parent
+ * that is not below its token (or below -1) counts as none, and raises UA_ERR_DEVICE_CHECK in the
+ * device status word, as does a q_len above max_seqlen_q, whose tokens from there on are left out.
+ * Rows past cu_seqlens_q[num_seqs] stay as they are.
+ */
+int ua_tree_mask(const ua_tree_t* call, void* stream);
+
+/* One ua_latent_attention call.  Tensors are contiguous. */
+typedef struct {
+  const void* q;                /* [total_q, num_heads, latent_dim + rope_dim] of `dtype` */
+  const void* cache;            /* [num_blocks, block_size, latent_dim + rope_dim] of `dtype` */
+  void* out;                    /* [total_q, num_heads, latent_dim] of out_dtype */
+  float* lse;                   /* [total_q, num_heads] or NULL: ln of each row's sum (-inf: no key) */
+  const int32_t* cu_seqlens_q;
+  const int32_t* seq_lens_k;
+  const int32_t* block_table;
+  const int32_t* tree_mask;     /* [total_q, tree_words] bits, or NULL: causal */
+  void* workspace;              /* device scratch, or NULL: the library's own (see ua_shape_t) */
+  size_t workspace_bytes;
+  int64_t tree_mask_stride;     /* words from one row of tree_mask to the next */
+  int32_t num_seqs;
+  int32_t total_q;
+  int32_t max_seqlen_q;         /* >= every q_len and kv_len: the grid's size follows from them */
+  int32_t max_seqlen_k;
+  int32_t max_blocks_per_seq;
+  int32_t num_blocks;
+  int32_t block_size;
+  int32_t num_heads;
+  int32_t latent_dim;
+  int32_t rope_dim;
+  int32_t dtype;
+  int32_t out_dtype;            /* F16, BF16 or F32 */
+  int32_t tree_words;           /* 32 tree_words >= max_seqlen_q */
+  float scale;                  /* > 0 */
+} ua_latent_t;
+
+/*
+ * ua_latent_attention -- attention over a latent cache with absorbed projections: q is in the
+ * latent space (the key up-projection applied to it), and so is out.  For row i of head h at
+ * position p = kv_len - q_len + i:
+ *   s_j = scale * q . [c_j | r_j],   out = sum_j e^{s_j} c_j / sum_j e^{s_j}
+ * over 0 <= j < kv_len with j <= p, or with tree_mask over j < kv_len - q_len and those new tokens
+ * j of the sequence whose bit j - (kv_len - q_len) is set in the row's mask (no other rule: a
+ * token sees itself only if its own bit is set).  A row that sees no key is written as 0.  Every
+ * slot below kv_len must hold finite values (their weight may be 0, but they are multiplied); slots
+ * past it may hold anything.  Every block size works; multiples of 8 load eight rows at a time.
+ * Returns UA_ERR_UNSUPPORTED where total_q * num_heads or num_blocks * block_size passes 31 bits,
+ * UA_ERR_WORKSPACE where `workspace` is smaller than ua_latent_workspace_bytes().
+ */
+int ua_latent_attention(const ua_latent_t* call, void* stream);
+
+/* Bytes of scratch that the call needs on the current device (0 on an invalid argument too). */
+size_t ua_latent_workspace_bytes(const ua_latent_t* call);
+
+/* One ua_latent_prefill call.  Strides are in elements: multiples of 8 (the last dim has stride 1). */
+typedef struct {
+  const void* q;                /* [total_q, num_heads, nope_dim + rope_dim] of `dtype` */
+  const void* k_nope;           /* [total_k, num_heads, nope_dim] */
+  const void* k_rope;           /* [total_k, rope_dim], shared by the heads */
+  const void* v;                /* [total_k, num_heads, value_dim] */
+  void* out;                    /* [total_q, num_heads, value_dim] of out_dtype, contiguous */
+  float* lse;                   /* [total_q, num_heads] or NULL: ln of each row's sum (-inf: no key) */
+  const int32_t* cu_seqlens_q;  /* [num_seqs + 1] */
+  const int32_t* cu_seqlens_k;  /* [num_seqs + 1] */
+  int64_t q_stride[2];          /* token, head */
+  int64_t k_nope_stride[2];
+  int64_t v_stride[2];
+  int64_t k_rope_stride;
+  int32_t num_seqs;
+  int32_t total_q;
+  int32_t total_k;
+  int32_t max_seqlen_q;         /* >= every q_len and k_len: the grid's shape follows from them */
+  int32_t max_seqlen_k;
+  int32_t num_heads;
+  int32_t nope_dim;             /* 64 or 128 */
+  int32_t rope_dim;             /* a multiple of 16 up to 64 */
+  int32_t value_dim;            /* 64 or 128 */
+  int32_t dtype;
+  int32_t out_dtype;            /* F16, BF16 or F32 */
+  float scale;                  /* > 0 */
+} ua_latent_prefill_t;
+
+/*
+ * ua_latent_prefill -- the expanded form, for prompts: keys and values of every head, as the
+ * up-projection of the latents gives them (k_nope and v may be slices of one tensor), and the rope
+ * keys.  For row i of a sequence of q_len queries and k_len keys, at position p = k_len - q_len + i:
+ *   s_j = scale * (q_nope . k_nope_j + q_rope . k_rope_j),  j <= p,   out = softmax(s) v
+ * A row that sees no key is written as 0.  Rows past cu_seqlens_q[num_seqs] stay as they are.
+ */
+int ua_latent_prefill(const ua_latent_prefill_t* call, void* stream);
+
+/*
  * ua_plan -- the dispatcher's decision for a call with these sizes, without touching
  * the GPU: path, kernel, partitions, grid and workspace bytes.  The split path is
  * taken (UA_BACKEND_AUTO) when the 2D grid fills less than one wave of SMs and the

@@ -3,7 +3,8 @@
 Python binding of the C ABI in ``include/ua.h``: it only turns torch tensors into
 device pointers, the current CUDA stream and host-side sizes, and calls
 ``ua_append_kv`` (new keys and values into the paged cache, rotated by position) and
-``ua_unified_attention`` (attention over it) in ``libua.so``.  Every step of the computation
+``ua_unified_attention`` (attention over it) in ``libua.so``, and their counterparts for caches
+of one latent vector a token (``latent.py``).  Every step of the computation
 runs in the library's CUDA kernels; without the built library this module raises.
 """
 from __future__ import annotations
@@ -19,6 +20,9 @@ from ._lib import (UA_BACKEND_2D, UA_BACKEND_AUTO, UA_BACKEND_SPLIT, UA_DT_BF16,
 
 __all__ = ["unified_attention", "prepare", "PreparedAttention", "append_kv", "prepare_append",
            "PreparedAppend", "rope_table", "plan", "device_status", "device_status_reset",
+           "append_latent", "prepare_append_latent", "PreparedAppendLatent", "latent_attention",
+           "prepare_latent_attention", "PreparedLatentAttention", "latent_workspace_bytes",
+           "latent_prefill", "prepare_latent_prefill", "PreparedLatentPrefill", "tree_mask",
            "UaError", "BACKENDS", "library_path"]
 
 BACKENDS = {"auto": UA_BACKEND_AUTO, "2d": UA_BACKEND_2D, "split": UA_BACKEND_SPLIT}
@@ -583,3 +587,9 @@ def device_status_reset(stream=None) -> None:
     rc = lib.ua_device_status_reset(ctypes.c_void_p(stream.cuda_stream))
     if rc != 0:
         raise UaError(rc, "ua_device_status_reset")
+
+
+from .latent import (PreparedAppendLatent, PreparedLatentAttention,  # noqa: E402
+                     PreparedLatentPrefill, append_latent, latent_attention, latent_prefill,
+                     latent_workspace_bytes, prepare_append_latent, prepare_latent_attention,
+                     prepare_latent_prefill, tree_mask)

@@ -20,7 +20,8 @@ UA_PATH_2D, UA_PATH_SPLIT = 1, 2
 
 # every symbol include/ua.h declares
 EXPORTS = ("ua_unified_attention", "ua_unified_attention_call", "ua_unified_attention_noalloc",
-           "ua_append_kv", "ua_plan", "ua_workspace_bytes", "ua_device_status",
+           "ua_append_kv", "ua_append_latent", "ua_latent_attention", "ua_latent_workspace_bytes",
+           "ua_latent_prefill", "ua_tree_mask", "ua_plan", "ua_workspace_bytes", "ua_device_status",
            "ua_device_status_reset", "ua_shape_bytes", "ua_status_string", "ua_version")
 
 
@@ -76,6 +77,52 @@ class UaAppend(ctypes.Structure):
             "block_size", "num_q_heads", "num_kv_heads", "head_dim", "dtype", "kv_dtype",
             "rot_dim", "max_position", "interleaved", "n_axes")] +
         [("axis_of", ctypes.c_void_p)])
+
+
+class UaAppendLatent(ctypes.Structure):
+    _fields_ = (
+        [(n, ctypes.c_void_p) for n in (
+            "latent", "k_rope", "q_rope", "q_rope_out", "cache", "cu_seqlens_q", "seq_lens_k",
+            "block_table", "norm_weight", "cos_sin", "positions")] +
+        [(n, ctypes.c_int64) for n in ("latent_stride", "k_rope_stride")] +
+        [(n, ctypes.c_int64 * 2) for n in ("q_rope_stride", "q_rope_out_stride")] +
+        [(n, ctypes.c_int32) for n in (
+            "num_seqs", "total_q", "max_blocks_per_seq", "num_blocks", "block_size", "num_heads",
+            "latent_dim", "rope_dim", "dtype", "norm_dtype", "max_position", "interleaved")] +
+        [("norm_eps", ctypes.c_float)])
+
+
+class UaTree(ctypes.Structure):
+    _fields_ = (
+        [(n, ctypes.c_void_p) for n in ("parents", "cu_seqlens_q", "seq_lens_k", "mask",
+                                        "positions")] +
+        [("mask_stride", ctypes.c_int64)] +
+        [(n, ctypes.c_int32) for n in ("num_seqs", "total_q", "max_seqlen_q", "mask_words")])
+
+
+class UaLatent(ctypes.Structure):
+    _fields_ = (
+        [(n, ctypes.c_void_p) for n in (
+            "q", "cache", "out", "lse", "cu_seqlens_q", "seq_lens_k", "block_table", "tree_mask",
+            "workspace")] +
+        [("workspace_bytes", ctypes.c_size_t), ("tree_mask_stride", ctypes.c_int64)] +
+        [(n, ctypes.c_int32) for n in (
+            "num_seqs", "total_q", "max_seqlen_q", "max_seqlen_k", "max_blocks_per_seq",
+            "num_blocks", "block_size", "num_heads", "latent_dim", "rope_dim", "dtype",
+            "out_dtype", "tree_words")] +
+        [("scale", ctypes.c_float)])
+
+
+class UaLatentPrefill(ctypes.Structure):
+    _fields_ = (
+        [(n, ctypes.c_void_p) for n in (
+            "q", "k_nope", "k_rope", "v", "out", "lse", "cu_seqlens_q", "cu_seqlens_k")] +
+        [(n, ctypes.c_int64 * 2) for n in ("q_stride", "k_nope_stride", "v_stride")] +
+        [("k_rope_stride", ctypes.c_int64)] +
+        [(n, ctypes.c_int32) for n in (
+            "num_seqs", "total_q", "total_k", "max_seqlen_q", "max_seqlen_k", "num_heads",
+            "nope_dim", "rope_dim", "value_dim", "dtype", "out_dtype")] +
+        [("scale", ctypes.c_float)])
 
 
 class UaPlan(ctypes.Structure):
@@ -136,6 +183,17 @@ def load():
         lib.ua_version.argtypes = []
         lib.ua_version.restype = ctypes.c_int
         _check_layout(lib)
+        missing = [name for name in EXPORTS if not hasattr(lib, name)]
+        if missing:
+            raise RuntimeError(f"{LIB_PATH} lacks {missing[0]}: build it again "
+                               "(varlen_gqa_attention_paged_gb300.build.build())")
+        for name, struct in (("ua_append_latent", UaAppendLatent), ("ua_tree_mask", UaTree),
+                             ("ua_latent_attention", UaLatent),
+                             ("ua_latent_prefill", UaLatentPrefill)):
+            fn = getattr(lib, name)
+            fn.argtypes, fn.restype = [ctypes.POINTER(struct), vp], ctypes.c_int
+        lib.ua_latent_workspace_bytes.argtypes = [ctypes.POINTER(UaLatent)]
+        lib.ua_latent_workspace_bytes.restype = ctypes.c_size_t
         _LIB = lib
         return lib
 

@@ -734,6 +734,20 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, void* out,
 namespace ua {
 int status_word(unsigned int** out) { return ::status_word(out); }
 int device_sm_count(int* out) { return ::device_sm_count(out); }
+int library_workspace(cudaStream_t stream, size_t bytes, void** out) {
+  return ::library_workspace(stream, bytes, out);
+}
+bool encode_half_map(CUtensorMap* map, const void* base, bool bf16, int rank,
+                     const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = ::tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+             static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 }  // namespace ua
 
 extern "C" {

@@ -1,0 +1,80 @@
+// ua_latent.h -- launch arguments of the latent-attention kernels of libua.so.
+#pragma once
+
+#include "ua_internal.h"
+
+namespace ua {
+
+// Rows (query token x head) of one CTA's tile, and keys of one tile.
+constexpr int kLatRows = 64;
+constexpr int kLatKeys = 64;
+
+// One launch of the absorbed form's kernel.  q is viewed as rows [total_q * heads][L + R] and the
+// cache as rows [num_blocks * block_size][L + R]; each has two maps: boxes of 64 elements x rows x
+// L / 64 column blocks of the latent part, and boxes of 64 elements x rows anywhere in a row
+// (elements past L + R read as zero).
+struct LatentParams {
+  CUtensorMap q_lat, q_row, k_lat, k_row;
+  void* out;                    // [total_q, heads, L]
+  float* lse;                   // [total_q, heads] or null
+  const int32_t* cu_seqlens_q;
+  const int32_t* seq_lens_k;
+  const int32_t* block_table;
+  const int32_t* tree;          // [total_q][tree_stride] words of bits, or null: causal
+  long long tree_stride;
+  int tree_words;
+  // partial rows of a tile that several workers share: slot 2 * cta (the worker entered the tile
+  // at a later key) or 2 * cta + 1 (it began the tile and did not end it), kLatRows rows each
+  float* ws_acc;
+  float* ws_m;
+  float* ws_l;
+  int4* ws_meta;                // [ctas] of the tile that a CTA began: first row, rows, parts
+  unsigned int* status;
+  int num_seqs, total_q, max_blocks_per_seq, num_blocks, block_size, heads, rope_dim, out_dtype;
+  int workers;                  // groups of `cl` CTAs that share a tile's keys
+  int cl;                       // CTAs (tiles of kLatRows rows) of a worker: 1 or 2
+  int box_rows;                 // 8: a box is eight cache rows; 1: one row
+  int min_share;                // key tiles that a worker takes at least
+  float scale;
+};
+
+// One launch of the expanded form's kernel: maps of q [total_q][heads][N + R], k_nope
+// [total_k][heads][N] and v [total_k][heads][V] (boxes of 64 elements x one head x 128 tokens) and
+// of k_rope [total_k][R] (64 elements x 128 tokens; elements past R read as zero).
+struct LatentPrefillParams {
+  CUtensorMap q, k, k_rope, v;
+  void* out;                    // [total_q, heads, V]
+  float* lse;                   // [total_q, heads] or null
+  const int32_t* cu_seqlens_q;
+  const int32_t* cu_seqlens_k;
+  unsigned int* status;
+  int num_seqs, total_q, total_k, heads, rope_dim, out_dtype, slots;
+  float scale;
+};
+
+struct LatentMergeParams {
+  void* out;
+  float* lse;
+  const float* ws_acc;
+  const float* ws_m;
+  const float* ws_l;
+  const int4* ws_meta;
+  long long rows;               // total_q * heads
+  int ctas, cl, out_dtype;
+};
+
+cudaError_t launch_latent_l128(const LatentParams& p, bool bf16, cudaStream_t s);
+cudaError_t launch_latent_l256(const LatentParams& p, bool bf16, cudaStream_t s);
+cudaError_t launch_latent_l512(const LatentParams& p, bool bf16, cudaStream_t s);
+cudaError_t launch_latent_prefill_n64(const LatentPrefillParams& p, int value, bool bf16,
+                                      cudaStream_t s);
+cudaError_t launch_latent_prefill_n128(const LatentPrefillParams& p, int value, bool bf16,
+                                       cudaStream_t s);
+cudaError_t launch_latent_merge(const LatentMergeParams& p, int latent, cudaStream_t s);
+
+// Scratch of a launch of `ctas` CTAs.
+constexpr size_t latent_scratch_bytes(int ctas, int latent) {
+  return static_cast<size_t>(ctas) * (2 * kLatRows * (static_cast<size_t>(latent) + 2) * 4 + 16);
+}
+
+}  // namespace ua

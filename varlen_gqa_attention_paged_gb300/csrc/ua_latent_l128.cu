@@ -1,0 +1,10 @@
+// ua_latent_l128.cu -- instantiations of the absorbed latent-attention kernel for 128 latent elements.
+#include "ua_latent.cuh"
+
+namespace ua {
+
+cudaError_t launch_latent_l128(const LatentParams& p, bool bf16, cudaStream_t s) {
+  return bf16 ? launch_latent_t<128, true>(p, s) : launch_latent_t<128, false>(p, s);
+}
+
+}  // namespace ua
