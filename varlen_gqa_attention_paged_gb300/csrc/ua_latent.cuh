@@ -189,10 +189,41 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   return BF16 ? pack_bf16(a, b) : pack_f16(a, b);
 }
 
-__device__ __forceinline__ void store_as(void* out, size_t at, float v, int dtype) {
-  if (dtype == UA_DT_F32) static_cast<float*>(out)[at] = v;
-  else if (dtype == UA_DT_BF16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
-  else static_cast<__half*>(out)[at] = __float2half_rn(v);
+// Two neighbouring elements of the output (`at` even).
+__device__ __forceinline__ void store_two(void* out, size_t at, float a, float b, int dtype) {
+  if (dtype == UA_DT_F32)
+    *reinterpret_cast<float2*>(static_cast<float*>(out) + at) = make_float2(a, b);
+  else
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + at) =
+        dtype == UA_DT_BF16 ? pack_bf16(a, b) : pack_f16(a, b);
+}
+
+// Whether the phase of `parity` is complete, for a whole warp, without waiting.
+__device__ __forceinline__ bool mbar_test_warp(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+
+// 16 lanes x 64 columns of an accumulator over a warp: register 4 g + 2 k + e of lane t holds row
+// t / 4 + 8 k, column 8 g + 2 (t mod 4) + e.
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
 }
 
 // ln of a row's sum: m its running max in log2 units, l the sum of 2^(x - m).
@@ -221,8 +252,8 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
   uint64_t* const o_empty = bars + 6;
   uint64_t* const fin = bars + 7;
   uint64_t* const k_full = bars + 8;   // [S]
-  uint64_t* const k_empty = k_full + S;
-  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(k_empty + S);
+  uint64_t* const k_empty = k_full + S;  // [S][2]: of a tile's first and second half
+  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(k_empty + 2 * S);
   float* const sF = reinterpret_cast<float*>(bars + 32);  // [2][64] factors of O's rows
   __shared__ int s_abort;
 
@@ -240,10 +271,8 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
     mbar_init(pv_done, 1);
     mbar_init(o_empty, 4);
     mbar_init(fin, 1);
-    for (int i = 0; i < S; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-    }
+    for (int i = 0; i < S; ++i) mbar_init(&k_full[i], 1);
+    for (int i = 0; i < 2 * S; ++i) mbar_init(&k_empty[i], 1);
     s_abort = 0;
     mbar_fence_init();
   }
@@ -299,7 +328,7 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
       // its cache row (past the cache, so that the copy fills zeros, where there is no key)
       auto row_of = [&](int j, int i, int blk) -> int {
         const int key = key_of(j, i);
-        if (key >= w.kv_len) return oob;
+        if (key >= w.kv_len || (p.box_rows == 8 && lane >= 8)) return oob;
         if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
           atomicOr(p.status, DEV_BAD_BLOCK);
           return oob;
@@ -314,31 +343,36 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
       }
       for (int n = 0; n < s.nt; ++n, ++it) {
         const int j = s.j0 + n, st = it % S;
-        if (it >= S && !pf_wait_warp(&k_empty[st], ((it / S) - 1) & 1, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(&k_full[st], C::kTileBytes);
-        __syncwarp();
         uint8_t* const tile = sK + st * C::kTileBytes;
-        if (p.box_rows == 8) {
-          if (lane < 8) {
-            const int row = row_of(j, 0, blk0[0]);
-            uint8_t* const dst = tile + lane * C::kGroup;
-            tma_load_3d_pf(dst, &p.k_lat, 0, row, 0, &k_full[st]);
-            tma_load_2d(dst + C::kCB * 1024, &p.k_row, L, row, &k_full[st]);
-          }
-        } else {
+        const int row0 = row_of(j, 0, blk0[0]);
+        const int row1 = p.box_rows == 8 ? 0 : row_of(j, 1, blk0[1]);
+        // a tile's halves are free one after the other
 #pragma unroll 1
-          for (int i = 0; i < 2; ++i) {
-            const int k = lane + 32 * i;
-            const int row = row_of(j, i, blk0[i]);
+        for (int half = 0; half < 2; ++half) {
+          if (it >= S && !pf_wait_warp(&k_empty[2 * st + half], ((it / S) - 1) & 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          // (only now: the tile before has arrived, so that its phase of the barrier is over)
+          if (half == 0) {
+            if (lane == 0) mbar_arrive_expect_tx(&k_full[st], C::kTileBytes);
+            __syncwarp();
+          }
+          if (p.box_rows == 8) {
+            if ((lane >> 2) == half) {
+              uint8_t* const dst = tile + lane * C::kGroup;
+              tma_load_3d_pf(dst, &p.k_lat, 0, row0, 0, &k_full[st]);
+              tma_load_2d(dst + C::kCB * 1024, &p.k_row, L, row0, &k_full[st]);
+            }
+          } else {
+            const int k = lane + 32 * half;
             uint8_t* const dst = tile + (k >> 3) * C::kGroup + (k & 7) * 128;
 #pragma unroll 1
             for (int cb = 0; cb < C::kCH; ++cb)
-              tma_load_2d(dst + cb * 1024, &p.k_row, 64 * cb, row, &k_full[st]);
+              tma_load_2d(dst + cb * 1024, &p.k_row, 64 * cb, half ? row1 : row0, &k_full[st]);
           }
         }
+        if (!ok) break;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           blk0[i] = blk1[i];
@@ -347,74 +381,102 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
       }
     }
     // never leave copies in flight into this CTA's shared memory (even after an abort)
-    for (int i = max(0, it - S); i < it; ++i)
+    // (a tile that was left half copied never completes: its first half has long arrived when the
+    // wait for it gives up)
+    for (int i = max(0, it - S + (ok ? 0 : 1)); i < it + (ok ? 0 : 1); ++i)
       mbar_wait_bounded(&k_full[i % S], (i / S) & 1, p.status, DEV_TIMEOUT);
     if (sg > 0) mbar_wait_bounded(q_full, (sg - 1) & 1, p.status, DEV_TIMEOUT);
   } else if (warp == kMma) {
     // ======================================================== MMA issue
-    // Per segment: S_0, S_1, then for every tile j: [P_j ready] O^T += V_j^T P_j^T, S_{j+2}.
-    // S_{j+2} overwrites S_j, which the softmax has read when P_j is ready.
+    // Two cursors over the worker's tiles, of S = Q K^T and of O^T += V^T P^T; whichever has its
+    // inputs goes next, P.V first (it frees its tile).  S_{i+2} overwrites S_i, which the softmax
+    // has read when P_i is ready.  The MMAs are unrolled: in a rolled loop an issue took 52 cycles
+    // a 64 x 64 x 16 product instead of the 33 that it takes to run.
     constexpr uint32_t kIdQK = umma_idesc_f16(kLatRows, kLatKeys, BF16, false);
     constexpr uint32_t kIdPV = umma_idesc_f16(128, kLatRows, BF16, false) | (1u << 15);
-    const int qk_steps = L / 16 + p.rope_dim / 16;
-    for (; ok && w.left > 0; w.next(p)) {
-      const LatentSeg s(p, w, rank);
-      if (s.nt <= 0) continue;
-      if (!pf_wait_warp(q_full, sg & 1, abort_flag, p.status)) { ok = false; break; }
-      auto qk = [&](int n) -> bool {
-        const int i = it + n, st = i % S;
-        if (!pf_wait_warp(&k_full[st], (i / S) & 1, abort_flag, p.status)) return false;
-        tc_fence_after();
-        const uint32_t qb = smem_addr(sQ), kb = smem_addr(sK + st * C::kTileBytes);
-#pragma unroll 4
-        for (int kk = 0; kk < qk_steps; ++kk) {
-          const uint64_t ad = smem_desc_sw128(qb + (kk >> 2) * C::kQCB + (kk & 3) * 32, 16, 1024);
-          const uint64_t bd =
-              smem_desc_sw128(kb + (kk >> 2) * 1024 + (kk & 3) * 32, 16, C::kGroup);
-          umma_f16_ss_warp(tmem + (i & 1) * kLatKeys, ad, bd, kIdQK, kk > 0 ? 1u : 0u);
+    const int rope_steps = p.rope_dim / 16;
+    struct Cursor {
+      LatentWalk w;
+      int n, nt, sg, i;  // tile of the segment, its tiles, segments and tiles before
+      __device__ __forceinline__ void seek(const LatentParams& p, int rank) {
+        n = nt = 0;
+        for (; w.left > 0; w.next(p)) {
+          const LatentSeg s(p, w, rank);
+          if (s.nt > 0) {
+            nt = s.nt;
+            return;
+          }
         }
-        umma_commit_warp(&s_full[i & 1]);
-        if (n == s.nt - 1) umma_commit_warp(q_empty);
-        return true;
-      };
-      auto pv = [&](int n) -> bool {
-        const int i = it + n, st = i % S;
-        if (!pf_wait_warp(p_full, i & 1, abort_flag, p.status)) return false;
-        if (n == 0 && sg > 0 && !pf_wait_warp(o_empty, (sg - 1) & 1, abort_flag, p.status))
-          return false;
+      }
+      __device__ __forceinline__ void step(const LatentParams& p, int rank) {
+        ++i;
+        if (++n < nt) return;
+        ++sg;
+        w.next(p);
+        seek(p, rank);
+      }
+    };
+    Cursor qk{w, 0, 0, 0, 0};
+    qk.seek(p, rank);
+    Cursor pv = qk;
+    unsigned long long since = global_timer_ns();
+    while (pv.nt > 0) {
+      if (pv.i < qk.i && mbar_test_warp(p_full, pv.i & 1) &&
+          (pv.n > 0 || pv.sg == 0 || mbar_test_warp(o_empty, (pv.sg - 1) & 1))) {
+        const int st = pv.i % S;
         tc_fence_after();
         const uint32_t vb = smem_addr(sK + st * C::kTileBytes), pb = smem_addr(sP);
 #pragma unroll
-        for (int ks = 0; ks < kLatKeys / 16; ++ks)
+        for (int ks = 0; ks < kLatKeys / 16; ++ks) {
 #pragma unroll
           for (int mb = 0; mb < C::kMB; ++mb) {
             const uint64_t ad =
                 smem_desc_sw128(vb + ks * 2 * C::kGroup + mb * 2048, 1024, C::kGroup);
             const uint64_t bd = smem_desc_sw128(pb + ks * 32, 16, 1024);
             umma_f16_ss_warp(tmem + C::kTmemO + mb * kLatRows, ad, bd, kIdPV,
-                             n > 0 || ks > 0 ? 1u : 0u);
+                             pv.n > 0 || ks > 0 ? 1u : 0u);
           }
+          if (ks == kLatKeys / 32 - 1) umma_commit_warp(&k_empty[2 * st]);
+        }
         umma_commit_warp(pv_done);
-        umma_commit_warp(&k_empty[st]);
-        return true;
-      };
-      ok = qk(0);
-      if (ok && s.nt > 1) ok = qk(1);
-      for (int n = 0; ok && n < s.nt; ++n) {
-        ok = pv(n);
-        if (ok && n + 2 < s.nt) ok = qk(n + 2);
+        umma_commit_warp(&k_empty[2 * st + 1]);
+        pv.step(p, rank);
+      } else if (qk.nt > 0 && qk.i < pv.i + 2 && mbar_test_warp(&k_full[qk.i % S], (qk.i / S) & 1) &&
+                 (qk.n > 0 || mbar_test_warp(q_full, qk.sg & 1))) {
+        const int st = qk.i % S;
+        tc_fence_after();
+        const uint32_t qb = smem_addr(sQ), kb = smem_addr(sK + st * C::kTileBytes);
+        const uint32_t tS = tmem + (qk.i & 1) * kLatKeys;
+#pragma unroll
+        for (int kk = 0; kk < 4 * C::kCH; ++kk) {
+          if (kk >= L / 16 && kk - L / 16 >= rope_steps) break;
+          const uint64_t ad = smem_desc_sw128(qb + (kk >> 2) * C::kQCB + (kk & 3) * 32, 16, 1024);
+          const uint64_t bd =
+              smem_desc_sw128(kb + (kk >> 2) * 1024 + (kk & 3) * 32, 16, C::kGroup);
+          umma_f16_ss_warp(tS, ad, bd, kIdQK, kk > 0 ? 1u : 0u);
+        }
+        umma_commit_warp(&s_full[qk.i & 1]);
+        if (qk.n == qk.nt - 1) umma_commit_warp(q_empty);
+        qk.step(p, rank);
+      } else {
+        const bool late = global_timer_ns() - since > kWaitLimitNs;
+        if (__any_sync(0xffffffffu, late || *abort_flag != 0)) {
+          if (*abort_flag == 0 && lane == 0) atomicOr(p.status, DEV_TIMEOUT);
+          *abort_flag = 1;
+          break;
+        }
+        continue;
       }
-      it += s.nt;
-      ++sg;
+      since = global_timer_ns();
     }
     // nothing may still be in flight on the tensor cores when the memory is freed
     umma_commit_warp(fin);
     mbar_wait_bounded(fin, 0, p.status, DEV_TIMEOUT);
   } else {
     // ======================================================== softmax, rescale, epilogue
-    // An M = 64 accumulator keeps rows 16 w .. 16 w + 15 in the first half of warp w's lanes.
-    const bool has_row = lane < 16;
-    const int r = 16 * warp + (lane & 15);
+    // An M = 64 accumulator keeps rows 16 w .. 16 w + 15 in the first half of warp w's lanes.  A
+    // lane reads two of them, rows ra and ra + 8, columns 8 g + 2 cq and the next: four lanes a row.
+    const int ra = 16 * warp + (lane >> 2), cq = lane & 3;
     const uint32_t lane_off = (32u * warp) << 16;
     const uint32_t tO = tmem + C::kTmemO + lane_off;
     const float c = p.scale * kLog2e;
@@ -431,84 +493,84 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
       if (w.j == 0 && !whole)
         meta = make_int4(grow0, rows,
                          static_cast<int>((w.pos + w.kt - 1) / w.share) - worker + 1, 0);
-      const bool rv = has_row && r < rows;
-      const int i_q = (s.row0 + min(r, rows - 1)) / p.heads;  // the row's token
-      const int32_t* tree = p.tree == nullptr || !rv
-                                ? nullptr
-                                : p.tree + (static_cast<long long>(w.q0) + i_q) * p.tree_stride;
+      const bool rv[2] = {ra < rows, ra + 8 < rows};
+      int i_q[2];  // the rows' tokens
+#pragma unroll
+      for (int k = 0; k < 2; ++k) i_q[k] = (s.row0 + min(ra + 8 * k, rows - 1)) / p.heads;
       // keys that every row of the tile sees without looking at its mask
       const int clear = min(w.kv_len, p.tree != nullptr ? s.ctx : s.ctx + s.row0 / p.heads + 1);
-      float m = -INFINITY, l = 0.f;
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // (l: this lane's columns)
       for (int n = 0; n < s.nt; ++n, ++it) {
         ok = pf_wait_warp(&s_full[it & 1], (it >> 1) & 1, abort_flag, p.status) && ok;
         tc_fence_after();
         const int k0 = (s.j0 + n) * kLatKeys;
-        const uint32_t tS = tmem + (it & 1) * kLatKeys + lane_off;
-        uint32_t xa[32], xb[32];
-        tmem_ld32(tS, xa);
-        tmem_ld32(tS + 32, xb);
+        uint32_t x[32];  // [g][row][2]
+        tmem_ld_16x256b_x8(tmem + (it & 1) * kLatKeys + lane_off, x);
         tmem_ld_wait();
         if (k0 + kLatKeys > clear) {
-          // the keys that the row sees: of the prefix (tree) or up to its own, and those its
-          // mask names
-          const int end = min(w.kv_len, p.tree != nullptr ? s.ctx : s.ctx + i_q + 1) - k0;
-          uint32_t ma = low_bits(end), mb = low_bits(end - 32);
-          if (tree != nullptr) {
-            const int last = w.kv_len - k0;
-            ma |= mask_bits32(tree, p.tree_words, k0 - s.ctx) & low_bits(last) &
-                  ~low_bits(s.ctx - k0);
-            mb |= mask_bits32(tree, p.tree_words, k0 + 32 - s.ctx) & low_bits(last - 32) &
-                  ~low_bits(s.ctx - k0 - 32);
+          // the keys that a row sees: of the prefix (tree) or up to its own, and those its mask
+          // names
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int end = min(w.kv_len, p.tree != nullptr ? s.ctx : s.ctx + i_q[k] + 1) - k0;
+            uint32_t lo = low_bits(end), hi = low_bits(end - 32);
+            if (p.tree != nullptr && rv[k]) {
+              const int32_t* row = p.tree + (static_cast<long long>(w.q0) + i_q[k]) * p.tree_stride;
+              const int last = w.kv_len - k0;
+              lo |= mask_bits32(row, p.tree_words, k0 - s.ctx) & low_bits(last) &
+                    ~low_bits(s.ctx - k0);
+              hi |= mask_bits32(row, p.tree_words, k0 + 32 - s.ctx) & low_bits(last - 32) &
+                    ~low_bits(s.ctx - k0 - 32);
+            }
+            lo >>= 2 * cq;
+            hi >>= 2 * cq;
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              const uint32_t two = (g < 4 ? lo : hi) >> (8 * (g & 3));
+              if (!(two & 1u)) x[4 * g + 2 * k] = 0xff800000u;
+              if (!(two & 2u)) x[4 * g + 2 * k + 1] = 0xff800000u;
+            }
           }
+        }
+        float alpha[2];
+        bool grow = false;
+        uint32_t pk[16];  // [row][g]
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            if (!((ma >> e) & 1u)) xa[e] = 0xff800000u;
-            if (!((mb >> e) & 1u)) xb[e] = 0xff800000u;
+        for (int k = 0; k < 2; ++k) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+            top = fmax3(top, __uint_as_float(x[4 * g + 2 * k]), __uint_as_float(x[4 * g + 2 * k + 1]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * c;
+          // The running max moves only by more than 8 in log2 units (P stays <= 256, inside
+          // f16's range and fp32 sums'), or to a row's first key.
+          alpha[k] = 1.f;
+          if (rv[k] && (top > m[k] + 8.f || (m[k] == -INFINITY && top > -INFINITY))) {
+            alpha[k] = m[k] == -INFINITY ? 0.f : fast_exp2(m[k] - top);
+            m[k] = top;
+            grow = true;
           }
-        }
-        float mx0 = -INFINITY, mx1 = -INFINITY;
+          const float mu = m[k] == -INFINITY ? 0.f : m[k];
+          // P rounded to 16 bits for the MMA (half a step of 2^-8 or 2^-11 of each weight); the
+          // sum is of the unrounded weights
+          float l0 = 0.f, l1 = 0.f;
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          mx0 = fmax3(mx0, __uint_as_float(xa[e]), __uint_as_float(xa[e + 1]));
-          mx1 = fmax3(mx1, __uint_as_float(xb[e]), __uint_as_float(xb[e + 1]));
+          for (int g = 0; g < 8; ++g) {
+            const float a = fast_exp2(fmaf(__uint_as_float(x[4 * g + 2 * k]), c, -mu));
+            const float b = fast_exp2(fmaf(__uint_as_float(x[4 * g + 2 * k + 1]), c, -mu));
+            l0 += a;
+            l1 += b;
+            pk[8 * k + g] = pack_half2<BF16>(a, b);
+          }
+          l[k] = l[k] * alpha[k] + (l0 + l1);
         }
-        const float mx = fmaxf(mx0, mx1) * c;
-        // The running max moves only by more than 8 in log2 units (P stays <= 256, inside f16's
-        // range and fp32 sums'), or to a row's first key.
-        float alpha = 1.f;
-        const bool grow = rv && (mx > m + 8.f || (m == -INFINITY && mx > -INFINITY));
-        if (grow) {
-          alpha = m == -INFINITY ? 0.f : fast_exp2(m - mx);
-          m = mx;
-        }
-        const float mu = m == -INFINITY ? 0.f : m;
-        // P rounded to 16 bits for the MMA (half a step of 2^-8 or 2^-11 of each weight); the
-        // sum is of the unrounded weights
-        uint32_t pk[32];
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float a = fast_exp2(fmaf(__uint_as_float(xa[2 * e]), c, -mu));
-          const float b = fast_exp2(fmaf(__uint_as_float(xa[2 * e + 1]), c, -mu));
-          l0 += a;
-          l1 += b;
-          pk[e] = pack_half2<BF16>(a, b);
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float a = fast_exp2(fmaf(__uint_as_float(xb[2 * e]), c, -mu));
-          const float b = fast_exp2(fmaf(__uint_as_float(xb[2 * e + 1]), c, -mu));
-          l0 += a;
-          l1 += b;
-          pk[16 + e] = pack_half2<BF16>(a, b);
-        }
-        l = l * alpha + (l0 + l1);
         // P's buffer and O are free when the P.V before is done
         if (it > 0) ok = pf_wait_warp(pv_done, (it - 1) & 1, abort_flag, p.status) && ok;
         tc_fence_after();
         if (n > 0) {
           float* const f = sF + (it & 1) * kLatRows;
-          if (has_row) f[r] = alpha;
+          if (cq == 0) f[ra] = alpha[0], f[ra + 8] = alpha[1];
           if (named_bar_any(1, 128, grow)) {
 #pragma unroll 1
             for (int cc = 0; cc < C::kMB * 2; ++cc) {
@@ -528,12 +590,12 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
             tmem_st_wait();
           }
         }
-        if (has_row) {
 #pragma unroll
-          for (int ch = 0; ch < 8; ++ch)
-            *reinterpret_cast<uint4*>(sP + r * 128 + ((ch ^ (r & 7)) << 4)) =
-                make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
-        }
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+            *reinterpret_cast<uint32_t*>(sP + (ra + 8 * k) * 128 + ((g ^ (ra & 7)) << 4) + 4 * cq) =
+                pk[8 * k + g];
         // Cache slots at or past kv_len may hold anything (NaN included): those that a copy of
         // eight rows brought in become zeros before they meet P = 0.
         if (k0 + kLatKeys > w.kv_len && (w.kv_len & 7) != 0) {
@@ -552,22 +614,28 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
       }
 
       // ---- epilogue: O / l of a tile that is this worker's alone, else the partial rows
-      const float inv = l == 0.f ? 0.f : 1.f / l;  // (a row that saw no key is 0; NaN stays)
       float* const f = sF + (it & 1) * kLatRows;
       if (s.nt > 0) {
         ok = pf_wait_warp(pv_done, (it - 1) & 1, abort_flag, p.status) && ok;
         tc_fence_after();
       }
-      if (rv && ok) {
-        if (whole) {
-          if (p.lse != nullptr)
-            p.lse[grow0 + r] = latent_lse(m, l);
-        } else {
-          p.ws_m[slot * kLatRows + r] = m;
-          p.ws_l[slot * kLatRows + r] = l;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float sum = l[k];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const int r = ra + 8 * k;
+        if (cq != 0) continue;
+        // (a row that saw no key is 0; NaN stays)
+        f[r] = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+        if (!rv[k] || !ok) continue;
+        if (!whole) {
+          p.ws_m[slot * kLatRows + r] = m[k];
+          p.ws_l[slot * kLatRows + r] = sum;
+        } else if (p.lse != nullptr) {
+          p.lse[grow0 + r] = latent_lse(m[k], sum);
         }
       }
-      if (has_row) f[r] = whole ? inv : 1.f;
       named_bar_sync(1, 128);
       const int d = 32 * warp + lane;  // this lane's element of a 128-element block of O
       if (ok && (whole || s.nt > 0)) {  // (an empty partial row's sum is 0: its elements are not read)
@@ -583,15 +651,27 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0u;
           }
+          if (!whole) {
+            float* const dst = p.ws_acc + static_cast<size_t>(slot * kLatRows + rb) * L + blk + d;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 32; ++e)
+              if (rb + e < rows) dst[static_cast<size_t>(e) * L] = __uint_as_float(o[e]);
+            continue;
+          }
+          // Two rows at a time: an even lane takes both its own and its neighbour's element of the
+          // first, an odd one of the second, so that a store has two elements.
+          const size_t at = static_cast<size_t>(grow0 + rb) * L + blk + (d & ~1);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
             if (rb + e >= rows) break;
-            const float v = __uint_as_float(o[e]);
-            if (whole)
-              store_as(p.out, static_cast<size_t>(grow0 + rb + e) * L + blk + d,
-                       f[rb + e] == 0.f ? 0.f : v * f[rb + e], p.out_dtype);
-            else
-              p.ws_acc[static_cast<size_t>(slot * kLatRows + rb + e) * L + blk + d] = v;
+            const float f0 = f[rb + e], f1 = f[rb + e + 1];
+            const float v0 = f0 == 0.f ? 0.f : __uint_as_float(o[e]) * f0;
+            const float v1 = f1 == 0.f ? 0.f : __uint_as_float(o[e + 1]) * f1;
+            const bool odd = lane & 1;
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+            const float a = odd ? got : v0, b = odd ? v1 : got;
+            if (rb + e + (odd ? 1 : 0) < rows)
+              store_two(p.out, at + static_cast<size_t>(e + (odd ? 1 : 0)) * L, a, b, p.out_dtype);
           }
         }
       }
