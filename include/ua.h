@@ -481,7 +481,8 @@ typedef struct {
  * j of the sequence whose bit j - (kv_len - q_len) is set in the row's mask (no other rule: a
  * token sees itself only if its own bit is set).  A row that sees no key is written as 0.  Every
  * slot below kv_len must hold finite values (their weight may be 0, but they are multiplied); slots
- * past it may hold anything.  Every block size works; multiples of 8 load eight rows at a time.
+ * past it may hold anything.  Every block size works; a copy takes as many rows at a time as the
+ * largest power of two that divides it (up to 64).
  * Returns UA_ERR_UNSUPPORTED where total_q * num_heads or num_blocks * block_size passes 31 bits,
  * UA_ERR_WORKSPACE where `workspace` is smaller than ua_latent_workspace_bytes().
  */

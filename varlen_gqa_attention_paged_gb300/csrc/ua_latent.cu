@@ -131,20 +131,13 @@ void shape(const ua_latent_t& a, int sms, int* workers, int* cl) {
       std::max(1LL, std::min(most, (tiles * keys + kMinShare - 1) / kMinShare)));
 }
 
-// Maps of a matrix of rows [L + R]: `box` rows of the latent part's column blocks, and of any one.
-bool row_maps(CUtensorMap* lat, CUtensorMap* row, const void* base, bool bf16, long long rows,
-              int latent, int rope, int box_rows) {
-  const cuuint64_t width = static_cast<cuuint64_t>(latent) + rope;
-  const cuuint64_t n = static_cast<cuuint64_t>(rows);
-  const cuuint64_t dims3[3] = {64, n, static_cast<cuuint64_t>(latent) / 64};
-  const cuuint64_t strides3[2] = {width * 2, 128};
-  const cuuint32_t box3[3] = {64, static_cast<cuuint32_t>(box_rows),
-                              static_cast<cuuint32_t>(latent) / 64};
-  const cuuint64_t dims2[2] = {width, n};
-  const cuuint64_t strides2[1] = {width * 2};
-  const cuuint32_t box2[2] = {64, static_cast<cuuint32_t>(box_rows)};
-  return ua::encode_half_map(lat, base, bf16, 3, dims3, strides3, box3) &&
-         ua::encode_half_map(row, base, bf16, 2, dims2, strides2, box2);
+// Rows [width] in boxes of 64 elements x `box_rows`.
+bool row_map(CUtensorMap* map, const void* base, bool bf16, long long rows, int width,
+             int box_rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(width) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  return ua::encode_half_map(map, base, bf16, 2, dims, strides, box);
 }
 
 int attend(const ua_latent_t& a, cudaStream_t st) {
@@ -170,12 +163,12 @@ int attend(const ua_latent_t& a, cudaStream_t st) {
     return rc;
   }
   const bool bf16 = a.dtype == UA_DT_BF16;
-  p.box_rows = a.block_size % 8 == 0 ? 8 : 1;
-  if (!row_maps(&p.q_lat, &p.q_row, a.q, bf16, static_cast<long long>(a.total_q) * a.num_heads,
-                a.latent_dim, a.rope_dim, ua::kLatRows) ||
-      !row_maps(&p.k_lat, &p.k_row, a.cache, bf16,
-                static_cast<long long>(a.num_blocks) * a.block_size, a.latent_dim, a.rope_dim,
-                p.box_rows))
+  p.box_rows = std::min(ua::kLatKeys, a.block_size & -a.block_size);
+  const int width = a.latent_dim + a.rope_dim;
+  if (!row_map(&p.q_map, a.q, bf16, static_cast<long long>(a.total_q) * a.num_heads, width,
+               ua::kLatRows) ||
+      !row_map(&p.k_map, a.cache, bf16, static_cast<long long>(a.num_blocks) * a.block_size, width,
+               p.box_rows))
     return UA_ERR_CUDA;
   p.out = a.out;
   p.lse = a.lse;

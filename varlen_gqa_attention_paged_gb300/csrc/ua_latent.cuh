@@ -12,7 +12,7 @@
 // O takes 256 of tensor memory's 512 columns, which as rows x L it would take whole, with no
 // room for S.  A key tile (64 keys x (L + R), 73.7 KB) is loaded once and read twice, as K and as
 // V; two of them and Q fill the shared memory, so P has one buffer and the softmax of tile j + 1
-// hands it over when P.V of tile j is done.
+// hands it over when P.V of tile j is done, and a tile changes hands in three parts.
 //
 // Work split: all (row tile, key tile) pairs of the batch, row tile after row tile, are cut into
 // equal shares for the workers (one CTA, or two that take neighbouring row tiles of a sequence over
@@ -36,8 +36,13 @@ struct LatentCfg {
   static constexpr int kMB = L / 128;            // accumulators of O^T
   static constexpr int kQCB = kLatRows * 128;    // one column block of Q
   static constexpr int kQBytes = kCH * kQCB;
-  static constexpr int kGroup = kCH * 1024;      // eight keys: every column block's 8 x 128 bytes
-  static constexpr int kTileBytes = kLatKeys / 8 * kGroup;
+  static constexpr int kKCB = kLatKeys * 128;    // one column block of a key tile
+  static constexpr int kTileBytes = kCH * kKCB;
+  // Parts of a key tile, which change hands one by one: the rope part (only Q K^T reads it), then
+  // the latent part's halves.
+  static constexpr int kHalves = kMB > 1 ? 2 : 1;
+  static constexpr int kParts = 1 + kHalves;
+  static constexpr int kHalfMB = kMB / kHalves;
   static constexpr int kPBytes = kLatRows * 128;
   static constexpr int kSmallBytes = 1024;       // barriers, rescale factors
   static constexpr int kFit =
@@ -47,9 +52,9 @@ struct LatentCfg {
       1024 + kQBytes + kStages * kTileBytes + kPBytes + kSmallBytes;
   static constexpr int kTmemO = 2 * kLatKeys;    // two S buffers, then O^T
   static constexpr int kTmemCols = kTmemO + kMB * kLatRows > 256 ? 512 : 256;
-  static constexpr int kThreads = 192;           // four softmax warps, MMA issue, copies
-  static_assert(L % 128 == 0 && L <= 512);
-  static_assert(kStages >= 2 && kSmemBytes + 16 <= 227 * 1024);
+  static constexpr int kThreads = 32 * (6 + kParts);  // softmax (4), MMA issue (2), a part's copies each
+  static_assert(L % 128 == 0 && L <= 512 && kMB % kHalves == 0);
+  static_assert(kStages >= 2 && kSmemBytes + 64 <= 227 * 1024);
 };
 
 // A worker's walk over its share: segments of consecutive key tiles of one row tile.  Every warp
@@ -160,16 +165,19 @@ struct LatentSeg {
   }
 };
 
-// Whether `v` holds in any of the barrier's threads; a barrier too.
-__device__ __forceinline__ bool named_bar_any(int id, int threads, bool v) {
-  uint32_t r;
+// D[tmem] (+)= A[smem] * B[smem], 128-byte swizzle, stride byte offset 1024 (eight rows), issued by
+// one lane of a converged warp; operands by their address / 16 and leading byte offset.
+__device__ __forceinline__ void umma_f16_ss_at(uint32_t d_tmem, uint32_t a16, uint32_t a_lbo,
+                                               uint32_t b16, uint32_t b_lbo, uint32_t idesc,
+                                               uint32_t accumulate) {
+  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(threads)
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a16 + ((a_lbo >> 4) << 16)), "r"(b16 + ((b_lbo >> 4) << 16)), "r"(hi), "r"(idesc),
+      "r"(accumulate)
       : "memory");
-  return r != 0;
 }
 
 // Bits [at, at + 32) of a row of words (at may be negative; words past the row are 0).
@@ -196,19 +204,6 @@ __device__ __forceinline__ void store_two(void* out, size_t at, float a, float b
   else
     *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + at) =
         dtype == UA_DT_BF16 ? pack_bf16(a, b) : pack_f16(a, b);
-}
-
-// Whether the phase of `parity` is complete, for a whole warp, without waiting.
-__device__ __forceinline__ bool mbar_test_warp(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return __all_sync(0xffffffffu, ok != 0);
 }
 
 // 16 lanes x 64 columns of an accumulator over a warp: register 4 g + 2 k + e of lane t holds row
@@ -251,16 +246,21 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
   uint64_t* const pv_done = bars + 5;
   uint64_t* const o_empty = bars + 6;
   uint64_t* const fin = bars + 7;
-  uint64_t* const k_full = bars + 8;   // [S]
-  uint64_t* const k_empty = k_full + S;  // [S][2]: of a tile's first and second half
-  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(k_empty + 2 * S);
-  float* const sF = reinterpret_cast<float*>(bars + 32);  // [2][64] factors of O's rows
+  uint64_t* const grown = bars + 8;    // the tile's rescale factors are written
+  uint64_t* const s_empty = bars + 9;  // [2]
+  uint64_t* const k_full = bars + 11;  // [S][parts]
+  uint64_t* const k_empty = k_full + S * C::kParts;
+  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(k_empty + S * C::kParts);
+  float* const sF = reinterpret_cast<float*>(bars + 64);  // [2][64] factors of O's rows
+  static_assert(8 * (11 + 2 * S * C::kParts) + 4 <= 512 && 512 + 512 <= C::kSmallBytes);
   __shared__ int s_abort;
+  // [tile mod 2][warp]: the tile + 1, if a row of the warp's moved its max in it
+  __shared__ int s_grow[2][4];
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int worker = blockIdx.x / p.cl, rank = blockIdx.x % p.cl;
-  constexpr int kMma = 4, kCopy = 5;
+  constexpr int kQk = 4, kPv = 5, kCopy = 6;  // (kCopy + g copies part g)
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -270,21 +270,25 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
     mbar_init(p_full, 4);
     mbar_init(pv_done, 1);
     mbar_init(o_empty, 4);
-    mbar_init(fin, 1);
-    for (int i = 0; i < S; ++i) mbar_init(&k_full[i], 1);
-    for (int i = 0; i < 2 * S; ++i) mbar_init(&k_empty[i], 1);
+    mbar_init(fin, 2);
+    mbar_init(grown, 4);
+    mbar_init(&s_empty[0], 4);
+    mbar_init(&s_empty[1], 4);
+    for (int i = 0; i < S * C::kParts; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
     s_abort = 0;
+    for (int i = 0; i < 8; ++i) s_grow[i >> 2][i & 3] = 0;
     mbar_fence_init();
   }
-  if (warp == kMma) {
+  if (warp == kQk) {
     tmem_alloc(tmem_holder, C::kTmemCols);
     tmem_relinquish();
   }
   if (warp == kCopy && lane == 0) {
-    tma_prefetch_desc(&p.q_lat);
-    tma_prefetch_desc(&p.q_row);
-    tma_prefetch_desc(&p.k_lat);
-    tma_prefetch_desc(&p.k_row);
+    tma_prefetch_desc(&p.q_map);
+    tma_prefetch_desc(&p.k_map);
   }
   tc_fence_before();
   __syncthreads();
@@ -299,38 +303,45 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
   int sg = 0;  // segments with key tiles so far
   bool ok = true;
 
-  if (warp == kCopy) {
+  if (warp >= kCopy) {
     // ======================================================== copies
+    // A warp a part of the tiles, each copied as soon as its place is free: Q K^T frees the rope
+    // part's, the P.V of a half the half's.  (One warp for all parts took 1000 cycles a part.)
+    const int g = warp - kCopy;
+    const int cb0 = g == 0 ? C::kCB : 2 * C::kHalfMB * (g - 1);
+    const int blocks = g == 0 ? 1 : 2 * C::kHalfMB;
     const int bs = p.block_size;
     const int oob = p.num_blocks * bs;
-    const int per_lane = p.box_rows == 8 ? 1 : 2;  // boxes of a tile that a lane loads
+    const int bw = p.box_rows, nb = kLatKeys / bw;  // keys of a box, boxes of a column block
     for (; ok && w.left > 0; w.next(p)) {
       const LatentSeg s(p, w, rank);
       if (s.nt <= 0) continue;
-      if (sg > 0 && !pf_wait_warp(q_empty, (sg - 1) & 1, abort_flag, p.status)) { ok = false; break; }
-      if (lane == 0) {
+      if (g == 0 && sg > 0 && !pf_wait_warp(q_empty, (sg - 1) & 1, abort_flag, p.status)) {
+        ok = false;
+        break;
+      }
+      if (g == 0 && lane == 0) {
         const int row = w.q0 * p.heads + s.row0;
         mbar_arrive_expect_tx(q_full, C::kQBytes);
-        tma_load_3d_pf(sQ, &p.q_lat, 0, row, 0, q_full);
-        tma_load_2d(sQ + C::kCB * C::kQCB, &p.q_row, L, row, q_full);
+        for (int cb = 0; cb < C::kCH; ++cb)
+          tma_load_2d(sQ + cb * C::kQCB, &p.q_map, 64 * cb, row, q_full);
       }
       ++sg;
       const int32_t* bt = p.block_table + static_cast<size_t>(w.b) * p.max_blocks_per_seq;
-      // the block of this lane's box i of key tile j, loaded two tiles ahead of its use
-      auto key_of = [&](int j, int i) -> int {
-        return j * kLatKeys + (p.box_rows == 8 ? 8 * lane : lane + 32 * i);
-      };
+      // the block of this lane's box (its second, of 64 boxes) of key tile j, loaded two tiles
+      // ahead of its use
       auto block_of = [&](int j, int i) -> int {
-        if (j >= s.j0 + s.nt || i >= per_lane || (p.box_rows == 8 && lane >= 8)) return -1;
-        const int key = key_of(j, i), col = key / bs;
-        return key < w.kv_len && col < p.max_blocks_per_seq ? __ldg(bt + col) : -1;
+        const int box = lane + 32 * i, key = j * kLatKeys + box * bw, col = key / bs;
+        return j < s.j0 + s.nt && box < nb && key < w.kv_len && col < p.max_blocks_per_seq
+                   ? __ldg(bt + col)
+                   : -1;
       };
       // its cache row (past the cache, so that the copy fills zeros, where there is no key)
       auto row_of = [&](int j, int i, int blk) -> int {
-        const int key = key_of(j, i);
-        if (key >= w.kv_len || (p.box_rows == 8 && lane >= 8)) return oob;
+        const int box = lane + 32 * i, key = j * kLatKeys + box * bw;
+        if (box >= nb || key >= w.kv_len) return oob;
         if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
-          atomicOr(p.status, DEV_BAD_BLOCK);
+          if (g == 0) atomicOr(p.status, DEV_BAD_BLOCK);
           return oob;
         }
         return blk * bs + key % bs;
@@ -341,38 +352,28 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
         blk0[i] = block_of(s.j0, i);
         blk1[i] = block_of(s.j0 + 1, i);
       }
-      for (int n = 0; n < s.nt; ++n, ++it) {
+      for (int n = 0; ok && n < s.nt; ++n, ++it) {
         const int j = s.j0 + n, st = it % S;
         uint8_t* const tile = sK + st * C::kTileBytes;
         const int row0 = row_of(j, 0, blk0[0]);
-        const int row1 = p.box_rows == 8 ? 0 : row_of(j, 1, blk0[1]);
-        // a tile's halves are free one after the other
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (it >= S && !pf_wait_warp(&k_empty[2 * st + half], ((it / S) - 1) & 1, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          // (only now: the tile before has arrived, so that its phase of the barrier is over)
-          if (half == 0) {
-            if (lane == 0) mbar_arrive_expect_tx(&k_full[st], C::kTileBytes);
-            __syncwarp();
-          }
-          if (p.box_rows == 8) {
-            if ((lane >> 2) == half) {
-              uint8_t* const dst = tile + lane * C::kGroup;
-              tma_load_3d_pf(dst, &p.k_lat, 0, row0, 0, &k_full[st]);
-              tma_load_2d(dst + C::kCB * 1024, &p.k_row, L, row0, &k_full[st]);
-            }
-          } else {
-            const int k = lane + 32 * half;
-            uint8_t* const dst = tile + (k >> 3) * C::kGroup + (k & 7) * 128;
-#pragma unroll 1
-            for (int cb = 0; cb < C::kCH; ++cb)
-              tma_load_2d(dst + cb * 1024, &p.k_row, 64 * cb, half ? row1 : row0, &k_full[st]);
-          }
+        const int row1 = nb > 32 ? row_of(j, 1, blk0[1]) : oob;
+        uint64_t* const full = &k_full[st * C::kParts + g];
+        if (it >= S && !pf_wait_warp(&k_empty[st * C::kParts + g], ((it / S) - 1) & 1, abort_flag,
+                                     p.status)) {
+          ok = false;
+          break;
         }
-        if (!ok) break;
+        // (only now: the tile before has arrived, so that its phase of the barrier is over)
+        if (lane == 0) mbar_arrive_expect_tx(full, blocks * C::kKCB);
+        __syncwarp();
+        for (int e = lane; e - lane < blocks * nb; e += 32) {
+          const int cb = cb0 + e / nb, box = e % nb;
+          const int lo = __shfl_sync(0xffffffffu, row0, box & 31);
+          const int hi = __shfl_sync(0xffffffffu, row1, box & 31);
+          if (e < blocks * nb)
+            tma_load_2d(tile + cb * C::kKCB + box * bw * 128, &p.k_map, 64 * cb,
+                        box < 32 ? lo : hi, full);
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           blk0[i] = blk1[i];
@@ -381,95 +382,87 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
       }
     }
     // never leave copies in flight into this CTA's shared memory (even after an abort)
-    // (a tile that was left half copied never completes: its first half has long arrived when the
-    // wait for it gives up)
-    for (int i = max(0, it - S + (ok ? 0 : 1)); i < it + (ok ? 0 : 1); ++i)
-      mbar_wait_bounded(&k_full[i % S], (i / S) & 1, p.status, DEV_TIMEOUT);
-    if (sg > 0) mbar_wait_bounded(q_full, (sg - 1) & 1, p.status, DEV_TIMEOUT);
-  } else if (warp == kMma) {
-    // ======================================================== MMA issue
-    // Two cursors over the worker's tiles, of S = Q K^T and of O^T += V^T P^T; whichever has its
-    // inputs goes next, P.V first (it frees its tile).  S_{i+2} overwrites S_i, which the softmax
-    // has read when P_i is ready.  The MMAs are unrolled: in a rolled loop an issue took 52 cycles
-    // a 64 x 64 x 16 product instead of the 33 that it takes to run.
-    constexpr uint32_t kIdQK = umma_idesc_f16(kLatRows, kLatKeys, BF16, false);
-    constexpr uint32_t kIdPV = umma_idesc_f16(128, kLatRows, BF16, false) | (1u << 15);
+    for (int i = max(0, it - S); i < it; ++i)
+      mbar_wait_bounded(&k_full[i % S * C::kParts + g], (i / S) & 1, p.status, DEV_TIMEOUT);
+    if (g == 0 && sg > 0) mbar_wait_bounded(q_full, (sg - 1) & 1, p.status, DEV_TIMEOUT);
+  } else if (warp == kQk) {
+    // ======================================================== MMA issue: S = Q K^T
+    // A warp issues these products and another P.V's, so that neither waits behind the other's
+    // inputs (one that took whichever was ready spent 350 cycles a look).  The MMAs are unrolled:
+    // in a rolled loop an issue took 52 cycles a 64 x 64 x 16 product instead of the 33 that it
+    // takes to run.
+    constexpr uint32_t kId = umma_idesc_f16(kLatRows, kLatKeys, BF16, false);
     const int rope_steps = p.rope_dim / 16;
-    struct Cursor {
-      LatentWalk w;
-      int n, nt, sg, i;  // tile of the segment, its tiles, segments and tiles before
-      __device__ __forceinline__ void seek(const LatentParams& p, int rank) {
-        n = nt = 0;
-        for (; w.left > 0; w.next(p)) {
-          const LatentSeg s(p, w, rank);
-          if (s.nt > 0) {
-            nt = s.nt;
-            return;
-          }
-        }
-      }
-      __device__ __forceinline__ void step(const LatentParams& p, int rank) {
-        ++i;
-        if (++n < nt) return;
-        ++sg;
-        w.next(p);
-        seek(p, rank);
-      }
-    };
-    Cursor qk{w, 0, 0, 0, 0};
-    qk.seek(p, rank);
-    Cursor pv = qk;
-    unsigned long long since = global_timer_ns();
-    while (pv.nt > 0) {
-      if (pv.i < qk.i && mbar_test_warp(p_full, pv.i & 1) &&
-          (pv.n > 0 || pv.sg == 0 || mbar_test_warp(o_empty, (pv.sg - 1) & 1))) {
-        const int st = pv.i % S;
-        tc_fence_after();
-        const uint32_t vb = smem_addr(sK + st * C::kTileBytes), pb = smem_addr(sP);
-#pragma unroll
-        for (int ks = 0; ks < kLatKeys / 16; ++ks) {
-#pragma unroll
-          for (int mb = 0; mb < C::kMB; ++mb) {
-            const uint64_t ad =
-                smem_desc_sw128(vb + ks * 2 * C::kGroup + mb * 2048, 1024, C::kGroup);
-            const uint64_t bd = smem_desc_sw128(pb + ks * 32, 16, 1024);
-            umma_f16_ss_warp(tmem + C::kTmemO + mb * kLatRows, ad, bd, kIdPV,
-                             pv.n > 0 || ks > 0 ? 1u : 0u);
-          }
-          if (ks == kLatKeys / 32 - 1) umma_commit_warp(&k_empty[2 * st]);
-        }
-        umma_commit_warp(pv_done);
-        umma_commit_warp(&k_empty[2 * st + 1]);
-        pv.step(p, rank);
-      } else if (qk.nt > 0 && qk.i < pv.i + 2 && mbar_test_warp(&k_full[qk.i % S], (qk.i / S) & 1) &&
-                 (qk.n > 0 || mbar_test_warp(q_full, qk.sg & 1))) {
-        const int st = qk.i % S;
-        tc_fence_after();
-        const uint32_t qb = smem_addr(sQ), kb = smem_addr(sK + st * C::kTileBytes);
-        const uint32_t tS = tmem + (qk.i & 1) * kLatKeys;
-#pragma unroll
-        for (int kk = 0; kk < 4 * C::kCH; ++kk) {
-          if (kk >= L / 16 && kk - L / 16 >= rope_steps) break;
-          const uint64_t ad = smem_desc_sw128(qb + (kk >> 2) * C::kQCB + (kk & 3) * 32, 16, 1024);
-          const uint64_t bd =
-              smem_desc_sw128(kb + (kk >> 2) * 1024 + (kk & 3) * 32, 16, C::kGroup);
-          umma_f16_ss_warp(tS, ad, bd, kIdQK, kk > 0 ? 1u : 0u);
-        }
-        umma_commit_warp(&s_full[qk.i & 1]);
-        if (qk.n == qk.nt - 1) umma_commit_warp(q_empty);
-        qk.step(p, rank);
-      } else {
-        const bool late = global_timer_ns() - since > kWaitLimitNs;
-        if (__any_sync(0xffffffffu, late || *abort_flag != 0)) {
-          if (*abort_flag == 0 && lane == 0) atomicOr(p.status, DEV_TIMEOUT);
-          *abort_flag = 1;
+    for (; ok && w.left > 0; w.next(p)) {
+      const LatentSeg s(p, w, rank);
+      if (s.nt <= 0) continue;
+      ok = pf_wait_warp(q_full, sg & 1, abort_flag, p.status);
+      for (int n = 0; ok && n < s.nt; ++n, ++it) {
+        const int st = it % S;
+        const uint32_t qd = smem_addr(sQ) >> 4, kd = smem_addr(sK + st * C::kTileBytes) >> 4;
+        const uint32_t tS = tmem + (it & 1) * kLatKeys;
+        uint64_t* const full = &k_full[st * C::kParts];
+        // the scores of two tiles before have been read
+        if (it >= 2 && !pf_wait_warp(&s_empty[it & 1], ((it >> 1) - 1) & 1, abort_flag, p.status)) {
+          ok = false;
           break;
         }
-        continue;
+        if (!pf_wait_warp(&full[0], (it / S) & 1, abort_flag, p.status)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          if (kk < rope_steps)
+            umma_f16_ss_at(tS, qd + (C::kCB * C::kQCB) / 16 + 2 * kk, 16,
+                           kd + (C::kCB * C::kKCB) / 16 + 2 * kk, 16, kId, kk > 0 ? 1u : 0u);
+        umma_commit_warp(&k_empty[st * C::kParts]);
+#pragma unroll
+        for (int g = 0; g < C::kHalves; ++g) {
+          if (!pf_wait_warp(&full[1 + g], (it / S) & 1, abort_flag, p.status)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 8 * C::kHalfMB; ++k) {
+            const int kk = g * 8 * C::kHalfMB + k;
+            umma_f16_ss_at(tS, qd + (kk >> 2) * (C::kQCB / 16) + (kk & 3) * 2, 16,
+                           kd + (kk >> 2) * (C::kKCB / 16) + (kk & 3) * 2, 16, kId, 1u);
+          }
+        }
+        if (!ok) break;
+        umma_commit_warp(&s_full[it & 1]);
+        if (n == s.nt - 1) umma_commit_warp(q_empty);
       }
-      since = global_timer_ns();
+      ++sg;
     }
     // nothing may still be in flight on the tensor cores when the memory is freed
+    umma_commit_warp(fin);
+    mbar_wait_bounded(fin, 0, p.status, DEV_TIMEOUT);
+  } else if (warp == kPv) {
+    // ======================================================== MMA issue: O^T += V^T P^T
+    constexpr uint32_t kId = umma_idesc_f16(128, kLatRows, BF16, false) | (1u << 15);
+    for (; ok && w.left > 0; w.next(p)) {
+      const LatentSeg s(p, w, rank);
+      if (s.nt <= 0) continue;
+      for (int n = 0; n < s.nt; ++n, ++it) {
+        const int st = it % S;
+        if (!pf_wait_warp(p_full, it & 1, abort_flag, p.status) ||
+            (n == 0 && sg > 0 && !pf_wait_warp(o_empty, (sg - 1) & 1, abort_flag, p.status))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t vd = smem_addr(sK + st * C::kTileBytes) >> 4, pd = smem_addr(sP) >> 4;
+#pragma unroll
+        for (int mb = 0; mb < C::kMB; ++mb) {
+#pragma unroll
+          for (int ks = 0; ks < kLatKeys / 16; ++ks)
+            umma_f16_ss_at(tmem + C::kTmemO + mb * kLatRows, vd + (mb * 2 * C::kKCB + ks * 2048) / 16,
+                           C::kKCB, pd + ks * 2, 16, kId, ks > 0 ? 1u : n > 0 ? 1u : 0u);
+          if ((mb + 1) % C::kHalfMB == 0)
+            umma_commit_warp(&k_empty[st * C::kParts + 1 + mb / C::kHalfMB]);
+        }
+        umma_commit_warp(pv_done);
+      }
+      ++sg;
+    }
     umma_commit_warp(fin);
     mbar_wait_bounded(fin, 0, p.status, DEV_TIMEOUT);
   } else {
@@ -507,6 +500,9 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
         uint32_t x[32];  // [g][row][2]
         tmem_ld_16x256b_x8(tmem + (it & 1) * kLatKeys + lane_off, x);
         tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[it & 1]);
         if (k0 + kLatKeys > clear) {
           // the keys that a row sees: of the prefix (tree) or up to its own, and those its mask
           // names
@@ -532,9 +528,8 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
             }
           }
         }
-        float alpha[2];
+        float alpha[2], mu[2];
         bool grow = false;
-        uint32_t pk[16];  // [row][g]
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float top = -INFINITY;
@@ -551,14 +546,26 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
             m[k] = top;
             grow = true;
           }
-          const float mu = m[k] == -INFINITY ? 0.f : m[k];
-          // P rounded to 16 bits for the MMA (half a step of 2^-8 or 2^-11 of each weight); the
-          // sum is of the unrounded weights
+          mu[k] = m[k] == -INFINITY ? 0.f : m[k];
+        }
+        // O has every row in every warp's lanes: the factors go round under the exponentials
+        float* const f = sF + (it & 1) * kLatRows;
+        if (n > 0) {
+          if (cq == 0) f[ra] = alpha[0], f[ra + 8] = alpha[1];
+          if (__any_sync(0xffffffffu, grow) && lane == 0) s_grow[it & 1][warp] = it + 1;
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(grown);
+        // P rounded to 16 bits for the MMA (half a step of 2^-8 or 2^-11 of each weight); the sum
+        // is of the unrounded weights
+        uint32_t pk[16];  // [row][g]
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
           float l0 = 0.f, l1 = 0.f;
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
-            const float a = fast_exp2(fmaf(__uint_as_float(x[4 * g + 2 * k]), c, -mu));
-            const float b = fast_exp2(fmaf(__uint_as_float(x[4 * g + 2 * k + 1]), c, -mu));
+            const float a = fast_exp2(fmaf(__uint_as_float(x[4 * g + 2 * k]), c, -mu[k]));
+            const float b = fast_exp2(fmaf(__uint_as_float(x[4 * g + 2 * k + 1]), c, -mu[k]));
             l0 += a;
             l1 += b;
             pk[8 * k + g] = pack_half2<BF16>(a, b);
@@ -568,10 +575,10 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
         // P's buffer and O are free when the P.V before is done
         if (it > 0) ok = pf_wait_warp(pv_done, (it - 1) & 1, abort_flag, p.status) && ok;
         tc_fence_after();
+        ok = pf_wait_warp(grown, it & 1, abort_flag, p.status) && ok;
         if (n > 0) {
-          float* const f = sF + (it & 1) * kLatRows;
-          if (cq == 0) f[ra] = alpha[0], f[ra + 8] = alpha[1];
-          if (named_bar_any(1, 128, grow)) {
+          const volatile int* const at = s_grow[it & 1];
+          if (at[0] == it + 1 || at[1] == it + 1 || at[2] == it + 1 || at[3] == it + 1) {
 #pragma unroll 1
             for (int cc = 0; cc < C::kMB * 2; ++cc) {
               uint32_t o[32];
@@ -596,14 +603,14 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
           for (int g = 0; g < 8; ++g)
             *reinterpret_cast<uint32_t*>(sP + (ra + 8 * k) * 128 + ((g ^ (ra & 7)) << 4) + 4 * cq) =
                 pk[8 * k + g];
-        // Cache slots at or past kv_len may hold anything (NaN included): those that a copy of
-        // eight rows brought in become zeros before they meet P = 0.
-        if (k0 + kLatKeys > w.kv_len && (w.kv_len & 7) != 0) {
-          const int lo = w.kv_len - k0, n0 = 8 - (lo & 7);
-          uint8_t* const tile = sK + (it % S) * C::kTileBytes + (lo >> 3) * C::kGroup;
-          for (int e = threadIdx.x; e < n0 * C::kCB * 8; e += 128) {
-            const int row = (lo & 7) + e / (C::kCB * 8), x = e % (C::kCB * 8);
-            *reinterpret_cast<uint4*>(tile + (x >> 3) * 1024 + row * 128 + (x & 7) * 16) =
+        // Cache slots at or past kv_len may hold anything (NaN included): they become zeros
+        // before they meet P = 0 (a box of a copy that lies past kv_len altogether is zeros).
+        if (k0 + kLatKeys > w.kv_len) {
+          const int lo = w.kv_len - k0, end = min(kLatKeys, (lo + p.box_rows - 1) & -p.box_rows);
+          uint8_t* const tile = sK + (it % S) * C::kTileBytes;
+          for (int e = threadIdx.x; e < (end - lo) * C::kCB * 8; e += 128) {
+            const int row = lo + e / (C::kCB * 8), x = e % (C::kCB * 8);
+            *reinterpret_cast<uint4*>(tile + (x >> 3) * C::kKCB + row * 128 + (x & 7) * 16) =
                 make_uint4(0, 0, 0, 0);
           }
         }
@@ -688,7 +695,7 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kMma) tmem_dealloc(tmem, C::kTmemCols);
+  if (warp == kQk) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 template <int L, bool BF16>

@@ -9,12 +9,11 @@ namespace ua {
 constexpr int kLatRows = 64;
 constexpr int kLatKeys = 64;
 
-// One launch of the absorbed form's kernel.  q is viewed as rows [total_q * heads][L + R] and the
-// cache as rows [num_blocks * block_size][L + R]; each has two maps: boxes of 64 elements x rows x
-// L / 64 column blocks of the latent part, and boxes of 64 elements x rows anywhere in a row
-// (elements past L + R read as zero).
+// One launch of the absorbed form's kernel.  q is mapped as rows [total_q * heads][L + R] in boxes of
+// 64 elements x 64 rows, the cache as rows [num_blocks * block_size][L + R] in boxes of 64 elements x
+// box_rows (elements past L + R read as zero).
 struct LatentParams {
-  CUtensorMap q_lat, q_row, k_lat, k_row;
+  CUtensorMap q_map, k_map;
   void* out;                    // [total_q, heads, L]
   float* lse;                   // [total_q, heads] or null
   const int32_t* cu_seqlens_q;
@@ -33,7 +32,7 @@ struct LatentParams {
   int num_seqs, total_q, max_blocks_per_seq, num_blocks, block_size, heads, rope_dim, out_dtype;
   int workers;                  // groups of `cl` CTAs that share a tile's keys
   int cl;                       // CTAs (tiles of kLatRows rows) of a worker: 1 or 2
-  int box_rows;                 // 8: a box is eight cache rows; 1: one row
+  int box_rows;                 // cache rows of a box: a power of two that divides the block size
   int min_share;                // key tiles that a worker takes at least
   float scale;
 };
