@@ -11,65 +11,35 @@
 
 namespace ua {
 
-// One warp a partial row: with m_k, l_k and acc_k of part k
+// One output row from its partial rows: with m_k, l_k and acc_k of part k
 //   M = max m_k,  L = sum l_k 2^(m_k - M),  out = sum acc_k 2^(m_k - M) / L
-// in the order of the parts.  Block (x, y) takes rows y, y + 8, .. (a warp each 8) of the tile that
-// CTA x began.
+// Blocks (x, y) share the rows of the tile that CTA x began: two warps a row, half of its elements
+// each, or, with many parts of few rows (one long sequence: 152 parts of 2 KB a row), a block a
+// row, an eighth of the parts a warp, joined in shared memory (16 heads over 16000 keys: 20.5 us a
+// call, 41 with a warp a row).  Sums run in a fixed order.
+constexpr int kMergeMany = 16;
+
 template <int L>
 __global__ void __launch_bounds__(256) ua_latent_merge_kernel(
     const __grid_constant__ LatentMergeParams p) {
-  constexpr int kPer = L / 128;  // float4s of a lane
+  constexpr int kVec = L / 4;             // float4s of a row
+  constexpr int kPer = (kVec + 31) / 32;  // of a lane, a warp a row
+  __shared__ float4 s_acc[8][kVec];
+  __shared__ float s_sum[8];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int cta = blockIdx.x;
+  const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 meta = p.ws_meta[cta];
   const int parts = min(meta.z, p.ctas / p.cl - cta / p.cl);
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (r >= min(meta.y, kLatRows) || parts <= 0) return;
-  const long long row = static_cast<long long>(meta.x) + r;
-  if (row < 0 || row >= p.rows) return;
-  auto at = [&](int k) -> size_t {  // part k's row
+  const int rows = static_cast<int>(
+      min(static_cast<long long>(min(meta.y, kLatRows)), p.rows - meta.x));
+  if (parts <= 0 || meta.x < 0) return;
+  auto at = [&](int k, int r) -> size_t {  // part k of row r
     const int slot = k == 0 ? 2 * cta + 1 : 2 * (cta + k * p.cl);
     return static_cast<size_t>(slot) * kLatRows + r;
   };
-  float M = -INFINITY;
-  for (int k = lane; k < parts; k += 32) M = fmaxf(M, p.ws_m[at(k)]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float4 acc[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-  for (int k0 = 0; k0 < parts; k0 += 32) {
-    const int k = k0 + lane;
-    const float l = k < parts ? p.ws_l[at(k)] : 0.f;
-    // (a part that saw no key has no elements either)
-    const float f = l == 0.f ? 0.f : fast_exp2(p.ws_m[at(k)] - M);
-    sum += l == 0.f ? 0.f : l * f;
-    const int n = min(32, parts - k0);
-#pragma unroll 4
-    for (int e = 0; e < n; ++e) {
-      const float fe = __shfl_sync(0xffffffffu, f, e);
-      const float le = __shfl_sync(0xffffffffu, l, e);
-      if (le == 0.f) continue;
-      const float4* a = reinterpret_cast<const float4*>(p.ws_acc + at(k0 + e) * L) + lane;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const float4 v = a[32 * i];
-        acc[i].x += v.x * fe;
-        acc[i].y += v.y * fe;
-        acc[i].z += v.z * fe;
-        acc[i].w += v.w * fe;
-      }
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const float4 v = make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
-    const size_t e = static_cast<size_t>(row) * L + 4 * (lane + 32 * i);
+  auto store = [&](int r, int v4, float4 v) {
+    const size_t e = (static_cast<size_t>(meta.x) + r) * L + 4 * v4;
     if (p.out_dtype == UA_DT_F32) {
       *reinterpret_cast<float4*>(static_cast<float*>(p.out) + e) = v;
     } else {
@@ -78,13 +48,126 @@ __global__ void __launch_bounds__(256) ua_latent_merge_kernel(
           make_uint2(bf ? pack_bf16(v.x, v.y) : pack_f16(v.x, v.y),
                      bf ? pack_bf16(v.z, v.w) : pack_f16(v.z, v.w));
     }
+  };
+  // max over the row's parts; the lane's first part with it
+  auto top_of = [&](int r, float& m0, float& l0) -> float {
+    m0 = lane < parts ? p.ws_m[at(lane, r)] : -INFINITY;
+    l0 = lane < parts ? p.ws_l[at(lane, r)] : 0.f;
+    float M = m0;
+    for (int k = lane + 32; k < parts; k += 32) M = fmaxf(M, p.ws_m[at(k, r)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    return M;
+  };
+  if (parts <= kMergeMany || rows > kLatRows / 2) {
+    constexpr int kHalf = (kPer + 1) / 2;
+    const int half = warp & 1;
+    for (int r = blockIdx.y * 4 + (warp >> 1); r < rows; r += gridDim.y * 4) {
+      float m, l;
+      const float M = top_of(r, m, l);
+      float sum = 0.f;
+      float4 acc[kHalf];
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k0 = 0; k0 < parts; k0 += 32) {
+        if (k0 > 0) {
+          m = k0 + lane < parts ? p.ws_m[at(k0 + lane, r)] : -INFINITY;
+          l = k0 + lane < parts ? p.ws_l[at(k0 + lane, r)] : 0.f;
+        }
+        // (a part that saw no key has no elements either)
+        const float f = l == 0.f ? 0.f : fast_exp2(m - M);
+        sum += l == 0.f ? 0.f : l * f;
+        for (int k = 0; k < min(32, parts - k0); k += 4) {
+          float4 v[4][kHalf];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // (lanes past the parts have l = 0)
+            const float le = __shfl_sync(0xffffffffu, l, k + e);
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i) {
+              const int v4 = (half * kHalf + i) * 32 + lane;
+              v[e][i] = le != 0.f && v4 < kVec
+                            ? reinterpret_cast<const float4*>(p.ws_acc + at(k0 + k + e, r) * L)[v4]
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float fe = __shfl_sync(0xffffffffu, f, k + e);
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i) {
+              acc[i].x += v[e][i].x * fe;
+              acc[i].y += v[e][i].y * fe;
+              acc[i].z += v[e][i].z * fe;
+              acc[i].w += v[e][i].w * fe;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) {
+        const int v4 = (half * kHalf + i) * 32 + lane;
+        if (v4 < kVec)
+          store(r, v4, make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv));
+      }
+      if (p.lse != nullptr && lane == 0 && half == 0)
+        p.lse[meta.x + r] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+    }
+    return;
   }
-  if (p.lse != nullptr && lane == 0)
-    p.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    float m0, l0;
+    const float M = top_of(r, m0, l0);
+    float4 acc[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int k = warp; k < parts; k += 8) {
+      const float l = p.ws_l[at(k, r)], f = l == 0.f ? 0.f : fast_exp2(p.ws_m[at(k, r)] - M);
+      sum += l == 0.f ? 0.f : l * f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float4 v = l != 0.f && 32 * i + lane < kVec
+                             ? reinterpret_cast<const float4*>(p.ws_acc + at(k, r) * L)[32 * i + lane]
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+        acc[i].x += v.x * f;
+        acc[i].y += v.y * f;
+        acc[i].z += v.z * f;
+        acc[i].w += v.w * f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (32 * i + lane < kVec) s_acc[warp][32 * i + lane] = acc[i];
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sum += s_sum[w];
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    for (int v4 = threadIdx.x; v4 < kVec; v4 += 256) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float4 v = s_acc[w][v4];
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+      }
+      store(r, v4, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
+    }
+    if (p.lse != nullptr && threadIdx.x == 0)
+      p.lse[meta.x + r] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+    __syncthreads();
+  }
 }
 
 cudaError_t launch_latent_merge(const LatentMergeParams& p, int latent, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(p.ctas), kLatRows / 8);
+  const dim3 grid(static_cast<unsigned>(p.ctas), static_cast<unsigned>(p.grid_rows));
   const auto kern = latent == 512   ? ua_latent_merge_kernel<512>
                     : latent == 256 ? ua_latent_merge_kernel<256>
                                     : ua_latent_merge_kernel<128>;
@@ -120,7 +203,7 @@ int check(const ua_latent_t& a) {
 
 // CTAs of a worker and workers of a call on `sms` SMs, from the host's sizes (a bound of the work:
 // the kernel takes its shares from the lengths themselves).
-constexpr int kMinShare = 4;
+constexpr int kMinShare = 2;
 void shape(const ua_latent_t& a, int sms, int* workers, int* cl) {
   *cl = static_cast<long long>(a.max_seqlen_q) * a.num_heads > ua::kLatRows ? 2 : 1;
   const long long tiles =
@@ -210,6 +293,9 @@ int attend(const ua_latent_t& a, cudaStream_t st) {
   m.ctas = ctas;
   m.cl = p.cl;
   m.out_dtype = a.out_dtype;
+  // blocks of a tile: one for each row, sixteen at most (they walk the others)
+  m.grid_rows = static_cast<int>(std::max(
+      1LL, std::min(16LL, static_cast<long long>(a.max_seqlen_q) * a.num_heads)));
   return ua::launch_latent_merge(m, a.latent_dim, st) == cudaSuccess ? UA_OK : UA_ERR_CUDA;
 }
 

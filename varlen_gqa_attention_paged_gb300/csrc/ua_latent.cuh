@@ -85,6 +85,12 @@ struct LatentWalk {
     kt = key_tiles(kv_len);
   }
 
+  // a / b, mostly of small numbers.
+  __device__ __forceinline__ static int quotient(long long a, int b) {
+    return static_cast<unsigned long long>(a) < 0x80000000ull ? static_cast<int>(a) / b
+                                                              : static_cast<int>(a / b);
+  }
+
   // Called by a whole warp.
   __device__ __forceinline__ LatentWalk(const LatentParams& p, int worker) {
     const int lane = threadIdx.x & 31;
@@ -95,10 +101,11 @@ struct LatentWalk {
     };
     const long long first = units(lane);
     long long total = first;
+#pragma unroll 4
     for (int base = 32; base < p.num_seqs; base += 32) total += units(base + lane);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    share = max(static_cast<long long>(p.min_share), (total + p.workers - 1) / p.workers);
+    share = max(p.min_share, quotient(total + p.workers - 1, p.workers));
     pos = worker * share;
     left = min(share, total - pos);
     b = t = j = 0;
@@ -119,8 +126,13 @@ struct LatentWalk {
         const long long off = pos - before - __shfl_sync(0xffffffffu, end - u, src);
         b = base + src;
         load(p);
-        t = static_cast<int>(off / kt);
-        j = static_cast<int>(off % kt);
+        t = quotient(off, kt);
+        j = static_cast<int>(off - static_cast<long long>(t) * kt);
+        // (the block table's entries are on their way to L2 while the roles set out)
+        if (lane == 0)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(
+              p.block_table + static_cast<size_t>(b) * p.max_blocks_per_seq +
+              min(j * kLatKeys / p.block_size, p.max_blocks_per_seq - 1)));
         return;
       }
       before += __shfl_sync(0xffffffffu, end, 31);

@@ -59,7 +59,7 @@ struct LatentMergeParams {
   const float* ws_l;
   const int4* ws_meta;
   long long rows;               // total_q * heads
-  int ctas, cl, out_dtype;
+  int ctas, cl, out_dtype, grid_rows;
 };
 
 cudaError_t launch_latent_l128(const LatentParams& p, bool bf16, cudaStream_t s);
