@@ -45,8 +45,8 @@ class Model:
         self.q_full, self.q_empty = Bar(1), Bar(1)
         self.k_full = [[Bar(1) for _ in range(PARTS)] for _ in range(stages)]
         self.k_empty = [[Bar(1) for _ in range(PARTS)] for _ in range(stages)]
-        self.s_full, self.s_empty = [Bar(1), Bar(1)], [Bar(4), Bar(4)]
-        self.p_full, self.pv_done, self.o_empty = Bar(4), Bar(1), Bar(4)
+        self.s_full, self.s_empty = [Bar(1), Bar(1)], [Bar(8), Bar(8)]
+        self.p_full, self.pv_done, self.o_empty = Bar(8), Bar(1), Bar(8)
         self.flying, self.queues = [], [[], []]
         self.tile = [[None] * PARTS for _ in range(stages)]     # what each part holds
         self.q = self.o = self.p = None
@@ -133,9 +133,9 @@ class Model:
                     assert self.read >= x[1] - 1, "scores overwritten before they were read"
                     self.s[x[1] & 1] = x[1]
                 else:
-                    assert self.tile[x[2]][x[3]] == x[1] and self.p == [x[1]] * 4
+                    assert self.tile[x[2]][x[3]] == x[1] and self.p == [x[1]] * 8
                     if x[4]:
-                        assert self.o is None or self.o == ["out", x[5] - 1, 4]
+                        assert self.o is None or self.o == ["out", x[5] - 1, 8]
                         self.o = ["sum", x[5], 0]
                     assert self.o[:2] == ["sum", x[5]]
             yield
@@ -154,7 +154,7 @@ class Model:
                 while it > 0 and not self.pv_done.done((it - 1) & 1):
                     yield
                 assert not any(x[0] == "pv" for x in self.queues[1]), "weights still read"
-                self.p = self.p or [None] * 4
+                self.p = self.p or [None] * 8
                 self.p[warp] = it
                 self.p_full.arrive()
                 it += 1
@@ -167,9 +167,9 @@ class Model:
             yield
 
     def run(self):
-        seen = [0] * 4
+        seen = [0] * 8
         roles = [self.copies(g) for g in range(PARTS)] + \
-            [self.scores(), self.values()] + [self.softmax(w, seen) for w in range(4)]
+            [self.scores(), self.values()] + [self.softmax(w, seen) for w in range(8)]
         live = roles + [self.land(), self.tensor()]
         weight = [self.rng.choice([1, 1, 3, 20]) for _ in live]
         for _ in range(200000):

@@ -223,6 +223,16 @@ bool row_map(CUtensorMap* map, const void* base, bool bf16, long long rows, int 
   return ua::encode_half_map(map, base, bf16, 2, dims, strides, box);
 }
 
+// The rows' latent parts as [blocks][rows][64]: boxes of 64 rows x `box_blocks`.
+bool block_map(CUtensorMap* map, const void* base, bool bf16, long long rows, int width, int latent,
+               int box_blocks) {
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(latent) / 64};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(width) * 2, 128};
+  const cuuint32_t box[3] = {64, 64, static_cast<cuuint32_t>(box_blocks)};
+  return ua::encode_half_map(map, base, bf16, 3, dims, strides, box);
+}
+
 int attend(const ua_latent_t& a, cudaStream_t st) {
   int rc = check(a);
   if (rc != UA_OK) return rc;
@@ -248,10 +258,13 @@ int attend(const ua_latent_t& a, cudaStream_t st) {
   const bool bf16 = a.dtype == UA_DT_BF16;
   p.box_rows = std::min(ua::kLatKeys, a.block_size & -a.block_size);
   const int width = a.latent_dim + a.rope_dim;
-  if (!row_map(&p.q_map, a.q, bf16, static_cast<long long>(a.total_q) * a.num_heads, width,
-               ua::kLatRows) ||
-      !row_map(&p.k_map, a.cache, bf16, static_cast<long long>(a.num_blocks) * a.block_size, width,
-               p.box_rows))
+  const long long q_rows = static_cast<long long>(a.total_q) * a.num_heads;
+  const long long k_rows = static_cast<long long>(a.num_blocks) * a.block_size;
+  const int half = a.latent_dim / (a.latent_dim > 128 ? 128 : 64);  // column blocks of a half
+  if (!row_map(&p.q_map, a.q, bf16, q_rows, width, ua::kLatRows) ||
+      !block_map(&p.q_lat, a.q, bf16, q_rows, width, a.latent_dim, a.latent_dim / 64) ||
+      !row_map(&p.k_map, a.cache, bf16, k_rows, width, p.box_rows) ||
+      !block_map(&p.k_half, a.cache, bf16, k_rows, width, a.latent_dim, half))
     return UA_ERR_CUDA;
   p.out = a.out;
   p.lse = a.lse;

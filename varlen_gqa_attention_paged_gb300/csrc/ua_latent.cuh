@@ -44,7 +44,8 @@ struct LatentCfg {
   static constexpr int kParts = 1 + kHalves;
   static constexpr int kHalfMB = kMB / kHalves;
   static constexpr int kPBytes = kLatRows * 128;
-  static constexpr int kSmallBytes = 1024;       // barriers, rescale factors
+  static constexpr int kBarBytes = 320;           // barriers
+  static constexpr int kSmallBytes = kBarBytes + 6 * kLatRows * 4;  // and row factors and maxima
   static constexpr int kFit =
       (227 * 1024 - 1024 - kSmallBytes - kQBytes - kPBytes) / kTileBytes;
   static constexpr int kStages = kFit > 4 ? 4 : kFit;
@@ -52,9 +53,9 @@ struct LatentCfg {
       1024 + kQBytes + kStages * kTileBytes + kPBytes + kSmallBytes;
   static constexpr int kTmemO = 2 * kLatKeys;    // two S buffers, then O^T
   static constexpr int kTmemCols = kTmemO + kMB * kLatRows > 256 ? 512 : 256;
-  static constexpr int kThreads = 32 * (6 + kParts);  // softmax (4), MMA issue (2), a part's copies each
+  static constexpr int kThreads = 32 * (10 + kParts);  // softmax (8), MMA issue (2), a part's copies each
   static_assert(L % 128 == 0 && L <= 512 && kMB % kHalves == 0);
-  static_assert(kStages >= 2 && kSmemBytes + 64 <= 227 * 1024);
+  static_assert(kStages >= 2 && kSmemBytes + 96 <= 227 * 1024);
 };
 
 // A worker's walk over its share: segments of consecutive key tiles of one row tile.  Every warp
@@ -177,6 +178,20 @@ struct LatentSeg {
   }
 };
 
+// A box of a tensor map on its way to L2.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
 // D[tmem] (+)= A[smem] * B[smem], 128-byte swizzle, stride byte offset 1024 (eight rows), issued by
 // one lane of a converged warp; operands by their address / 16 and leading byte offset.
 __device__ __forceinline__ void umma_f16_ss_at(uint32_t d_tmem, uint32_t a16, uint32_t a_lbo,
@@ -218,18 +233,15 @@ __device__ __forceinline__ void store_two(void* out, size_t at, float a, float b
         dtype == UA_DT_BF16 ? pack_bf16(a, b) : pack_f16(a, b);
 }
 
-// 16 lanes x 64 columns of an accumulator over a warp: register 4 g + 2 k + e of lane t holds row
+// 16 lanes x 32 columns of an accumulator over a warp: register 4 g + 2 k + e of lane t holds row
 // t / 4 + 8 k, column 8 g + 2 (t mod 4) + e.
-__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
 
@@ -260,38 +272,41 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
   uint64_t* const fin = bars + 7;
   uint64_t* const grown = bars + 8;    // the tile's rescale factors are written
   uint64_t* const s_empty = bars + 9;  // [2]
-  uint64_t* const k_full = bars + 11;  // [S][parts]
+  uint64_t* const scaled = bars + 11;  // the factors of a tile that moves a max are written
+  uint64_t* const k_full = bars + 12;  // [S][parts]
   uint64_t* const k_empty = k_full + S * C::kParts;
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(k_empty + S * C::kParts);
-  float* const sF = reinterpret_cast<float*>(bars + 64);  // [2][64] factors of O's rows
-  static_assert(8 * (11 + 2 * S * C::kParts) + 4 <= 512 && 512 + 512 <= C::kSmallBytes);
+  float* const sF = reinterpret_cast<float*>(bars + C::kBarBytes / 8);  // [2][64] factors of O's rows
+  float* const sT = sF + 2 * kLatRows;                    // [2][2][64] row maxima (sums) of column halves
+  static_assert(8 * (12 + 2 * S * C::kParts) + 4 <= C::kBarBytes);
   __shared__ int s_abort;
-  // [tile mod 2][warp]: the tile + 1, if a row of the warp's moved its max in it
-  __shared__ int s_grow[2][4];
+  // [tile mod 2][warp]: the tile + 1, if a row of the warp's is to move its max in it
+  __shared__ int4 s_grow[2][2];
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int worker = blockIdx.x / p.cl, rank = blockIdx.x % p.cl;
-  constexpr int kQk = 4, kPv = 5, kCopy = 6;  // (kCopy + g copies part g)
+  constexpr int kQk = 8, kPv = 9, kCopy = 10;  // (kCopy + g copies part g)
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
-    mbar_init(p_full, 4);
+    mbar_init(p_full, 8);
     mbar_init(pv_done, 1);
-    mbar_init(o_empty, 4);
+    mbar_init(o_empty, 8);
     mbar_init(fin, 2);
-    mbar_init(grown, 4);
-    mbar_init(&s_empty[0], 4);
-    mbar_init(&s_empty[1], 4);
+    mbar_init(grown, 8);
+    mbar_init(scaled, 8);
+    mbar_init(&s_empty[0], 8);
+    mbar_init(&s_empty[1], 8);
     for (int i = 0; i < S * C::kParts; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
     }
     s_abort = 0;
-    for (int i = 0; i < 8; ++i) s_grow[i >> 2][i & 3] = 0;
+    for (int i = 0; i < 4; ++i) s_grow[i >> 1][i & 1] = make_int4(0, 0, 0, 0);
     mbar_fence_init();
   }
   if (warp == kQk) {
@@ -300,7 +315,9 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
   }
   if (warp == kCopy && lane == 0) {
     tma_prefetch_desc(&p.q_map);
+    tma_prefetch_desc(&p.q_lat);
     tma_prefetch_desc(&p.k_map);
+    tma_prefetch_desc(&p.k_half);
   }
   tc_fence_before();
   __syncthreads();
@@ -335,13 +352,13 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
       if (g == 0 && lane == 0) {
         const int row = w.q0 * p.heads + s.row0;
         mbar_arrive_expect_tx(q_full, C::kQBytes);
-        for (int cb = 0; cb < C::kCH; ++cb)
-          tma_load_2d(sQ + cb * C::kQCB, &p.q_map, 64 * cb, row, q_full);
+        tma_load_3d_pf(sQ, &p.q_lat, 0, row, 0, q_full);
+        tma_load_2d(sQ + C::kCB * C::kQCB, &p.q_map, L, row, q_full);
       }
       ++sg;
       const int32_t* bt = p.block_table + static_cast<size_t>(w.b) * p.max_blocks_per_seq;
-      // the block of this lane's box (its second, of 64 boxes) of key tile j, loaded two tiles
-      // ahead of its use
+      // the block of this lane's box (its second, of 64 boxes) of key tile j, loaded three
+      // tiles ahead of its use
       auto block_of = [&](int j, int i) -> int {
         const int box = lane + 32 * i, key = j * kLatKeys + box * bw, col = key / bs;
         return j < s.j0 + s.nt && box < nb && key < w.kv_len && col < p.max_blocks_per_seq
@@ -358,11 +375,12 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
         }
         return blk * bs + key % bs;
       };
-      int blk0[2], blk1[2];
+      int blk0[2], blk1[2], blk2[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         blk0[i] = block_of(s.j0, i);
         blk1[i] = block_of(s.j0 + 1, i);
+        blk2[i] = block_of(s.j0 + 2, i);
       }
       for (int n = 0; ok && n < s.nt; ++n, ++it) {
         const int j = s.j0 + n, st = it % S;
@@ -378,18 +396,34 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
         // (only now: the tile before has arrived, so that its phase of the barrier is over)
         if (lane == 0) mbar_arrive_expect_tx(full, blocks * C::kKCB);
         __syncwarp();
-        for (int e = lane; e - lane < blocks * nb; e += 32) {
-          const int cb = cb0 + e / nb, box = e % nb;
-          const int lo = __shfl_sync(0xffffffffu, row0, box & 31);
-          const int hi = __shfl_sync(0xffffffffu, row1, box & 31);
-          if (e < blocks * nb)
-            tma_load_2d(tile + cb * C::kKCB + box * bw * 128, &p.k_map, 64 * cb,
-                        box < 32 ? lo : hi, full);
+        if (g > 0 && bw == kLatKeys) {  // the half in one box
+          if (lane == 0) tma_load_3d_pf(tile + cb0 * C::kKCB, &p.k_half, 0, row0, cb0, full);
+        } else {
+          for (int e = lane; e - lane < blocks * nb; e += 32) {
+            const int cb = cb0 + e / nb, box = e % nb;
+            const int lo = __shfl_sync(0xffffffffu, row0, box & 31);
+            const int hi = __shfl_sync(0xffffffffu, row1, box & 31);
+            if (e < blocks * nb)
+              tma_load_2d(tile + cb * C::kKCB + box * bw * 128, &p.k_map, 64 * cb,
+                          box < 32 ? lo : hi, full);
+          }
         }
+        // With two tiles in shared memory the copy of one waits for the products of the one before:
+        // the next but one comes as far as L2 meanwhile.
+        if (n + 2 < s.nt) {
+          const int ahead = row_of(j + 2, 0, blk2[0]);
+          if (g > 0 && bw == kLatKeys) {
+            if (lane == 0) tma_prefetch_3d(&p.k_half, 0, ahead, cb0);
+          } else if (lane < min(nb, 32)) {
+            for (int cb = cb0; cb < cb0 + blocks; ++cb) tma_prefetch_2d(&p.k_map, 64 * cb, ahead);
+          }
+        }
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           blk0[i] = blk1[i];
-          blk1[i] = block_of(j + 2, i);
+          blk1[i] = blk2[i];
+          blk2[i] = block_of(j + 3, i);
         }
       }
     }
@@ -479,12 +513,18 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
     mbar_wait_bounded(fin, 0, p.status, DEV_TIMEOUT);
   } else {
     // ======================================================== softmax, rescale, epilogue
-    // An M = 64 accumulator keeps rows 16 w .. 16 w + 15 in the first half of warp w's lanes.  A
-    // lane reads two of them, rows ra and ra + 8, columns 8 g + 2 cq and the next: four lanes a row.
-    const int ra = 16 * warp + (lane >> 2), cq = lane & 3;
-    const uint32_t lane_off = (32u * warp) << 16;
+    // An M = 64 accumulator keeps rows 16 w .. 16 w + 15 in the first half of lane quarter w.  Two
+    // warps share them, half of the columns each: a lane has rows ra and ra + 8, columns 32 half +
+    // 8 g + 2 cq and the next.
+    const int quad = warp & 3, half = warp >> 2;
+    const int ra = 16 * quad + (lane >> 2), cq = lane & 3;
+    const uint32_t lane_off = (32u * quad) << 16;
     const uint32_t tO = tmem + C::kTmemO + lane_off;
     const float c = p.scale * kLog2e;
+    // (of O's 32-column pieces, the warps of a lane quarter take every other 128-element block, or,
+    // with one block, a piece each)
+    auto mine = [&](int piece) { return (C::kMB > 1 ? piece >> 1 & 1 : piece & 1) == half; };
+    int moved = 0;  // tiles that moved a max
     int4 meta = make_int4(0, 0, 0, 0);
     // (After a wait that gave up, these warps go on to the end, through every barrier that they
     // share; their later waits return at once, and nothing is stored.)
@@ -509,90 +549,108 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
         ok = pf_wait_warp(&s_full[it & 1], (it >> 1) & 1, abort_flag, p.status) && ok;
         tc_fence_after();
         const int k0 = (s.j0 + n) * kLatKeys;
-        uint32_t x[32];  // [g][row][2]
-        tmem_ld_16x256b_x8(tmem + (it & 1) * kLatKeys + lane_off, x);
+        uint32_t x[16];  // [g][row][2]
+        tmem_ld_16x256b_x4(tmem + (it & 1) * kLatKeys + 32 * half + lane_off, x);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[it & 1]);
-        if (k0 + kLatKeys > clear) {
+        const int kh = k0 + 32 * half;
+        if (kh + 32 > clear) {
           // the keys that a row sees: of the prefix (tree) or up to its own, and those its mask
           // names
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int end = min(w.kv_len, p.tree != nullptr ? s.ctx : s.ctx + i_q[k] + 1) - k0;
-            uint32_t lo = low_bits(end), hi = low_bits(end - 32);
+            uint32_t see =
+                low_bits(min(w.kv_len, p.tree != nullptr ? s.ctx : s.ctx + i_q[k] + 1) - kh);
             if (p.tree != nullptr && rv[k]) {
               const int32_t* row = p.tree + (static_cast<long long>(w.q0) + i_q[k]) * p.tree_stride;
-              const int last = w.kv_len - k0;
-              lo |= mask_bits32(row, p.tree_words, k0 - s.ctx) & low_bits(last) &
-                    ~low_bits(s.ctx - k0);
-              hi |= mask_bits32(row, p.tree_words, k0 + 32 - s.ctx) & low_bits(last - 32) &
-                    ~low_bits(s.ctx - k0 - 32);
+              see |= mask_bits32(row, p.tree_words, kh - s.ctx) & low_bits(w.kv_len - kh) &
+                     ~low_bits(s.ctx - kh);
             }
-            lo >>= 2 * cq;
-            hi >>= 2 * cq;
+            see >>= 2 * cq;
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              const uint32_t two = (g < 4 ? lo : hi) >> (8 * (g & 3));
-              if (!(two & 1u)) x[4 * g + 2 * k] = 0xff800000u;
-              if (!(two & 2u)) x[4 * g + 2 * k + 1] = 0xff800000u;
+            for (int g = 0; g < 4; ++g) {
+              if (!(see >> (8 * g) & 1u)) x[4 * g + 2 * k] = 0xff800000u;
+              if (!(see >> (8 * g) & 2u)) x[4 * g + 2 * k + 1] = 0xff800000u;
             }
           }
         }
-        float alpha[2], mu[2];
+        // The running max moves only by more than 8 in log2 units (P stays <= 256, inside f16's
+        // range and fp32 sums'), or to a row's first key.  That is rare, so the exponentials are
+        // taken with the old max while the column halves hear from each other whether it moves.
+        float top[2];
         bool grow = false;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float top = -INFINITY;
+          float t = -INFINITY;
 #pragma unroll
-          for (int g = 0; g < 8; ++g)
-            top = fmax3(top, __uint_as_float(x[4 * g + 2 * k]), __uint_as_float(x[4 * g + 2 * k + 1]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * c;
-          // The running max moves only by more than 8 in log2 units (P stays <= 256, inside
-          // f16's range and fp32 sums'), or to a row's first key.
-          alpha[k] = 1.f;
-          if (rv[k] && (top > m[k] + 8.f || (m[k] == -INFINITY && top > -INFINITY))) {
-            alpha[k] = m[k] == -INFINITY ? 0.f : fast_exp2(m[k] - top);
-            m[k] = top;
-            grow = true;
-          }
-          mu[k] = m[k] == -INFINITY ? 0.f : m[k];
+          for (int g = 0; g < 4; ++g)
+            t = fmax3(t, __uint_as_float(x[4 * g + 2 * k]), __uint_as_float(x[4 * g + 2 * k + 1]));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+          top[k] = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2)) * c;
+          grow = grow || (rv[k] && (top[k] > m[k] + 8.f || (m[k] == -INFINITY && top[k] > -INFINITY)));
         }
-        // O has every row in every warp's lanes: the factors go round under the exponentials
-        float* const f = sF + (it & 1) * kLatRows;
-        if (n > 0) {
-          if (cq == 0) f[ra] = alpha[0], f[ra + 8] = alpha[1];
-          if (__any_sync(0xffffffffu, grow) && lane == 0) s_grow[it & 1][warp] = it + 1;
-          __syncwarp();
+        float* const tops = sT + (it & 1) * 2 * kLatRows;
+        if (cq == 0) {
+          tops[half * kLatRows + ra] = top[0];
+          tops[half * kLatRows + ra + 8] = top[1];
         }
+        if (__any_sync(0xffffffffu, grow) && lane == 0)
+          reinterpret_cast<int*>(s_grow[it & 1])[warp] = it + 1;
+        __syncwarp();
         if (lane == 0) mbar_arrive(grown);
         // P rounded to 16 bits for the MMA (half a step of 2^-8 or 2^-11 of each weight); the sum
         // is of the unrounded weights
-        uint32_t pk[16];  // [row][g]
+        uint32_t pk[8];  // [row][g]
+        float add[2];
+        auto weights = [&]() {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float l0 = 0.f, l1 = 0.f;
+          for (int k = 0; k < 2; ++k) {
+            const float mu = m[k] == -INFINITY ? 0.f : m[k];
+            float l0 = 0.f, l1 = 0.f;
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            const float a = fast_exp2(fmaf(__uint_as_float(x[4 * g + 2 * k]), c, -mu[k]));
-            const float b = fast_exp2(fmaf(__uint_as_float(x[4 * g + 2 * k + 1]), c, -mu[k]));
-            l0 += a;
-            l1 += b;
-            pk[8 * k + g] = pack_half2<BF16>(a, b);
+            for (int g = 0; g < 4; ++g) {
+              const float a = fast_exp2(fmaf(__uint_as_float(x[4 * g + 2 * k]), c, -mu));
+              const float b = fast_exp2(fmaf(__uint_as_float(x[4 * g + 2 * k + 1]), c, -mu));
+              l0 += a;
+              l1 += b;
+              pk[4 * k + g] = pack_half2<BF16>(a, b);
+            }
+            add[k] = l0 + l1;
           }
-          l[k] = l[k] * alpha[k] + (l0 + l1);
-        }
+        };
+        weights();
         // P's buffer and O are free when the P.V before is done
         if (it > 0) ok = pf_wait_warp(pv_done, (it - 1) & 1, abort_flag, p.status) && ok;
         tc_fence_after();
         ok = pf_wait_warp(grown, it & 1, abort_flag, p.status) && ok;
-        if (n > 0) {
-          const volatile int* const at = s_grow[it & 1];
-          if (at[0] == it + 1 || at[1] == it + 1 || at[2] == it + 1 || at[3] == it + 1) {
+        const int4 ga = s_grow[it & 1][0], gb = s_grow[it & 1][1];
+        const int now = it + 1;
+        if (ga.x == now || ga.y == now || ga.z == now || ga.w == now || gb.x == now || gb.y == now ||
+            gb.z == now || gb.w == now) {
+          float* const f = sF + (it & 1) * kLatRows;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float t = fmaxf(top[k], tops[(half ^ 1) * kLatRows + ra + 8 * k]);
+            float alpha = 1.f;
+            if (rv[k] && (t > m[k] + 8.f || (m[k] == -INFINITY && t > -INFINITY))) {
+              alpha = m[k] == -INFINITY ? 0.f : fast_exp2(m[k] - t);
+              m[k] = t;
+            }
+            l[k] *= alpha;
+            if (half == 0 && cq == 0) f[ra + 8 * k] = alpha;
+          }
+          weights();
+          // O has every row in every warp's lanes
+          __syncwarp();
+          if (lane == 0) mbar_arrive(scaled);
+          ok = pf_wait_warp(scaled, moved & 1, abort_flag, p.status) && ok;
+          ++moved;
+          if (n > 0) {
 #pragma unroll 1
             for (int cc = 0; cc < C::kMB * 2; ++cc) {
+              if (!mine(cc)) continue;
               uint32_t o[32];
               tmem_ld32(tO + 32 * cc, o);
               tmem_ld_wait();
@@ -610,17 +668,19 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
           }
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 2; ++k) {
+          l[k] += add[k];
 #pragma unroll
-          for (int g = 0; g < 8; ++g)
-            *reinterpret_cast<uint32_t*>(sP + (ra + 8 * k) * 128 + ((g ^ (ra & 7)) << 4) + 4 * cq) =
-                pk[8 * k + g];
+          for (int g = 0; g < 4; ++g)
+            *reinterpret_cast<uint32_t*>(sP + (ra + 8 * k) * 128 + (((4 * half + g) ^ (ra & 7)) << 4) +
+                                         4 * cq) = pk[4 * k + g];
+        }
         // Cache slots at or past kv_len may hold anything (NaN included): they become zeros
         // before they meet P = 0 (a box of a copy that lies past kv_len altogether is zeros).
         if (k0 + kLatKeys > w.kv_len) {
           const int lo = w.kv_len - k0, end = min(kLatKeys, (lo + p.box_rows - 1) & -p.box_rows);
           uint8_t* const tile = sK + (it % S) * C::kTileBytes;
-          for (int e = threadIdx.x; e < (end - lo) * C::kCB * 8; e += 128) {
+          for (int e = threadIdx.x; e < (end - lo) * C::kCB * 8; e += 256) {
             const int row = lo + e / (C::kCB * 8), x = e % (C::kCB * 8);
             *reinterpret_cast<uint4*>(tile + (x >> 3) * C::kKCB + row * 128 + (x & 7) * 16) =
                 make_uint4(0, 0, 0, 0);
@@ -638,13 +698,19 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
         ok = pf_wait_warp(pv_done, (it - 1) & 1, abort_flag, p.status) && ok;
         tc_fence_after();
       }
+      // a row's sum: its lanes', then the column halves'
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float sum = l[k];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+        if (half == 1 && cq == 0) sT[(it & 1) * 2 * kLatRows + ra + 8 * k] = l[k];
+      }
+      named_bar_sync(1, 256);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
         const int r = ra + 8 * k;
-        if (cq != 0) continue;
+        if (half != 0 || cq != 0) continue;
+        const float sum = l[k] + sT[(it & 1) * 2 * kLatRows + r];
         // (a row that saw no key is 0; NaN stays)
         f[r] = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
         if (!rv[k] || !ok) continue;
@@ -655,13 +721,13 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
           p.lse[grow0 + r] = latent_lse(m[k], sum);
         }
       }
-      named_bar_sync(1, 128);
-      const int d = 32 * warp + lane;  // this lane's element of a 128-element block of O
+      named_bar_sync(1, 256);
+      const int d = 32 * quad + lane;  // this lane's element of a 128-element block of O
       if (ok && (whole || s.nt > 0)) {  // (an empty partial row's sum is 0: its elements are not read)
 #pragma unroll 1
         for (int cc = 0; cc < C::kMB * 2; ++cc) {
           const int rb = 32 * (cc & 1), blk = (cc >> 1) * 128;
-          if (rb >= rows) continue;
+          if (rb >= rows || !mine(cc)) continue;
           uint32_t o[32];
           if (s.nt > 0) {
             tmem_ld32(tO + 32 * cc, o);
@@ -700,7 +766,7 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
         if (lane == 0) mbar_arrive(o_empty);
         ++sg;
       }
-      named_bar_sync(1, 128);  // the factors have been read
+      named_bar_sync(1, 256);  // the factors have been read
     }
     if (threadIdx.x == 0) p.ws_meta[blockIdx.x] = ok ? meta : make_int4(0, 0, 0, 0);
   }

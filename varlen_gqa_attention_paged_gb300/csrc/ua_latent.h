@@ -11,9 +11,10 @@ constexpr int kLatKeys = 64;
 
 // One launch of the absorbed form's kernel.  q is mapped as rows [total_q * heads][L + R] in boxes of
 // 64 elements x 64 rows, the cache as rows [num_blocks * block_size][L + R] in boxes of 64 elements x
-// box_rows (elements past L + R read as zero).
+// box_rows (elements past L + R read as zero); and the latent parts as column blocks of 64 elements,
+// in boxes of 64 rows of all of them (q) or of a half (the cache).
 struct LatentParams {
-  CUtensorMap q_map, k_map;
+  CUtensorMap q_map, q_lat, k_map, k_half;
   void* out;                    // [total_q, heads, L]
   float* lse;                   // [total_q, heads] or null
   const int32_t* cu_seqlens_q;
