@@ -8,9 +8,12 @@
 // A CTA owns two tiles of 128 query tokens of one head.  Per key tile (128 keys) and q tile:
 // S = Q K^T over N / 64 + 1 column blocks of 64 (the last is the rope part, its k-steps past R left
 // out), softmax with one thread a row, P (16 bits) over S in tensor memory, O += P V.  While one
-// q tile's rows are in the softmax the tensor cores work on the other's.  K tiles (48 KB at
-// N = 128) have two buffers beside Q (96 KB) and V (32 KB) one: V_j arrives under Q K^T of the next
-// tile.
+// q tile's rows are in the softmax the tensor cores work on the other's.  Beside Q (96 KB at N =
+// 128) there is room for eight blocks of 128 keys x 64 elements, where a key tile has three and a
+// value tile two: they go through one ring in the order in which they are used up, K_0 V_0 K_1 V_1
+// ..., so that what one tile frees takes the next but one.  (Barriers are a tile's: a commit costs
+// the issuing warp about 200 cycles.)  (With whole tiles, two of K and one of
+// V, the tensor cores waited 1800 of 4700 cycles a step for V.)
 #pragma once
 
 #include <atomic>
@@ -29,19 +32,18 @@ struct LatentPrefillCfg {
   static constexpr int kVB = V / 64;               // and of a value
   static constexpr int kBlk = 128 * 128;           // bytes of one column block of a tile
   static constexpr int kQBytes = kCB * kBlk;       // one q tile
-  static constexpr int kKBytes = kCB * kBlk;
-  static constexpr int kVBytes = kVB * kBlk;
-  static constexpr int kBarBytes = 512;
-  static constexpr int kRoom = 227 * 1024 - 1024 - kBarBytes - kNQ * kQBytes;
-  static constexpr int kRingK = 2;
-  static constexpr int kRingV = (kRoom - kRingK * kKBytes) / kVBytes >= 2 ? 2 : 1;
-  static constexpr int kSmemBytes =
-      1024 + kBarBytes + kNQ * kQBytes + kRingK * kKBytes + kRingV * kVBytes;
+  static constexpr int kPer = kCB + kVB;           // blocks of a key tile and its values
+  static constexpr int kBarBytes = 256;
+  static constexpr int kRoom = (227 * 1024 - 1024 - kBarBytes - kNQ * kQBytes) / kBlk;
+  static constexpr int kRing = kRoom > 4 * kPer ? 4 * kPer : kRoom;
+  static constexpr int kTiles = 4;                 // barriers: tiles that may be in the ring
+  static constexpr int kSmemBytes = 1024 + kBarBytes + kNQ * kQBytes + kRing * kBlk;
   static constexpr int kTmemStride = kBN + V;      // S (and P over it), then O, of one q tile
   static constexpr int kTmemCols = 512;
-  static constexpr int kThreads = 32 * (4 * kNQ + 3);
-  static_assert(N % 64 == 0 && V % 64 == 0 && kNQ * kTmemStride <= kTmemCols);
-  static_assert(kSmemBytes + 16 <= 227 * 1024);
+  static constexpr int kThreads = 32 * (4 * kNQ + 2);  // softmax, copies, MMA issue
+  static_assert(N % 64 == 0 && (V == 64 || V == 128) && kNQ * kTmemStride <= kTmemCols);
+  static_assert(kRing >= kPer + kVB && kSmemBytes + 16 <= 227 * 1024);
+  static_assert(8 * (9 + 4 * kTiles) + 4 <= kBarBytes);
 };
 
 // The sequence owning slot x of q-blocks of tb tokens, by one warp: the last b with
@@ -73,31 +75,66 @@ __device__ __forceinline__ LatentSeqOf latent_seq_of_slot(const int32_t* __restr
   return r;
 }
 
+// The slot with the y-th longest walk, of up to 64, by one warp: with few q-blocks an SM has one or
+// two, and those that start last must not be the longest (58.1 against 67.7 us for five chunks behind
+// prefixes, whose longest sequence comes first in the batch).
+__device__ __forceinline__ int latent_slot_by_length(const int32_t* __restrict__ cq,
+                                                     const int32_t* __restrict__ ck, int num_seqs,
+                                                     int slots, int y, int tb) {
+  const int lane = threadIdx.x & 31;
+  int walk[2] = {-1, -1};  // of slots lane and lane + 32 (an idle one: -1)
+  for (int base = 0; base < num_seqs; base += 32) {
+    const int i = base + lane;
+    const bool in = i < num_seqs;
+    const int q0 = in ? __ldg(cq + i) : 0, q1 = in ? __ldg(cq + i + 1) : 0;
+    const int k_len = in ? __ldg(ck + i + 1) - __ldg(ck + i) : 0;
+    for (int e = 0; e < min(32, num_seqs - base); ++e) {
+      const int s0 = __shfl_sync(0xffffffffu, q0, e), n = __shfl_sync(0xffffffffu, q1, e) - s0;
+      const int k = __shfl_sync(0xffffffffu, k_len, e), first = s0 / tb + base + e;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int t = (lane + 32 * u - first) * tb;  // the slot's first token in this sequence
+        if (t >= 0) walk[u] = t < n ? max(0, k - n + min(t + tb, n)) : -1;  // (the last one owns it)
+      }
+    }
+  }
+  int rank[2] = {0, 0};
+#pragma unroll
+  for (int v = 0; v < 2; ++v)
+    for (int e = 0; e < 32; ++e) {
+      const int o = __shfl_sync(0xffffffffu, walk[v], e), x = e + 32 * v;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        rank[u] += x < slots && (o > walk[u] || (o == walk[u] && x < lane + 32 * u));
+    }
+  const unsigned a = __ballot_sync(0xffffffffu, lane < slots && rank[0] == y);
+  const unsigned b = __ballot_sync(0xffffffffu, lane + 32 < slots && rank[1] == y);
+  return a != 0u ? __ffs(a) - 1 : b != 0u ? __ffs(b) + 31 : y;
+}
+
 template <int N, int V, bool BF16>
 __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
     ua_latent_prefill_kernel(const __grid_constant__ LatentPrefillParams p) {
   using C = LatentPrefillCfg<N, V>;
-  constexpr int BM = C::kBM, BN = C::kBN, NQ = C::kNQ, RK = C::kRingK, RV = C::kRingV;
+  constexpr int BM = C::kBM, BN = C::kBN, NQ = C::kNQ, RING = C::kRing, PER = C::kPer;
   constexpr int TB = NQ * BM;
-  constexpr int kCopyK = 4 * NQ, kCopyV = 4 * NQ + 1, kMma = 4 * NQ + 2;
+  constexpr int kCopy = 4 * NQ, kMma = 4 * NQ + 1;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* const sQ = smem;
-  uint8_t* const sK = sQ + NQ * C::kQBytes;
-  uint8_t* const sV = sK + RK * C::kKBytes;
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(sV + RV * C::kVBytes);
+  uint8_t* const ring = sQ + NQ * C::kQBytes;
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(ring + RING * C::kBlk);
   uint64_t* const q_full = bars + 0;   // [NQ]
   uint64_t* const s_full = bars + 2;   // [NQ]
   uint64_t* const p_full = bars + 4;   // [NQ]
   uint64_t* const pv_done = bars + 6;  // [NQ]
   uint64_t* const fin = bars + 8;
-  uint64_t* const k_full = bars + 9;   // [RK]
-  uint64_t* const k_empty = k_full + RK;
-  uint64_t* const v_full = k_empty + RK;  // [RV]
-  uint64_t* const v_empty = v_full + RV;
-  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(v_empty + RV);
+  // full, empty of key tile j: [2 (j mod kTiles)] its keys, and the next, its values
+  uint64_t* const full = bars + 9;
+  uint64_t* const empty = full + 2 * C::kTiles;
+  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(empty + 2 * C::kTiles);
   __shared__ int s_abort;
 
   const int warp = threadIdx.x >> 5;
@@ -112,13 +149,9 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(fin, 1);
-    for (int i = 0; i < RK; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-    }
-    for (int i = 0; i < RV; ++i) {
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
+    for (int i = 0; i < 2 * C::kTiles; ++i) {
+      mbar_init(&full[i], i % 2 == 0 ? C::kCB : C::kVB);
+      mbar_init(&empty[i], 1);
     }
     s_abort = 0;
     mbar_fence_init();
@@ -127,7 +160,7 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
     tmem_alloc(tmem_holder, C::kTmemCols);
     tmem_relinquish();
   }
-  if (warp == kCopyK && lane == 0) {
+  if (warp == kCopy && lane == 0) {
     tma_prefetch_desc(&p.q);
     tma_prefetch_desc(&p.k);
     tma_prefetch_desc(&p.k_rope);
@@ -141,8 +174,11 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
   grid_dependency_wait();
   grid_launch_dependents();
 
-  // longest walks first: slots are taken in reverse order
-  const int x = static_cast<int>(gridDim.y - 1 - blockIdx.y);
+  // longest walks first: by length, or (many slots) in reverse order
+  const int slots = static_cast<int>(gridDim.y), y = static_cast<int>(blockIdx.y);
+  const int x = slots <= 64 ? latent_slot_by_length(p.cu_seqlens_q, p.cu_seqlens_k, p.num_seqs, slots,
+                                                    y, TB)
+                            : slots - 1 - y;
   const LatentSeqOf sq = latent_seq_of_slot(p.cu_seqlens_q, p.cu_seqlens_k, p.num_seqs, x, TB);
   const int t_first = (x - (sq.q0 / TB + sq.b)) * TB;
   // (tokens from total_q on, and keys from total_k on, do not exist)
@@ -161,11 +197,13 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
     return (max(0, min(last, k_len)) + BN - 1) / BN;
   };
   const int n0 = tiles(0), n1 = tiles(1);
+  // the barriers of tile j's keys (v 0) or values (1), and their phase
+  auto bar_of = [&](int j, int v) { return 2 * (j % C::kTiles) + v; };
+  auto phase_of = [&](int j) { return (j / C::kTiles) & 1; };
   const int nt = max(n0, n1);
 
-  if (warp == kCopyK) {
-    // ======================================================== Q, then K tiles
-    bool ok = true;
+  if (warp == kCopy) {
+    // ======================================================== Q, then the blocks of K_0 V_0 K_1 ..
     int issued = 0;
     if (lane == 0 && nt > 0) {
       for (int qt = 0; qt < nq; ++qt) {
@@ -175,100 +213,101 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
                          sq.q0 + t_first + qt * BM, &q_full[qt]);
       }
     }
-    for (int j = 0; ok && j < nt; ++j) {
-      const int st = j % RK;
-      if (j >= RK && !pf_wait_warp(&k_empty[st], ((j / RK) - 1) & 1, abort_flag, p.status)) break;
+    for (int j = 0, e = 0; j < nt; ++issued) {
+      const int before = issued - RING;  // the block whose place this one takes
+      if (before >= 0 &&
+          !pf_wait_warp(&empty[bar_of(before / PER, before % PER >= C::kCB)], phase_of(before / PER),
+                        abort_flag, p.status))
+        break;
       if (lane == 0) {
-        uint8_t* const dst = sK + st * C::kKBytes;
+        uint8_t* const dst = ring + issued % RING * C::kBlk;
+        uint64_t* const bar = &full[bar_of(j, e >= C::kCB)];
         const int row = sq.k0 + j * BN;
-        mbar_arrive_expect_tx(&k_full[st], C::kKBytes);
-        for (int cb = 0; cb < N / 64; ++cb)
-          tma_load_3d_pf(dst + cb * C::kBlk, &p.k, 64 * cb, h, row, &k_full[st]);
-        tma_load_2d(dst + (N / 64) * C::kBlk, &p.k_rope, 0, row, &k_full[st]);
+        mbar_arrive_expect_tx(bar, C::kBlk);
+        if (e < N / 64) tma_load_3d_pf(dst, &p.k, 64 * e, h, row, bar);
+        else if (e == N / 64) tma_load_2d(dst, &p.k_rope, 0, row, bar);
+        else tma_load_3d_pf(dst, &p.v, 64 * (e - C::kCB), h, row, bar);
       }
       __syncwarp();
-      issued = j + 1;
+      if (++e == PER) {
+        e = 0;
+        ++j;
+      }
     }
-    // never leave copies in flight into this CTA's shared memory (even after an abort)
-    for (int j = max(0, issued - RK); j < issued; ++j)
-      mbar_wait_bounded(&k_full[j % RK], (j / RK) & 1, p.status, DEV_TIMEOUT);
+    // never leave copies in flight into this CTA's shared memory (even after an abort: a tile of
+    // which only some blocks were sent for never completes, and its wait gives up)
+    for (int j = max(0, issued / PER - C::kTiles); j * PER < issued; ++j)
+      for (int v = 0; v < 2; ++v)
+        if (v == 0 || j * PER + C::kCB < issued)
+          mbar_wait_bounded(&full[bar_of(j, v)], phase_of(j), p.status, DEV_TIMEOUT);
     for (int qt = 0; nt > 0 && qt < nq; ++qt)
       mbar_wait_bounded(&q_full[qt], 0, p.status, DEV_TIMEOUT);
-  } else if (warp == kCopyV) {
-    // ======================================================== V tiles
-    int issued = 0;
-    for (int j = 0; j < nt; ++j) {
-      const int st = j % RV;
-      if (j >= RV && !pf_wait_warp(&v_empty[st], ((j / RV) - 1) & 1, abort_flag, p.status)) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&v_full[st], C::kVBytes);
-        for (int cb = 0; cb < C::kVB; ++cb)
-          tma_load_3d_pf(sV + st * C::kVBytes + cb * C::kBlk, &p.v, 64 * cb, h, sq.k0 + j * BN,
-                         &v_full[st]);
-      }
-      __syncwarp();
-      issued = j + 1;
-    }
-    for (int j = max(0, issued - RV); j < issued; ++j)
-      mbar_wait_bounded(&v_full[j % RV], (j / RV) & 1, p.status, DEV_TIMEOUT);
   } else if (warp == kMma) {
     // ======================================================== MMA issue
     // Step j: for each q tile, O += P_{j-1} V_{j-1} (which frees its S/P columns), then
-    // S = Q K_j^T.  Tensor-core operations of one thread run in issue order.
+    // S = Q K_j^T.  Tensor-core operations of one thread run in issue order, and the order keeps
+    // one q tile in the softmax while the other has the tensor cores.
     constexpr uint32_t kIdQK = umma_idesc_f16(BM, BN, BF16, false);
     constexpr uint32_t kIdPV = umma_idesc_f16(BM, V, BF16, true);
-    const int qk_steps = N / 16 + p.rope_dim / 16;
+    constexpr uint32_t kIdPVBlock = umma_idesc_f16(BM, 64, BF16, true);
+    const int rope_steps = p.rope_dim / 16;
+    const uint32_t ring0 = smem_addr(ring) >> 4, q0 = smem_addr(sQ) >> 4;
     bool ok = true;
+    int kslot = 0;  // ring slot of K_j's first block
     for (int j = 0; ok && j <= nt; ++j) {
       const int i = j - 1;  // key tile of this step's P.V
-      uint8_t* const vs = sV + (i >= 0 ? i % RV : 0) * C::kVBytes;
-      if (i >= 0) {
-        if (!pf_wait_warp(&v_full[i % RV], (i / RV) & 1, abort_flag, p.status)) { ok = false; break; }
-        // rows past the sequence's keys are another's, or none's, and may hold anything (NaN
-        // included): they become zeros before they meet P = 0
-        const int from = k_len - i * BN;
-        if (from < BN) {
-          for (int e = lane; e < (BN - from) * C::kVB * 8; e += 32) {
-            const int r = from + e / (C::kVB * 8), c = e % (C::kVB * 8);
-            *reinterpret_cast<uint4*>(vs + (c / 8) * C::kBlk + r * 128 + (c % 8) * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-      }
-      if (j < nt && !pf_wait_warp(&k_full[j % RK], (j / RK) & 1, abort_flag, p.status)) { ok = false; break; }
+      const int vslot = kslot >= C::kVB ? kslot - C::kVB : kslot - C::kVB + RING;  // V_i's
+      if (i >= 0 && !pf_wait_warp(&full[bar_of(i, 1)], phase_of(i), abort_flag, p.status)) { ok = false; break; }
 #pragma unroll
       for (int qt = 0; qt < NQ; ++qt) {
         const int n = qt == 0 ? n0 : n1;
+        const bool last = qt == (n1 > 0 ? 1 : 0);  // of the q tiles that read a block
         const uint32_t tS = tmem + qt * C::kTmemStride;
         if (i >= 0 && i < n) {
           if (!pf_wait_warp(&p_full[qt], i & 1, abort_flag, p.status)) { ok = false; break; }
           tc_fence_after();
+          const uint32_t vb = ring0 + vslot * (C::kBlk / 16);
+          if (vslot + C::kVB <= RING) {
 #pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk) {
-            const uint64_t bd = smem_desc_sw128(smem_addr(vs) + kk * 16 * 128, C::kBlk, 1024);
-            umma_f16_ts_warp(tS + BN, tS + 8 * kk, bd, kIdPV, i > 0 || kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < BN / 16; ++kk)
+              umma_f16_ts_warp(tS + BN, tS + 8 * kk, smem_desc_at(vb + kk * 128, C::kBlk), kIdPV,
+                               i > 0 || kk > 0 ? 1u : 0u);
+          } else {  // the blocks lie at the ring's two ends
+#pragma unroll
+            for (int e = 0; e < C::kVB; ++e)
+#pragma unroll
+              for (int kk = 0; kk < BN / 16; ++kk)
+                umma_f16_ts_warp(tS + BN + 64 * e, tS + 8 * kk,
+                                 smem_desc_at((e == 0 ? vb : ring0) + kk * 128, C::kBlk), kIdPVBlock,
+                                 i > 0 || kk > 0 ? 1u : 0u);
           }
           if (i == n - 1) umma_commit_warp(&pv_done[qt]);
         }
+        if (last && i >= 0) umma_commit_warp(&empty[bar_of(i, 1)]);
         if (j < n) {
-          if (j == 0 && !pf_wait_warp(&q_full[qt], 0, abort_flag, p.status)) { ok = false; break; }
+          if ((j == 0 && !pf_wait_warp(&q_full[qt], 0, abort_flag, p.status)) ||
+              ((qt == 0 || j >= n0) &&
+               !pf_wait_warp(&full[bar_of(j, 0)], phase_of(j), abort_flag, p.status))) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
-          const uint32_t qb = smem_addr(sQ + qt * C::kQBytes);
-          const uint32_t kb = smem_addr(sK + (j % RK) * C::kKBytes);
-#pragma unroll 4
-          for (int kk = 0; kk < qk_steps; ++kk) {
-            const uint64_t ad = smem_desc_sw128(qb + (kk >> 2) * C::kBlk + (kk & 3) * 32, 16, 1024);
-            const uint64_t bd = smem_desc_sw128(kb + (kk >> 2) * C::kBlk + (kk & 3) * 32, 16, 1024);
-            umma_f16_ss_warp(tS, ad, bd, kIdQK, kk > 0 ? 1u : 0u);
+          const uint32_t qb = q0 + qt * (C::kQBytes / 16);
+#pragma unroll
+          for (int e = 0; e < C::kCB; ++e) {
+            const int slot = kslot + e >= RING ? kslot + e - RING : kslot + e;
+            const uint32_t kb = ring0 + slot * (C::kBlk / 16);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (e < N / 64 || kk < rope_steps)
+                umma_f16_ss_at(tS, qb + e * (C::kBlk / 16) + 2 * kk, 16, kb + 2 * kk, 16, kIdQK,
+                               e > 0 || kk > 0 ? 1u : 0u);
           }
           umma_commit_warp(&s_full[qt]);
         }
+        if (last && j < nt) umma_commit_warp(&empty[bar_of(j, 0)]);
       }
-      if (!ok) break;
-      if (j < nt) umma_commit_warp(&k_empty[j % RK]);
-      if (i >= 0) umma_commit_warp(&v_empty[i % RV]);
+      kslot = kslot + PER >= RING ? kslot + PER - RING : kslot + PER;
     }
     // nothing may still be in flight on the tensor cores when the memory is freed
     umma_commit_warp(fin);
@@ -354,6 +393,18 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
       }
       l = l * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y));
       tmem_st_wait();
+      // V rows past the sequence's keys are another's, or none's, and may hold anything (NaN
+      // included): they become zeros before they meet P = 0
+      const int from = k_len - k0;
+      if (from < BN) {
+        if (!pf_wait_warp(&full[bar_of(n, 1)], phase_of(n), abort_flag, p.status)) { ok = false; break; }
+        for (int e = threadIdx.x & 127; e < (BN - from) * C::kVB * 8; e += 128) {
+          const int r = from + e / (C::kVB * 8), x = e % (C::kVB * 8);
+          *reinterpret_cast<uint4*>(ring + (n * PER + C::kCB + x / 8) % RING * C::kBlk + r * 128 +
+                                    (x % 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[qt]);
