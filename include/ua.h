@@ -508,7 +508,7 @@ typedef struct {
   int32_t num_seqs;
   int32_t total_q;
   int32_t total_k;
-  int32_t max_seqlen_q;         /* >= every q_len and k_len: the grid's shape follows from them */
+  int32_t max_seqlen_q;         /* >= every q_len and k_len: the grid's order follows from them */
   int32_t max_seqlen_k;
   int32_t num_heads;
   int32_t nope_dim;             /* 64 or 128 */

@@ -49,6 +49,7 @@ struct LatentPrefillParams {
   const int32_t* cu_seqlens_k;
   unsigned int* status;
   int num_seqs, total_q, total_k, heads, rope_dim, out_dtype, slots;
+  int by_length;                // 1: q-blocks start by the length of their walks (at most 64 slots)
   float scale;
 };
 

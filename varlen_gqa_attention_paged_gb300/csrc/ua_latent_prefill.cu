@@ -75,8 +75,9 @@ int prefill(const ua_latent_prefill_t& a, cudaStream_t st) {
   p.lse = a.lse;
   p.cu_seqlens_q = a.cu_seqlens_q;
   p.cu_seqlens_k = a.cu_seqlens_k;
-  int rc;
+  int rc, sms = 0;
   if ((rc = ua::status_word(&p.status)) != UA_OK) return rc;
+  if ((rc = ua::device_sm_count(&sms)) != UA_OK) return rc;
   p.num_seqs = a.num_seqs;
   p.total_q = a.total_q;
   p.total_k = a.total_k;
@@ -85,6 +86,8 @@ int prefill(const ua_latent_prefill_t& a, cudaStream_t st) {
   p.out_dtype = a.out_dtype;
   p.slots = static_cast<int>(slots);
   p.scale = a.scale;
+  // (where all start at once, or all are short, the order is nothing: it costs 500 cycles)
+  p.by_length = slots <= 64 && slots * a.num_heads > sms && a.max_seqlen_k > 2 * kBlockTokens;
   const auto launch =
       a.nope_dim == 64 ? ua::launch_latent_prefill_n64 : ua::launch_latent_prefill_n128;
   return launch(p, a.value_dim, bf16, st) == cudaSuccess ? UA_OK : UA_ERR_CUDA;

@@ -174,9 +174,9 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
   grid_dependency_wait();
   grid_launch_dependents();
 
-  // longest walks first: by length, or (many slots) in reverse order
+  // longest walks first: by length, or (many slots, or all at once) in reverse order
   const int slots = static_cast<int>(gridDim.y), y = static_cast<int>(blockIdx.y);
-  const int x = slots <= 64 ? latent_slot_by_length(p.cu_seqlens_q, p.cu_seqlens_k, p.num_seqs, slots,
+  const int x = p.by_length ? latent_slot_by_length(p.cu_seqlens_q, p.cu_seqlens_k, p.num_seqs, slots,
                                                     y, TB)
                             : slots - 1 - y;
   const LatentSeqOf sq = latent_seq_of_slot(p.cu_seqlens_q, p.cu_seqlens_k, p.num_seqs, x, TB);

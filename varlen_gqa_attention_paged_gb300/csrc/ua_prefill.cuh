@@ -42,18 +42,6 @@ __device__ __forceinline__ void umma_f16_ss_at(uint32_t d_tmem, uint32_t a16, ui
       : "memory");
 }
 
-// Whether `v` holds in any of the barrier's threads; a barrier too.
-__device__ __forceinline__ bool named_bar_any(int id, int threads, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(threads)
-      : "memory");
-  return r != 0;
-}
-
 // The descriptor of an operand at address 16 a16: 128-byte swizzle, stride byte offset 1024.
 __device__ __forceinline__ uint64_t smem_desc_at(uint32_t a16, uint32_t lbo) {
   constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);

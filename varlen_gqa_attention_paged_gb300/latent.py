@@ -73,11 +73,11 @@ class _Prepared:
         self._call = call
         self._ref = ctypes.byref(call)
         self._static = static
+        self._names = tuple(tensors)
         self._meta = {n: (t.shape, t.stride(), t.dtype, t.device)
                       for n, t in tensors.items() if t is not None}
-        # the tensors passed last: one passed again, as most are, costs four comparisons
-        self._now = {n: (None, 0, None, None) if t is None else
-                     (t, t.data_ptr(), t.shape, t.stride()) for n, t in tensors.items()}
+        # the tensors passed last, and where they were
+        self._now = {n: (t, 0 if t is None else t.data_ptr()) for n, t in tensors.items()}
         dev = next(t.device for t in tensors.values() if t is not None)
         self._device = dev.index
         self._one_device = torch.cuda.device_count() == 1
@@ -86,28 +86,32 @@ class _Prepared:
     def _step(self, passed, stream):
         now = self._now
         new = None
-        for name, t in passed:
+        for name, t in zip(self._names, passed):
             if t is None:
                 continue
-            kept, ptr, shape, stride = now[name]
-            if t is not kept or t.data_ptr() != ptr or t.shape != shape or t.stride() != stride:
-                if (t.shape, t.stride(), t.dtype, t.device) != self._meta.get(name):
-                    raise ValueError(f"{name}: shape, strides, dtype or device differs from the "
-                                     "prepared call")
+            kept, at = now[name]
+            meta = self._meta.get(name)
+            # (the layout of a tensor that is passed again may have changed in place)
+            if meta is None or t.shape != meta[0] or t.stride() != meta[1] or \
+                    (t is not kept and (t.dtype != meta[2] or t.device != meta[3])):
+                raise ValueError(f"{name}: shape, strides, dtype or device differs from the "
+                                 "prepared call")
+            ptr = t.data_ptr()
+            if t is not kept or ptr != at:
                 new = new or []
-                new.append((name, t))
+                new.append((name, t, ptr, at))
         if new:  # (none is taken if one was refused)
-            for name, t in new:
-                setattr(self._call, name, t.data_ptr())
-                now[name] = (t, t.data_ptr(), t.shape, t.stride())
+            for name, t, ptr, at in new:
+                now[name] = (t, ptr)
+                if ptr != at:
+                    setattr(self._call, name, ptr)
         if stream is not None:
             self._stream = stream
-        handle = self._stream.cuda_stream
         if self._one_device or torch.cuda.current_device() == self._device:
-            rc = self._entry(self._ref, handle)
+            rc = self._entry(self._ref, self._stream.cuda_stream)
         else:
             with torch.cuda.device(self._device):
-                rc = self._entry(self._ref, handle)
+                rc = self._entry(self._ref, self._stream.cuda_stream)
         if rc != 0:
             raise UaError(rc, self._what)
 
@@ -125,10 +129,8 @@ class PreparedAppendLatent(_Prepared):
 
     def __call__(self, latent=None, k_rope=None, q_rope=None, q_rope_out=None, cu_seqlens_q=None,
                  seq_lens_k=None, block_table=None, positions=None, stream=None):
-        self._step((("latent", latent), ("k_rope", k_rope), ("q_rope", q_rope),
-                    ("q_rope_out", q_rope_out), ("cu_seqlens_q", cu_seqlens_q),
-                    ("seq_lens_k", seq_lens_k), ("block_table", block_table),
-                    ("positions", positions)), stream)
+        self._step((latent, k_rope, q_rope, q_rope_out, cu_seqlens_q, seq_lens_k, block_table,
+                    positions), stream)
         return self._last("q_rope_out")
 
 
@@ -238,9 +240,7 @@ class PreparedLatentAttention(_Prepared):
 
     def __call__(self, q=None, cu_seqlens_q=None, seq_lens_k=None, block_table=None,
                  tree_mask=None, out=None, lse=None, stream=None):
-        self._step((("q", q), ("cu_seqlens_q", cu_seqlens_q), ("seq_lens_k", seq_lens_k),
-                    ("block_table", block_table), ("tree_mask", tree_mask), ("out", out),
-                    ("lse", lse)), stream)
+        self._step((q, cu_seqlens_q, seq_lens_k, block_table, tree_mask, out, lse), stream)
         out, lse = self._last("out"), self._last("lse")
         return out if lse is None else (out, lse)
 
@@ -371,8 +371,11 @@ def tree_mask(parents, cu_seqlens_q, seq_lens_k, *, max_seqlen_q: int, mask=None
     call = _lib.UaTree(parents.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens_k.data_ptr(),
                        mask.data_ptr(), positions.data_ptr(), max(mask.stride(0), mask.shape[1]),
                        num_seqs, total_q, int(max_seqlen_q), mask.shape[1])
-    with torch.cuda.device(dev):
-        rc = lib.ua_tree_mask(ctypes.byref(call), ctypes.c_void_p(stream.cuda_stream))
+    if torch.cuda.current_device() == dev.index:
+        rc = lib.ua_tree_mask(ctypes.byref(call), stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = lib.ua_tree_mask(ctypes.byref(call), stream.cuda_stream)
     if rc != 0:
         raise UaError(rc, "ua_tree_mask")
     return mask, positions
@@ -387,9 +390,7 @@ class PreparedLatentPrefill(_Prepared):
 
     def __call__(self, q=None, k_nope=None, k_rope=None, v=None, cu_seqlens_q=None,
                  cu_seqlens_k=None, out=None, lse=None, stream=None):
-        self._step((("q", q), ("k_nope", k_nope), ("k_rope", k_rope), ("v", v),
-                    ("cu_seqlens_q", cu_seqlens_q), ("cu_seqlens_k", cu_seqlens_k), ("out", out),
-                    ("lse", lse)), stream)
+        self._step((q, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, out, lse), stream)
         out, lse = self._last("out"), self._last("lse")
         return out if lse is None else (out, lse)
 
