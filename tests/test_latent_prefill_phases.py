@@ -16,6 +16,7 @@ TILES = 4
 class Model:
     def __init__(self, n, key_blocks, value_blocks, ring, rng, early=False):
         self.n, self.kb, self.vb, self.ring, self.rng = n, key_blocks, value_blocks, ring, rng
+        self.last = 1 if n[1] > 0 else 0
         self.early = early      # hand a value tile on behind the first q tile's product
         self.per = key_blocks + value_blocks
         self.full = [Bar(key_blocks if v == 0 else value_blocks)
@@ -52,7 +53,6 @@ class Model:
 
     def issue(self):
         nt, out = max(self.n), self.queue
-        last = 1 if self.n[1] > 0 else 0
         for j in range(nt + 1):
             i = j - 1
             while i >= 0 and not self.there(i, 1):
@@ -62,15 +62,13 @@ class Model:
                     while not self.p_full[qt].done(i & 1):
                         yield
                     out += [("read", i * self.per + self.kb + e) for e in range(self.vb)]
-                if i >= 0 and qt == (0 if self.early else last):
+                if i >= 0 and qt == (0 if self.early else self.last):
                     out.append(("commit", self.empty[self.bar(i, 1)]))
                 if j < self.n[qt]:
                     while not self.there(j, 0):
                         yield
                     out += [("read", j * self.per + e) for e in range(self.kb)]
                     out.append(("commit", self.s_full[qt]))
-                if j < nt and qt == last:
-                    out.append(("commit", self.empty[self.bar(j, 0)]))
                 yield
 
     def tensor(self):
@@ -87,6 +85,8 @@ class Model:
         for t in range(self.n[qt]):
             while not self.s_full[qt].done(t & 1):
                 yield
+            if qt == self.last:     # both q tiles' products with the keys are done
+                self.empty[self.bar(t, 0)].arrive()
             yield
             self.p_full[qt].arrive()
             yield

@@ -246,7 +246,8 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
     // ======================================================== MMA issue
     // Step j: for each q tile, O += P_{j-1} V_{j-1} (which frees its S/P columns), then
     // S = Q K_j^T.  Tensor-core operations of one thread run in issue order, and the order keeps
-    // one q tile in the softmax while the other has the tensor cores.
+    // one q tile in the softmax while the other has the tensor cores.  Their queue is a few deep
+    // only, so that what lies between two products leaves them idle: the softmax hands K_j on.
     constexpr uint32_t kIdQK = umma_idesc_f16(BM, BN, BF16, false);
     constexpr uint32_t kIdPV = umma_idesc_f16(BM, V, BF16, true);
     constexpr uint32_t kIdPVBlock = umma_idesc_f16(BM, 64, BF16, true);
@@ -305,7 +306,6 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
           }
           umma_commit_warp(&s_full[qt]);
         }
-        if (last && j < nt) umma_commit_warp(&empty[bar_of(j, 0)]);
       }
       kslot = kslot + PER >= RING ? kslot + PER - RING : kslot + PER;
     }
@@ -323,11 +323,14 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
     const float c = p.scale * kLog2e;
     const uint32_t tS = tmem + qt * C::kTmemStride + ((32u * quad) << 16);
     const uint32_t tO = tS + BN;
+    const bool hands_on = quad == 0 && qt == (n1 > 0 ? 1 : 0);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int n = 0; n < n_tiles; ++n) {
       if (!pf_wait_warp(&s_full[qt], n & 1, abort_flag, p.status)) { ok = false; break; }
       tc_fence_after();
+      // (the commit behind the last q tile's S covers both tiles' products with K_n)
+      if (hands_on && lane == 0) mbar_arrive(&empty[bar_of(n, 0)]);
       uint32_t s[4][32];
 #pragma unroll
       for (int g = 0; g < 4; ++g) tmem_ld32(tS + 32 * g, s[g]);
