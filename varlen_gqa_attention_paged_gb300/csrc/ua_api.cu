@@ -16,6 +16,7 @@
 
 #include "ua.h"
 #include "ua_internal.h"
+#include "ua_latent.h"
 
 namespace {
 

@@ -25,12 +25,6 @@ constexpr float kScaleMax = 1099511627776.f;        // 2^40
 // SM count.
 int status_word(unsigned int** out);
 int device_sm_count(int* out);
-// The library's own scratch on the current device for work on `stream`: grow-only, one for each
-// stream and one for each capture.
-int library_workspace(cudaStream_t stream, size_t bytes, void** out);
-// A tensor map of f16 or bf16 elements, boxes in the 128-byte swizzle, zeros outside the tensor.
-bool encode_half_map(CUtensorMap* map, const void* base, bool bf16, int rank,
-                     const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box);
 
 // Everything one launch of the attention tile kernel needs (passed by value).
 struct AttnParams {

@@ -23,7 +23,7 @@
 #include <atomic>
 
 #include "ua_latent.h"
-#include "ua_prefill.cuh"
+#include "ua_latent_tc.cuh"
 
 #include "ua.h"
 

@@ -5,6 +5,13 @@
 
 namespace ua {
 
+// The library's own scratch on the current device for work on `stream`: grow-only, one for each
+// stream and one for each capture.
+int library_workspace(cudaStream_t stream, size_t bytes, void** out);
+// A tensor map of f16 or bf16 elements, boxes in the 128-byte swizzle, zeros outside the tensor.
+bool encode_half_map(CUtensorMap* map, const void* base, bool bf16, int rank,
+                     const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box);
+
 // Rows (query token x head) of one CTA's tile, and keys of one tile.
 constexpr int kLatRows = 64;
 constexpr int kLatKeys = 64;
