@@ -36,7 +36,7 @@ struct AppendLatentParams {
 };
 
 template <int L, bool BF>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, 6)
     ua_append_latent_kernel(const __grid_constant__ AppendLatentParams p) {
   constexpr int kPer = (L + 255) / 256;  // 16-byte chunks of the latent that a lane takes
   constexpr int U = 4;                   // passes whose loads are in flight together
@@ -47,27 +47,46 @@ __global__ void __launch_bounds__(128)
   const int t = static_cast<int>(task / p.warps_per_token);
   const int part = static_cast<int>(task % p.warps_per_token);
   if (t >= p.total_q) return;
-  // what does not need the token's place is loaded first
-  uint4 x[kPer];
+  const int c = lane % p.lanes, slot = lane / p.lanes;
+  const bool inter = p.interleaved != 0;
+  // the lane's two chunks of a rope row, half a row apart: halves apart they are the two sides of its
+  // eight pairs, interleaved four pairs each (so that an access covers whole sectors)
+  struct {
+    int lo, hi;
+  } const ch = {8 * c, p.rope_dim / 2 + 8 * c};
+  // What does not need the token's place is loaded first: the search, the table and the block table
+  // are a chain of three loads.
+  uint4 x[kPer], lo[U], hi[U];
+  const uint16_t* const src = p.q_rope + t * p.q_stride[0];
+  const int h0 = (part - 1) * p.pass_group * p.heads_per_pass;
+  const int h1 = min(p.heads, h0 + p.pass_group * p.heads_per_pass);
+  auto load_heads = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = base + u * p.heads_per_pass + slot;
+      if (slot >= p.heads_per_pass || h >= h1) continue;
+      lo[u] = *reinterpret_cast<const uint4*>(src + h * p.q_stride[1] + ch.lo);
+      hi[u] = *reinterpret_cast<const uint4*>(src + h * p.q_stride[1] + ch.hi);
+    }
+  };
   if (part == 0) {
-    const uint4* src = reinterpret_cast<const uint4*>(p.latent + t * p.latent_stride);
+    const uint4* from = reinterpret_cast<const uint4*>(p.latent + t * p.latent_stride);
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (32 * i + lane < L / 8) x[i] = __ldg(src + 32 * i + lane);
+      if (32 * i + lane < L / 8) x[i] = __ldg(from + 32 * i + lane);
+    if (slot == 0) {
+      const uint16_t* k = p.k_rope + t * p.k_rope_stride;
+      lo[0] = __ldg(reinterpret_cast<const uint4*>(k + ch.lo));
+      hi[0] = __ldg(reinterpret_cast<const uint4*>(k + ch.hi));
+    }
+  } else {
+    load_heads(h0);
   }
   const ua::SeqOf s = ua::seq_of(p.cu_seqlens_q, p.seq_lens_k, p.num_seqs, t,
                                  [](int c, int) -> long long { return c; });
   if (t < s.q0 || t >= s.end) return;
   const int at = s.kv_len - (s.end - t);
   if (at < 0) return;
-  const int c = lane % p.lanes, slot = lane / p.lanes;
-  const bool inter = p.interleaved != 0;
-  // the lane's two chunks, half a row apart: halves apart they are the two sides of its eight pairs,
-  // interleaved four pairs each (chunks side by side made each access write half sectors:
-  // 8192 tokens of 64 heads took 30.2 us)
-  struct {
-    int lo, hi;
-  } const ch = {8 * c, p.rope_dim / 2 + 8 * c};
   float cs[8], sn[8];
   if (p.cos_sin != nullptr) {
     const int pos = p.positions != nullptr ? __ldg(p.positions + t) : at;
@@ -104,12 +123,6 @@ __global__ void __launch_bounds__(128)
     }
     uint16_t* const row = p.cache + (static_cast<size_t>(blk) * p.block_size + at % p.block_size) *
                                         static_cast<size_t>(L + p.rope_dim);
-    uint4 lo, hi;
-    if (slot == 0) {
-      const uint16_t* src = p.k_rope + t * p.k_rope_stride;
-      lo = __ldg(reinterpret_cast<const uint4*>(src + ch.lo));
-      hi = __ldg(reinterpret_cast<const uint4*>(src + ch.hi));
-    }
     if (p.weight != nullptr) {
       float v[kPer][8], sum = 0.f;
 #pragma unroll
@@ -157,27 +170,17 @@ __global__ void __launch_bounds__(128)
     for (int i = 0; i < kPer; ++i)
       if (32 * i + lane < L / 8) reinterpret_cast<uint4*>(row)[32 * i + lane] = x[i];
     if (slot == 0) {
-      turned(lo, hi);
-      *reinterpret_cast<uint4*>(row + L + ch.lo) = lo;
-      *reinterpret_cast<uint4*>(row + L + ch.hi) = hi;
+      turned(lo[0], hi[0]);
+      *reinterpret_cast<uint4*>(row + L + ch.lo) = lo[0];
+      *reinterpret_cast<uint4*>(row + L + ch.hi) = hi[0];
     }
     return;
   }
 
   // query heads: passes of heads_per_pass, U of them at a time
-  const uint16_t* const src = p.q_rope + t * p.q_stride[0];
   uint16_t* const dst = p.q_rope_out + t * p.q_out_stride[0];
-  const int h0 = (part - 1) * p.pass_group * p.heads_per_pass;
-  const int h1 = min(p.heads, h0 + p.pass_group * p.heads_per_pass);
   for (int base = h0; base < h1; base += U * p.heads_per_pass) {
-    uint4 lo[U], hi[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = base + u * p.heads_per_pass + slot;
-      if (slot >= p.heads_per_pass || h >= h1) continue;
-      lo[u] = *reinterpret_cast<const uint4*>(src + h * p.q_stride[1] + ch.lo);
-      hi[u] = *reinterpret_cast<const uint4*>(src + h * p.q_stride[1] + ch.hi);
-    }
+    if (base > h0) load_heads(base);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = base + u * p.heads_per_pass + slot;
