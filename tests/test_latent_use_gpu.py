@@ -144,7 +144,7 @@ def test_results_are_the_same_every_time():
 
 
 def captured(run):
-    stream = torch.cuda.Stream()
+    stream = torch.cuda.Stream(priority=-1)
     with torch.cuda.stream(stream):
         run(stream)
         graph = torch.cuda.CUDAGraph()
@@ -182,7 +182,7 @@ def test_a_captured_step_follows_the_lengths():
 def test_two_graphs_of_one_stream_run_side_by_side():
     steps = [step_of([(1, 6000), (1, 3000)], seed=s) for s in (0, 10)]
     want = [s[0]().clone() for s in steps]
-    stream = torch.cuda.Stream()
+    stream = torch.cuda.Stream(priority=-1)
     graphs = []
     for s, _ in steps:
         s(stream=stream)
@@ -193,7 +193,7 @@ def test_two_graphs_of_one_stream_run_side_by_side():
         graphs.append(g)
     for s, _ in steps:
         s._last("out").zero_()
-    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    sides = [torch.cuda.Stream(priority=-1), torch.cuda.Stream(priority=-1)]
     torch.cuda.synchronize()
     for _ in range(20):
         for g, side in zip(graphs, sides):
@@ -207,7 +207,7 @@ def test_two_graphs_of_one_stream_run_side_by_side():
 def test_two_streams_at_once():
     steps = [step_of([(1, 6000), (2, 3000)], seed=s) for s in (0, 10)]
     want = [s[0]().clone() for s in steps]
-    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    sides = [torch.cuda.Stream(priority=-1), torch.cuda.Stream(priority=-1)]
     torch.cuda.synchronize()
     for _ in range(20):
         for (s, _), side in zip(steps, sides):
