@@ -488,7 +488,7 @@ typedef struct {
  */
 int ua_latent_attention(const ua_latent_t* call, void* stream);
 
-/* Bytes of scratch that the call needs on the current device (0 on an invalid argument too). */
+/* Bytes of scratch that the call needs on the current device (0: none, or an invalid argument). */
 size_t ua_latent_workspace_bytes(const ua_latent_t* call);
 
 /* One ua_latent_prefill call.  Strides are in elements: multiples of 8 (the last dim has stride 1). */

@@ -81,6 +81,40 @@ def test_attention(lens, h, latent, rope, bs, dtype):
     compare(t, rope, out_dtype=F32)
 
 
+FAR = 1 << 20   # a bound of the lengths that leaves a cluster a row tile no good
+
+
+@pytest.mark.parametrize("lens,h,latent,rope,bs,dtype", CASES)
+def test_attention_by_even_shares(lens, h, latent, rope, bs, dtype):
+    t = make(lens, h, latent, rope, bs, dtype)
+    compare(t, rope, out_dtype=F32, max_seqlen_k=FAR)
+
+
+@pytest.mark.parametrize("lens,h,latent", [
+    # row tiles of 64 token-heads, the keys of each in 1, 2, 4, 8, 4 and 8 parts, parts without keys,
+    # clusters without a row tile
+    ([(1, 300)] * 100, 16, 512),
+    ([(1, 150), (0, 9), (1, 0)] * 17, 16, 512),
+    ([(1, 333), (1, 70), (0, 100), (1, 64), (3, 3)] * 5, 16, 512),
+    ([(5, 700), (1, 1), (2, 129)], 64, 512),
+    ([(1, 200), (4, 66)], 7, 256),
+    ([(2, 500), (31, 90)], 5, 128),
+])
+@pytest.mark.parametrize("masked", [False, True])
+def test_attention_by_parts(lens, h, latent, masked):
+    t = make(lens, h, latent, bs=16)
+    mask = masks(lens) if masked else None
+    q, cache, cu, sl, bt = (x.cuda() for x in t)
+    for far, whole in ((None, True), (FAR, False)):
+        size = sizes(t[2], t[3])
+        step = ua.prepare_latent_attention(
+            q, cache, cu, sl, bt, scale=0.08, max_seqlen_q=size["max_seqlen_q"],
+            max_seqlen_k=far or size["max_seqlen_k"])
+        assert (ua.latent_workspace_bytes(step) == 0) == whole
+    compare(t, mask=mask)
+    compare(t, mask=mask, out_dtype=F32)
+
+
 def masks(lens, seed=0):
     """Random masks: not trees, rows that see nothing among them."""
     g = torch.Generator().manual_seed(seed)

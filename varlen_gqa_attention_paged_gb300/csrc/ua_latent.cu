@@ -204,14 +204,38 @@ int check(const ua_latent_t& a) {
 // CTAs of a worker and workers of a call on `sms` SMs, from the host's sizes (a bound of the work:
 // the kernel takes its shares from the lengths themselves).
 constexpr int kMinShare = 2;
-void shape(const ua_latent_t& a, int sms, int* workers, int* cl) {
+// Few row tiles over few keys take a cluster of up to kSpread CTAs each instead (`spread` CTAs; 0: even
+// shares), with an even part of the keys a CTA: that saves the merge kernel and the second row tile
+// that a share may reach into, but the longest sequence sets the time.  So a part may be longer than a
+// share by one tile where there is one sequence, and otherwise longer by three (five, where a worker
+// is two CTAs) than half a share, which is what shares come to where lengths are spread from 0 up to
+// the longest.  Clusters of eight are placed onto seven eighths of the SMs at most (17 of them took
+// 12.4 us where 17 of four took 10.7).  In us, parts against even shares (tiles of each):
+//   16 heads:   1 x 700 keys 10.6 : 12.2 (2 : 2), 1 x 1500 13.1 : 13.1 (3 : 2), 1 x 2500 16.2 : 13.4 (5 : 2),
+//               28 x 1000 15.6 : 19.2 (4 : 3), 28 x 2500 25.2 : 25.3 (10 : 8), 50 x 300 13.5 : 18.4 (3 : 2),
+//               50 x 2500 43.4 : 42.2 (20 : 14), 100 x 300 16.2 : 25.0 (5 : 4)
+//   128 heads:  1 x 700 14.1 : 13.6 (2 : 2), 1 x 2500 20.2 : 17.0 (5 : 2), 12 x 300 14.6 : 20.8 (2 : 2),
+//               25 x 1000 24.4 : 30.6 (8 : 6)
+constexpr int kSpread = 8;
+void shape(const ua_latent_t& a, int sms, int* workers, int* cl, int* spread) {
   *cl = static_cast<long long>(a.max_seqlen_q) * a.num_heads > ua::kLatRows ? 2 : 1;
-  const long long tiles =
-      static_cast<long long>(a.total_q) * a.num_heads / (ua::kLatRows * *cl) + a.num_seqs;
-  const long long keys = std::max(1, (a.max_seqlen_k + ua::kLatKeys - 1) / ua::kLatKeys);
+  const long long rows = static_cast<long long>(a.total_q) * a.num_heads;
+  const long long tiles = rows / (ua::kLatRows * *cl) + a.num_seqs;
+  const long long keys = (std::max(a.max_seqlen_k, 1) + ua::kLatKeys - 1) / ua::kLatKeys;
   const long long most = std::max(1, sms / *cl);
   *workers = static_cast<int>(
       std::max(1LL, std::min(most, (tiles * keys + kMinShare - 1) / kMinShare)));
+  *spread = 0;
+  const long long slots = rows / ua::kLatRows + a.num_seqs;  // row tiles at most
+  int parts = 1;
+  while (parts < kSpread && parts < keys && slots * 2 * parts <= (parts < 4 ? sms : sms * 7 / 8))
+    parts *= 2;
+  const long long share = std::max<long long>(kMinShare, (tiles * keys + most - 1) / most);
+  const long long longest = a.num_seqs > 1 ? share / 2 + 1 + 2 * *cl : share + 1;
+  if (slots * parts > sms || (keys + parts - 1) / parts > longest) return;
+  *spread = parts;
+  *workers = static_cast<int>(slots);
+  *cl = 1;
 }
 
 // Rows [width] in boxes of 64 elements x `box_rows`.
@@ -246,14 +270,16 @@ int attend(const ua_latent_t& a, cudaStream_t st) {
   int sms = 0;
   if ((rc = ua::device_sm_count(&sms)) != UA_OK) return rc;
   ua::LatentParams p{};
-  shape(a, sms, &p.workers, &p.cl);
-  const int ctas = p.workers * p.cl;
-  const size_t need = ua::latent_scratch_bytes(ctas, a.latent_dim);
+  shape(a, sms, &p.workers, &p.cl, &p.spread);
+  const int ctas = p.spread > 0 ? 0 : p.workers * p.cl;  // that need scratch
   void* ws = a.workspace;
-  if (ws != nullptr) {
-    if (a.workspace_bytes < need || !aligned(ws, 16)) return UA_ERR_WORKSPACE;
-  } else if ((rc = ua::library_workspace(st, need, &ws)) != UA_OK) {
-    return rc;
+  if (ctas > 0) {
+    const size_t need = ua::latent_scratch_bytes(ctas, a.latent_dim);
+    if (ws != nullptr) {
+      if (a.workspace_bytes < need || !aligned(ws, 16)) return UA_ERR_WORKSPACE;
+    } else if ((rc = ua::library_workspace(st, need, &ws)) != UA_OK) {
+      return rc;
+    }
   }
   const bool bf16 = a.dtype == UA_DT_BF16;
   p.box_rows = std::min(ua::kLatKeys, a.block_size & -a.block_size);
@@ -274,11 +300,13 @@ int attend(const ua_latent_t& a, cudaStream_t st) {
   p.tree = a.tree_mask;
   p.tree_stride = a.tree_mask_stride;
   p.tree_words = a.tree_words;
-  const size_t slots = static_cast<size_t>(ctas) * 2 * ua::kLatRows;
-  p.ws_acc = static_cast<float*>(ws);
-  p.ws_meta = reinterpret_cast<int4*>(p.ws_acc + slots * a.latent_dim);
-  p.ws_m = reinterpret_cast<float*>(p.ws_meta + ctas);
-  p.ws_l = p.ws_m + slots;
+  if (ctas > 0) {
+    const size_t slots = static_cast<size_t>(ctas) * 2 * ua::kLatRows;
+    p.ws_acc = static_cast<float*>(ws);
+    p.ws_meta = reinterpret_cast<int4*>(p.ws_acc + slots * a.latent_dim);
+    p.ws_m = reinterpret_cast<float*>(p.ws_meta + ctas);
+    p.ws_l = p.ws_m + slots;
+  }
   if ((rc = ua::status_word(&p.status)) != UA_OK) return rc;
   p.num_seqs = a.num_seqs;
   p.total_q = a.total_q;
@@ -294,7 +322,7 @@ int attend(const ua_latent_t& a, cudaStream_t st) {
                       : a.latent_dim == 256 ? ua::launch_latent_l256
                                             : ua::launch_latent_l128;
   if (launch(p, bf16, st) != cudaSuccess) return UA_ERR_CUDA;
-  if (p.workers == 1) return UA_OK;  // no tile is shared
+  if (p.workers == 1 || p.spread > 0) return UA_OK;  // no tile is shared through scratch
   ua::LatentMergeParams m{};
   m.out = a.out;
   m.lse = a.lse;
@@ -324,8 +352,8 @@ extern "C" int ua_latent_attention(const ua_latent_t* call, void* stream) {
 }
 
 extern "C" size_t ua_latent_workspace_bytes(const ua_latent_t* call) {
-  int sms = 0, workers = 0, cl = 0;
+  int sms = 0, workers = 0, cl = 0, spread = 0;
   if (call == nullptr || check(*call) != UA_OK || ua::device_sm_count(&sms) != UA_OK) return 0;
-  shape(*call, sms, &workers, &cl);
-  return ua::latent_scratch_bytes(workers * cl, call->latent_dim);
+  shape(*call, sms, &workers, &cl, &spread);
+  return spread > 0 ? 0 : ua::latent_scratch_bytes(workers * cl, call->latent_dim);
 }

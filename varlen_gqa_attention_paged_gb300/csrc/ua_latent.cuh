@@ -17,7 +17,9 @@
 // Work split: all (row tile, key tile) pairs of the batch, row tile after row tile, are cut into
 // equal shares for the workers (one CTA, or two that take neighbouring row tiles of a sequence over
 // the same keys, so that the second read of a key hits L2).  A row tile that ends up with
-// several workers leaves fp32 partial rows for the merge kernel.
+// several workers leaves fp32 partial rows for the merge kernel.  A few row tiles over few keys take
+// another split (SPREAD): a cluster of CTAs a row tile, an even part of its keys each, whose rows meet
+// through distributed shared memory, without scratch and without a second kernel.
 #pragma once
 
 #include <atomic>
@@ -55,6 +57,7 @@ struct LatentCfg {
   static constexpr int kTmemCols = kTmemO + kMB * kLatRows > 256 ? 512 : 256;
   static constexpr int kThreads = 32 * (10 + kParts);  // softmax (8), MMA issue (2), a part's copies each
   static_assert(L % 128 == 0 && L <= 512 && kMB % kHalves == 0);
+  static_assert(kStages * kTileBytes >= kLatRows * L * 4);  // a part's rows, where tiles were
   static_assert(kStages >= 2 && kSmemBytes + 96 <= 227 * 1024);
 };
 
@@ -84,6 +87,32 @@ struct LatentWalk {
     rows = rows_of(p, q0, q1);
     rt = row_tiles(p, rows);
     kt = key_tiles(kv_len);
+  }
+
+  // Part z of `parts` of the keys of row tile x (tiles of a sequence counted from floor(first row /
+  // 64) + b): none left where there is no such tile, or no part.
+  __device__ __forceinline__ LatentWalk(const LatentParams& p, int x, int z, int parts) {
+    const int lane = threadIdx.x & 31;
+    pos = left = 0;
+    share = 1;
+    b = t = j = 0;
+    q0 = q_len = kv_len = rows = rt = kt = 0;
+    for (int base = 0; base < p.num_seqs; base += 32) {
+      const int i = base + lane;
+      const int first = i < p.num_seqs ? __ldg(p.cu_seqlens_q + i) * p.heads / kLatRows + i : x + 1;
+      const unsigned m = __ballot_sync(0xffffffffu, first <= x);
+      if (m != 0u) b = base + 31 - __clz(m);
+      if (m != 0xffffffffu) break;
+    }
+    load(p);
+    t = x - (q0 * p.heads / kLatRows + b);
+    if (t < 0 || t >= rt) {
+      rows = 0;
+      return;
+    }
+    const int n = (kt + parts - 1) / parts;
+    j = min(z * n, kt);
+    left = min(n, kt - j);
   }
 
   // a / b, mostly of small numbers.
@@ -235,7 +264,58 @@ __device__ __forceinline__ float latent_lse(float m, float l) {
   return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-template <int L, bool BF16>
+// The rows of a tile from the parts in the cluster's shared memory: a warp of the cluster takes 256
+// elements (or a whole shorter row) at a time.
+template <int L>
+__device__ __forceinline__ void latent_join_parts(const LatentParams& p, uint32_t rows_at,
+                                                  uint32_t stats_at, int rows, int row0, int warp,
+                                                  int warps) {
+  constexpr int kPieces = L > 256 ? L / 256 : 1, kPer = L / kPieces / 128;  // float4s of a lane
+  const int lane = threadIdx.x & 31, parts = static_cast<int>(gridDim.y);
+  for (int e = warp; e < rows * kPieces; e += warps) {
+    const int r = e / kPieces, piece = e % kPieces;
+    float m = -INFINITY, l = 0.f;
+    if (lane < parts) {
+      const uint32_t at = cluster_map(stats_at + 4 * r, lane);
+      m = ld_cluster_f32(at);
+      l = ld_cluster_f32(at + 4 * kLatRows);
+    }
+    float M = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float f = l == 0.f ? 0.f : fast_exp2(m - M);
+    float sum = l == 0.f ? 0.f : l * f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    float4 acc[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = 0; k < parts; ++k) {
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+      if (__shfl_sync(0xffffffffu, l, k) == 0.f) continue;
+      const uint32_t at = cluster_map(rows_at + 4 * (r * L + piece * 256 + 4 * lane), k);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float4 v = ld_cluster_f32x4(at + 512 * i);
+        acc[i].x += v.x * fk;
+        acc[i].y += v.y * fk;
+        acc[i].z += v.z * fk;
+        acc[i].w += v.w * fk;
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const size_t to = static_cast<size_t>(row0 + r) * L + piece * 256 + 128 * i + 4 * lane;
+      store_two(p.out, to, acc[i].x * inv, acc[i].y * inv, p.out_dtype);
+      store_two(p.out, to + 2, acc[i].z * inv, acc[i].w * inv, p.out_dtype);
+    }
+    if (p.lse != nullptr && lane == 0 && piece == 0) p.lse[row0 + r] = latent_lse(M, sum);
+  }
+}
+
+template <int L, bool BF16, bool SPREAD>
 __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
     ua_latent_kernel(const __grid_constant__ LatentParams p) {
   using C = LatentCfg<L>;
@@ -270,7 +350,7 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int worker = blockIdx.x / p.cl, rank = blockIdx.x % p.cl;
+  const int worker = SPREAD ? blockIdx.x : blockIdx.x / p.cl, rank = SPREAD ? 0 : blockIdx.x % p.cl;
   constexpr int kQk = 8, kPv = 9, kCopy = 10;  // (kCopy + g copies part g)
 
   if (threadIdx.x == 0) {
@@ -312,7 +392,10 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
   grid_dependency_wait();
   grid_launch_dependents();
 
-  LatentWalk w(p, worker);
+  LatentWalk w = SPREAD ? LatentWalk(p, worker, blockIdx.y, gridDim.y) : LatentWalk(p, worker);
+  // SPREAD: the row tile, in every CTA of the cluster
+  const int tile_rows = SPREAD ? min(kLatRows, w.rows - w.t * kLatRows) : 0;
+  const int tile_row0 = SPREAD ? w.q0 * p.heads + w.t * kLatRows : 0;
   int it = 0;  // key tiles of all segments so far
   int sg = 0;  // segments with key tiles so far
   bool ok = true;
@@ -430,7 +513,7 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
       ok = pf_wait_warp(q_full, sg & 1, abort_flag, p.status);
       for (int n = 0; ok && n < s.nt; ++n, ++it) {
         const int st = it % S;
-        const uint32_t qd = smem_addr(sQ) >> 4, kd = smem_addr(sK + st * C::kTileBytes) >> 4;
+        const uint32_t qd = smem_units(sQ), kd = smem_units(sK + st * C::kTileBytes);
         const uint32_t tS = tmem + (it & 1) * kLatKeys;
         uint64_t* const full = &k_full[st * C::kParts];
         // the scores of two tiles before have been read
@@ -480,7 +563,7 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t vd = smem_addr(sK + st * C::kTileBytes) >> 4, pd = smem_addr(sP) >> 4;
+        const uint32_t vd = smem_units(sK + st * C::kTileBytes), pd = smem_units(sP);
 #pragma unroll
         for (int mb = 0; mb < C::kMB; ++mb) {
 #pragma unroll
@@ -516,11 +599,11 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
     for (; w.left > 0; w.next(p)) {
       const LatentSeg s(p, w, rank);
       const int grow0 = w.q0 * p.heads + s.row0;  // its first row in q and out
-      const bool whole = w.j == 0 && w.length() == w.kt;
+      const bool whole = !SPREAD && w.j == 0 && w.length() == w.kt;
       const int slot = 2 * blockIdx.x + (w.j == 0 ? 1 : 0);
       const int rows = s.rows;
       if (rows <= 0) continue;
-      if (w.j == 0 && !whole)
+      if (!SPREAD && w.j == 0 && !whole)
         meta = make_int4(grow0, rows,
                          static_cast<int>((w.pos + w.kt - 1) / w.share) - worker + 1, 0);
       const bool rv[2] = {ra < rows, ra + 8 < rows};
@@ -696,6 +779,11 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
         const int r = ra + 8 * k;
         if (half != 0 || cq != 0) continue;
         const float sum = l[k] + sT[(it & 1) * 2 * kLatRows + r];
+        if constexpr (SPREAD) {
+          sF[r] = m[k];
+          sF[kLatRows + r] = ok ? sum : NAN;  // (after a wait that gave up the tile's rows are NaN)
+          continue;
+        }
         // (a row that saw no key is 0; NaN stays)
         f[r] = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
         if (!rv[k] || !ok) continue;
@@ -720,6 +808,13 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          if constexpr (SPREAD) {
+            float* const dst = reinterpret_cast<float*>(sK) + rb * L + blk + d;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (rb + e < rows) dst[e * L] = __uint_as_float(o[e]);
+            continue;
           }
           if (!whole) {
             float* const dst = p.ws_acc + static_cast<size_t>(slot * kLatRows + rb) * L + blk + d;
@@ -753,18 +848,31 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
       }
       named_bar_sync(1, 256);  // the factors have been read
     }
-    if (threadIdx.x == 0) p.ws_meta[blockIdx.x] = ok ? meta : make_int4(0, 0, 0, 0);
+    if constexpr (SPREAD) {
+      if (sg == 0 && threadIdx.x < kLatRows) {  // (a part that saw no key counts for nothing)
+        sF[threadIdx.x] = -INFINITY;
+        sF[kLatRows + threadIdx.x] = 0.f;
+      }
+    } else if (threadIdx.x == 0) {
+      p.ws_meta[blockIdx.x] = ok ? meta : make_int4(0, 0, 0, 0);
+    }
   }
 
   tc_fence_before();
   __syncthreads();
   if (warp == kQk) tmem_dealloc(tmem, C::kTmemCols);
+  if constexpr (SPREAD) {
+    cluster_sync();  // every part's rows, maxima and sums are in its shared memory
+    latent_join_parts<L>(p, smem_addr(sK), smem_addr(sF), tile_rows, tile_row0,
+                         blockIdx.y * (C::kThreads / 32) + warp, gridDim.y * (C::kThreads / 32));
+    cluster_sync_relaxed();  // no CTA leaves while another reads its shared memory
+  }
 }
 
-template <int L, bool BF16>
+template <int L, bool BF16, bool SPREAD>
 cudaError_t launch_latent_t(const LatentParams& p, cudaStream_t stream) {
   using C = LatentCfg<L>;
-  auto kern = ua_latent_kernel<L, BF16>;
+  auto kern = ua_latent_kernel<L, BF16, SPREAD>;
   static std::atomic<unsigned long long> configured{0};  // one bit per device
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -775,8 +883,16 @@ cudaError_t launch_latent_t(const LatentParams& p, cudaStream_t stream) {
     if (err != cudaSuccess) return err;
     configured.fetch_or(bit);
   }
-  return launch_pdl(kern, dim3(static_cast<unsigned>(p.workers * p.cl)), dim3(C::kThreads),
-                    C::kSmemBytes, stream, 1, p);
+  const dim3 grid = SPREAD ? dim3(static_cast<unsigned>(p.workers), static_cast<unsigned>(p.spread))
+                           : dim3(static_cast<unsigned>(p.workers * p.cl));
+  return launch_pdl(kern, grid, dim3(C::kThreads), C::kSmemBytes, stream, SPREAD ? p.spread : 1, p);
+}
+
+template <int L>
+cudaError_t launch_latent_any(const LatentParams& p, bool bf16, cudaStream_t s) {
+  if (p.spread > 0)
+    return bf16 ? launch_latent_t<L, true, true>(p, s) : launch_latent_t<L, false, true>(p, s);
+  return bf16 ? launch_latent_t<L, true, false>(p, s) : launch_latent_t<L, false, false>(p, s);
 }
 
 }  // namespace ua

@@ -38,8 +38,9 @@ struct LatentParams {
   int4* ws_meta;                // [ctas] of the tile that a CTA began: first row, rows, parts
   unsigned int* status;
   int num_seqs, total_q, max_blocks_per_seq, num_blocks, block_size, heads, rope_dim, out_dtype;
-  int workers;                  // groups of `cl` CTAs that share a tile's keys
+  int workers;                  // groups of `cl` CTAs that share a tile's keys; or (spread) row tiles
   int cl;                       // CTAs (tiles of kLatRows rows) of a worker: 1 or 2
+  int spread;                   // > 0: a cluster of that many CTAs a row tile, a part of its keys each
   int box_rows;                 // cache rows of a box: a power of two that divides the block size
   int min_share;                // key tiles that a worker takes at least
   float scale;

@@ -4,7 +4,7 @@
 namespace ua {
 
 cudaError_t launch_latent_l256(const LatentParams& p, bool bf16, cudaStream_t s) {
-  return bf16 ? launch_latent_t<256, true>(p, s) : launch_latent_t<256, false>(p, s);
+  return launch_latent_any<256>(p, bf16, s);
 }
 
 }  // namespace ua

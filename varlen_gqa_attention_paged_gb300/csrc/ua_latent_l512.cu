@@ -4,7 +4,7 @@
 namespace ua {
 
 cudaError_t launch_latent_l512(const LatentParams& p, bool bf16, cudaStream_t s) {
-  return bf16 ? launch_latent_t<512, true>(p, s) : launch_latent_t<512, false>(p, s);
+  return launch_latent_any<512>(p, bf16, s);
 }
 
 }  // namespace ua

@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
     constexpr uint32_t kIdPV = umma_idesc_f16(BM, V, BF16, true);
     constexpr uint32_t kIdPVBlock = umma_idesc_f16(BM, 64, BF16, true);
     const int rope_steps = p.rope_dim / 16;
-    const uint32_t ring0 = smem_addr(ring) >> 4, q0 = smem_addr(sQ) >> 4;
+    const uint32_t ring0 = smem_units(ring), q0 = smem_units(sQ);
     bool ok = true;
     int kslot = 0;  // ring slot of K_j's first block
     for (int j = 0; ok && j <= nt; ++j) {

@@ -29,6 +29,12 @@ __device__ __forceinline__ void umma_f16_ss_at(uint32_t d_tmem, uint32_t a16, ui
       : "memory");
 }
 
+// A shared-memory address as descriptors have it, in 16-byte units.  (In a CTA of a cluster the bits
+// above the window's 18 hold its rank, which would land in the leading byte offset.)
+__device__ __forceinline__ uint32_t smem_units(const void* at) {
+  return (smem_addr(at) & 0x3ffffu) >> 4;
+}
+
 // The descriptor of an operand at address 16 a16: 128-byte swizzle, stride byte offset 1024.
 __device__ __forceinline__ uint64_t smem_desc_at(uint32_t a16, uint32_t lbo) {
   constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
