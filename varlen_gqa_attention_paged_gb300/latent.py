@@ -324,7 +324,8 @@ def prepare_latent_attention(q, cache, cu_seqlens_q, seq_lens_k, block_table, *,
 
 
 def latent_workspace_bytes(prepared: PreparedLatentAttention) -> int:
-    """Bytes of scratch that a prepared call needs on its device (``workspace`` may be given)."""
+    """Bytes of scratch that a prepared call needs on its device: 0, or what ``workspace``
+    has to hold where one is given."""
     with torch.cuda.device(prepared._device):  # noqa: SLF001
         return _lib.load().ua_latent_workspace_bytes(prepared._ref)  # noqa: SLF001
 
@@ -344,38 +345,40 @@ def tree_mask(parents, cu_seqlens_q, seq_lens_k, *, max_seqlen_q: int, mask=None
     lib = _lib.load()
     if not parents.is_cuda:
         raise ValueError("parents must be a CUDA tensor")
-    dev = parents.device
-    for name, t in (("parents", parents), ("cu_seqlens_q", cu_seqlens_q),
-                    ("seq_lens_k", seq_lens_k)):
-        _ints(name, t, dev)
+    dev, i32 = parents.device, torch.int32
+    given = (parents, cu_seqlens_q, seq_lens_k) if positions is None else \
+        (parents, cu_seqlens_q, seq_lens_k, positions)
+    for t in given:
+        if t.dtype != i32 or t.dim() != 1 or t.device != dev or not t.is_contiguous():
+            raise ValueError("parents, cu_seqlens_q, seq_lens_k and positions must be contiguous "
+                             "int32 vectors on one device")
     total_q, num_seqs = parents.numel(), cu_seqlens_q.numel() - 1
-    if parents.dim() != 1 or num_seqs < 0 or seq_lens_k.numel() != num_seqs:
-        raise ValueError("parents [total_q], cu_seqlens_q [S + 1] and seq_lens_k [S] disagree")
-    words = max(1, (int(max_seqlen_q) + 31) // 32)
+    if num_seqs < 0 or seq_lens_k.numel() != num_seqs or \
+            (positions is not None and positions.numel() != total_q):
+        raise ValueError("parents [total_q], cu_seqlens_q [S + 1], seq_lens_k [S] and positions "
+                         "[total_q] disagree")
+    need = max(1, (int(max_seqlen_q) + 31) // 32)
     if mask is None:
-        mask = _new((total_q, words), torch.int32, dev, stream)
-    elif mask.dtype != torch.int32 or mask.device != dev or mask.dim() != 2 or \
-            mask.shape[0] != total_q or mask.shape[1] < words or \
-            (mask.shape[1] > 1 and mask.stride(1) != 1) or \
-            (total_q > 1 and mask.stride(0) < mask.shape[1]):
+        mask = _new((total_q, need), i32, dev, stream)
+    rows, words = mask.shape if mask.dim() == 2 else (-1, 0)
+    step, inner = mask.stride() if rows >= 0 else (0, 0)
+    if mask.dtype != i32 or mask.device != dev or rows != total_q or words < need or \
+            (words > 1 and inner != 1) or (rows > 1 and step < words):
         raise ValueError("mask must be int32 [total_q, words], 32 words >= max_seqlen_q, on "
                          "parents' device")
     if positions is None:
-        positions = _new((total_q,), torch.int32, dev, stream)
-    else:
-        _ints("positions", positions, dev)
-        if tuple(positions.shape) != (total_q,):
-            raise ValueError("positions must be int32 [total_q]")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        positions = _new((total_q,), i32, dev, stream)
+    # (the handle of the current stream without the object: that costs 3 us)
+    handle = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None \
+        else stream.cuda_stream
     call = _lib.UaTree(parents.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens_k.data_ptr(),
-                       mask.data_ptr(), positions.data_ptr(), max(mask.stride(0), mask.shape[1]),
-                       num_seqs, total_q, int(max_seqlen_q), mask.shape[1])
+                       mask.data_ptr(), positions.data_ptr(), max(step, words), num_seqs, total_q,
+                       int(max_seqlen_q), words)
     if torch.cuda.current_device() == dev.index:
-        rc = lib.ua_tree_mask(ctypes.byref(call), stream.cuda_stream)
+        rc = lib.ua_tree_mask(ctypes.byref(call), handle)
     else:
         with torch.cuda.device(dev):
-            rc = lib.ua_tree_mask(ctypes.byref(call), stream.cuda_stream)
+            rc = lib.ua_tree_mask(ctypes.byref(call), handle)
     if rc != 0:
         raise UaError(rc, "ua_tree_mask")
     return mask, positions
