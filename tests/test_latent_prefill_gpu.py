@@ -38,7 +38,7 @@ def run(t, **kw):
         else:
             d.append(x.cuda())
     n = [int((c[1:] - c[:-1]).max()) if c.numel() > 1 else 0 for c in (t[4], t[5])]
-    return ua.latent_prefill(*d, max_seqlen_q=n[0], max_seqlen_k=n[1], **kw)
+    return ua.latent_prefill(*d, **{**dict(max_seqlen_q=n[0], max_seqlen_k=n[1]), **kw})
 
 
 def compare(t, scale=None, out_dtype=None, **kw):
@@ -66,6 +66,17 @@ def test_prefill(lens, h, nope, rope, value, dtype):
     t = make(lens, h, nope, rope, value, dtype, pad_q=3, pad_k=5)
     compare(t)
     compare(t, out_dtype=F32, scale=0.2)
+
+
+@pytest.mark.parametrize("lens,h,nope,rope,value,dtype", CASES + [
+    ([(256, 900), (77, 129)], 20, 128, 64, 128, BF), ([(100, 1500)], 40, 64, 64, 64, F16),
+    ([(64, 3000)], 16, 128, 64, 128, BF),
+])
+def test_prefill_by_parts(lens, h, nope, rope, value, dtype):
+    """A bound of the key lengths that has a few CTAs share every q-block's keys, some with none."""
+    t = make(lens, h, nope, rope, value, dtype, pad_q=3, pad_k=5)
+    compare(t, max_seqlen_k=1 << 20)
+    compare(t, out_dtype=F32, scale=0.2, max_seqlen_k=1 << 20)
 
 
 def test_steep_scores():

@@ -49,6 +49,8 @@ struct LatentParams {
 // One launch of the expanded form's kernel: maps of q [total_q][heads][N + R], k_nope
 // [total_k][heads][N] and v [total_k][heads][V] (boxes of 64 elements x one head x 128 tokens) and
 // of k_rope [total_k][R] (64 elements x 128 tokens; elements past R read as zero).
+constexpr int kLatentParts = 4;
+
 struct LatentPrefillParams {
   CUtensorMap q, k, k_rope, v;
   void* out;                    // [total_q, heads, V]
@@ -57,6 +59,7 @@ struct LatentPrefillParams {
   const int32_t* cu_seqlens_k;
   unsigned int* status;
   int num_seqs, total_q, total_k, heads, rope_dim, out_dtype, slots;
+  int parts;                    // CTAs (a cluster) that share a q-block's keys: 1 .. kLatentParts
   int by_length;                // 1: q-blocks start by the length of their walks (at most 64 slots)
   float scale;
 };

@@ -29,6 +29,23 @@ bool head_map(CUtensorMap* map, const void* base, bool bf16, int tokens, int hea
   return ua::encode_half_map(map, base, bf16, 3, dims, strides, box);
 }
 
+// CTAs (a cluster) that share a q-block's keys: 2 or 4, if all q-blocks still start at once and the
+// longest walk becomes shorter by four key tiles of 128 or more, which is what joining the parts
+// costs.  In us, 4 | 2 | 1 CTAs a q-block of 256 tokens, 16 heads unless said: 64 tokens behind 3,936
+// 19.1 | 31.4 | 54.4; 256 behind 7,744 37.7 | 66.8 | 115.3; 1,000 of 8 heads 13.7 | 18.1 | 20.4; 1,000
+// (256 CTAs if of four) 25.0 | 18.3 | 20.6; 600 (5 key tiles) - | 15.1 | 13.4; 2,000 (256 CTAs if of
+// two) - | 37.4 | 34.3.  Parts of eight were slower than of four wherever they fitted.
+int parts(const ua_latent_prefill_t& a, long long slots, int sms) {
+  const long long blocks =
+      std::min(slots, static_cast<long long>(a.num_seqs) *
+                          ((static_cast<long long>(a.max_seqlen_q) + kBlockTokens - 1) / kBlockTokens)) *
+      a.num_heads;
+  const int tiles = static_cast<int>((static_cast<long long>(a.max_seqlen_k) + 127) / 128);
+  for (int n = ua::kLatentParts; n > 1; n /= 2)
+    if (blocks * n <= (n > 2 ? sms * 7 / 8 : sms) && tiles - (tiles + n - 1) / n >= 4) return n;
+  return 1;
+}
+
 int prefill(const ua_latent_prefill_t& a, cudaStream_t st) {
   if (a.num_seqs < 0 || a.total_q < 0 || a.total_k < 0 || a.max_seqlen_q < 0 || a.max_seqlen_k < 0 ||
       a.num_heads < 1)
@@ -86,6 +103,7 @@ int prefill(const ua_latent_prefill_t& a, cudaStream_t st) {
   p.out_dtype = a.out_dtype;
   p.slots = static_cast<int>(slots);
   p.scale = a.scale;
+  p.parts = parts(a, slots, sms);
   // (where all start at once, or all are short, the order is nothing: it costs 500 cycles)
   p.by_length = slots <= 64 && slots * a.num_heads > sms && a.max_seqlen_k > 2 * kBlockTokens;
   const auto launch =

@@ -44,6 +44,9 @@ struct LatentPrefillCfg {
   static_assert(N % 64 == 0 && (V == 64 || V == 128) && kNQ * kTmemStride <= kTmemCols);
   static_assert(kRing >= kPer + kVB && kSmemBytes + 16 <= 227 * 1024);
   static_assert(8 * (9 + 4 * kTiles) + 4 <= kBarBytes);
+  // a part's rows and their statistics, where Q and the ring were
+  static constexpr int kPartBytes = kNQ * kBM * 4 * (V + 2);
+  static_assert(kPartBytes <= kNQ * kQBytes + kRing * kBlk);
 };
 
 // The sequence owning slot x of q-blocks of tb tokens, by one warp: the last b with
@@ -112,7 +115,66 @@ __device__ __forceinline__ int latent_slot_by_length(const int32_t* __restrict__
   return a != 0u ? __ffs(a) - 1 : b != 0u ? __ffs(b) + 31 : y;
 }
 
-template <int N, int V, bool BF16>
+// Where a part keeps the 16-byte chunk c of its row r (a thread writes a row, a warp reads one).
+template <int V>
+__device__ __forceinline__ int latent_part_at(int r, int c) {
+  return r * V * 4 + ((c ^ r) & (V / 4 - 1)) * 16;
+}
+
+// The rows of a q-block from the parts in the cluster's shared memory, whole rows a warp.
+template <int V>
+__device__ __forceinline__ void latent_prefill_join(const LatentPrefillParams& p, uint32_t rows_at,
+                                                    uint32_t stats_at, int rows, int parts,
+                                                    size_t token0, int h, int warp, int warps) {
+  constexpr int kChunks = V / 4, kRows = 32 / kChunks;  // chunks of a row, rows of a warp at a time
+  constexpr int kStat = LatentPrefillCfg<64, V>::kNQ * LatentPrefillCfg<64, V>::kBM * 4;
+  const int lane = threadIdx.x & 31, c = lane % kChunks;
+#pragma unroll 1
+  for (int r = warp * kRows + lane / kChunks; r < rows; r += warps * kRows) {
+    float m[kLatentParts], l[kLatentParts];
+    float4 v[kLatentParts];
+#pragma unroll
+    for (int k = 0; k < kLatentParts; ++k) {
+      m[k] = -INFINITY;
+      l[k] = 0.f;
+      if (k < parts) {
+        const uint32_t at = cluster_map(stats_at + 4 * r, k);
+        m[k] = ld_cluster_f32(at);
+        l[k] = ld_cluster_f32(at + kStat);
+        v[k] = ld_cluster_f32x4(cluster_map(rows_at + latent_part_at<V>(r, c), k));
+      }
+    }
+    float M = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kLatentParts; ++k) M = fmaxf(M, m[k]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kLatentParts; ++k) {
+      if (k >= parts || l[k] == 0.f) continue;  // (its row may not have been written)
+      const float f = fast_exp2(m[k] - M);
+      sum += l[k] * f;
+      o.x += v[k].x * f;
+      o.y += v[k].y * f;
+      o.z += v[k].z * f;
+      o.w += v[k].w * f;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const size_t row = (token0 + r) * p.heads + h, at = row * V + 4 * c;
+    if (p.out_dtype == UA_DT_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
+          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    } else {
+      const bool bf = p.out_dtype == UA_DT_BF16;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+          make_uint2(bf ? pack_bf16(o.x * inv, o.y * inv) : pack_f16(o.x * inv, o.y * inv),
+                     bf ? pack_bf16(o.z * inv, o.w * inv) : pack_f16(o.z * inv, o.w * inv));
+    }
+    if (p.lse != nullptr && c == 0)
+      p.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+  }
+}
+
+template <int N, int V, bool BF16, bool SPLIT>
 __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
     ua_latent_prefill_kernel(const __grid_constant__ LatentPrefillParams p) {
   using C = LatentPrefillCfg<N, V>;
@@ -196,7 +258,11 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
     const int last = ctx + min(t_first + (qt + 1) * BM, q_end);  // one past it
     return (max(0, min(last, k_len)) + BN - 1) / BN;
   };
-  const int n0 = tiles(0), n1 = tiles(1);
+  // SPLIT: the CTA's part of them, from tile j0 on
+  const int all = max(tiles(0), tiles(1));
+  const int per = SPLIT ? (all + static_cast<int>(gridDim.z) - 1) / static_cast<int>(gridDim.z) : all;
+  const int j0 = SPLIT ? static_cast<int>(blockIdx.z) * per : 0;
+  const int n0 = max(0, min(tiles(0) - j0, per)), n1 = max(0, min(tiles(1) - j0, per));
   // the barriers of tile j's keys (v 0) or values (1), and their phase
   auto bar_of = [&](int j, int v) { return 2 * (j % C::kTiles) + v; };
   auto phase_of = [&](int j) { return (j / C::kTiles) & 1; };
@@ -222,7 +288,7 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
       if (lane == 0) {
         uint8_t* const dst = ring + issued % RING * C::kBlk;
         uint64_t* const bar = &full[bar_of(j, e >= C::kCB)];
-        const int row = sq.k0 + j * BN;
+        const int row = sq.k0 + (j0 + j) * BN;
         mbar_arrive_expect_tx(bar, C::kBlk);
         if (e < N / 64) tma_load_3d_pf(dst, &p.k, 64 * e, h, row, bar);
         else if (e == N / 64) tma_load_2d(dst, &p.k_rope, 0, row, bar);
@@ -335,7 +401,7 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
 #pragma unroll
       for (int g = 0; g < 4; ++g) tmem_ld32(tS + 32 * g, s[g]);
       tmem_ld_wait();
-      const int k0 = n * BN;
+      const int k0 = (j0 + n) * BN;
       if (k0 + BN > clear) {
         const int last = see - k0;
 #pragma unroll
@@ -413,8 +479,29 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
       if (lane == 0) mbar_arrive(&p_full[qt]);
     }
     if (ok && n_tiles > 0) ok = pf_wait_warp(&pv_done[qt], 0, abort_flag, p.status);
+    if constexpr (SPLIT) {
+      // (Q and the ring are free when the other q tile's products are done too)
+      if (ok && (qt == 0 ? n1 : n0) > 0) ok = pf_wait_warp(&pv_done[qt ^ 1], 0, abort_flag, p.status);
+      tc_fence_after();
+      const int r = qt * BM + 32 * quad + lane;
+      float* const stats = reinterpret_cast<float*>(sQ + NQ * BM * V * 4);
+      stats[r] = m;
+      stats[NQ * BM + r] = ok ? l : NAN;  // (after a wait that gave up the rows are NaN)
+      if (ok && n_tiles > 0) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < V; c0 += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + c0, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(sQ + latent_part_at<V>(r, c0 / 4 + e)) =
+                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+    }
     tc_fence_after();
-    if (ok && qt < nq) {
+    if (!SPLIT && ok && qt < nq) {
       const float inv = l == 0.f ? 0.f : 1.f / l;  // (a row that saw no key is 0; NaN stays)
       const size_t row = (static_cast<size_t>(sq.q0) + i_q) * p.heads + h;
       if (rv && p.lse != nullptr)
@@ -457,12 +544,21 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == kMma) tmem_dealloc(tmem, C::kTmemCols);
+  if constexpr (SPLIT) {
+    cluster_sync();  // every part's rows, maxima and sums are in its shared memory
+    const int parts = static_cast<int>(gridDim.z);
+    latent_prefill_join<V>(p, smem_addr(sQ), smem_addr(sQ) + NQ * BM * V * 4, min(TB, q_end - t_first),
+                           parts, static_cast<size_t>(sq.q0) + t_first, h,
+                           static_cast<int>(blockIdx.z) * (C::kThreads / 32) + warp,
+                           parts * (C::kThreads / 32));
+    cluster_sync_relaxed();  // no CTA leaves while another reads its shared memory
+  }
 }
 
-template <int N, int V, bool BF16>
+template <int N, int V, bool BF16, bool SPLIT>
 cudaError_t launch_latent_prefill_t(const LatentPrefillParams& p, cudaStream_t stream) {
   using C = LatentPrefillCfg<N, V>;
-  auto kern = ua_latent_prefill_kernel<N, V, BF16>;
+  auto kern = ua_latent_prefill_kernel<N, V, BF16, SPLIT>;
   static std::atomic<unsigned long long> configured{0};  // one bit per device
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -473,8 +569,18 @@ cudaError_t launch_latent_prefill_t(const LatentPrefillParams& p, cudaStream_t s
     if (err != cudaSuccess) return err;
     configured.fetch_or(bit);
   }
-  const dim3 grid(static_cast<unsigned>(p.heads), static_cast<unsigned>(p.slots));
-  return launch_pdl(kern, grid, dim3(C::kThreads), C::kSmemBytes, stream, 1, p);
+  const dim3 grid(static_cast<unsigned>(p.heads), static_cast<unsigned>(p.slots),
+                  static_cast<unsigned>(p.parts));
+  return launch_pdl_cluster(kern, grid, dim3(C::kThreads), C::kSmemBytes, stream, 1, p.parts, p);
+}
+
+template <int N, int V>
+cudaError_t launch_latent_prefill_any(const LatentPrefillParams& p, bool bf16, cudaStream_t s) {
+  if (p.parts > 1)
+    return bf16 ? launch_latent_prefill_t<N, V, true, true>(p, s)
+                : launch_latent_prefill_t<N, V, false, true>(p, s);
+  return bf16 ? launch_latent_prefill_t<N, V, true, false>(p, s)
+              : launch_latent_prefill_t<N, V, false, false>(p, s);
 }
 
 }  // namespace ua

@@ -6,11 +6,8 @@ namespace ua {
 
 cudaError_t launch_latent_prefill_n64(const LatentPrefillParams& p, int value, bool bf16,
                                      cudaStream_t s) {
-  if (value == 64)
-    return bf16 ? launch_latent_prefill_t<64, 64, true>(p, s)
-                : launch_latent_prefill_t<64, 64, false>(p, s);
-  return bf16 ? launch_latent_prefill_t<64, 128, true>(p, s)
-              : launch_latent_prefill_t<64, 128, false>(p, s);
+  return value == 64 ? launch_latent_prefill_any<64, 64>(p, bf16, s)
+                     : launch_latent_prefill_any<64, 128>(p, bf16, s);
 }
 
 }  // namespace ua
