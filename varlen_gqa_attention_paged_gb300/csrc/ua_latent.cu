@@ -221,7 +221,7 @@ void shape(const ua_latent_t& a, int sms, int* workers, int* cl, int* spread) {
   *cl = static_cast<long long>(a.max_seqlen_q) * a.num_heads > ua::kLatRows ? 2 : 1;
   const long long rows = static_cast<long long>(a.total_q) * a.num_heads;
   const long long tiles = rows / (ua::kLatRows * *cl) + a.num_seqs;
-  const long long keys = (std::max(a.max_seqlen_k, 1) + ua::kLatKeys - 1) / ua::kLatKeys;
+  const long long keys = (std::max<long long>(a.max_seqlen_k, 1) + ua::kLatKeys - 1) / ua::kLatKeys;
   const long long most = std::max(1, sms / *cl);
   *workers = static_cast<int>(
       std::max(1LL, std::min(most, (tiles * keys + kMinShare - 1) / kMinShare)));
