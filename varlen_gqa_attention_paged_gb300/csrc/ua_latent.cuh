@@ -99,12 +99,22 @@ struct LatentWalk {
     q0 = q_len = kv_len = rows = rt = kt = 0;
     for (int base = 0; base < p.num_seqs; base += 32) {
       const int i = base + lane;
-      const int first = i < p.num_seqs ? __ldg(p.cu_seqlens_q + i) * p.heads / kLatRows + i : x + 1;
-      const unsigned m = __ballot_sync(0xffffffffu, first <= x);
-      if (m != 0u) b = base + 31 - __clz(m);
+      const bool in = i < p.num_seqs;
+      const int c0 = in ? __ldg(p.cu_seqlens_q + i) : 0, c1 = in ? __ldg(p.cu_seqlens_q + i + 1) : 0;
+      const int len = in ? __ldg(p.seq_lens_k + i) : 0;  // (all in one round of loads)
+      const unsigned m = __ballot_sync(0xffffffffu, in && c0 * p.heads / kLatRows + i <= x);
+      if (m != 0u) {
+        const int src = 31 - __clz(m);
+        b = base + src;
+        q0 = __shfl_sync(0xffffffffu, c0, src);
+        q_len = __shfl_sync(0xffffffffu, c1, src) - q0;
+        kv_len = max(0, __shfl_sync(0xffffffffu, len, src));
+      }
       if (m != 0xffffffffu) break;
     }
-    load(p);
+    rows = rows_of(p, q0, q0 + q_len);
+    rt = row_tiles(p, rows);
+    kt = key_tiles(kv_len);
     t = x - (q0 * p.heads / kLatRows + b);
     if (t < 0 || t >= rt) {
       rows = 0;
@@ -491,7 +501,8 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
         if (n == 0 && nb <= 32) rows_b = row_of(1, second);
         // With two tiles in shared memory the copy of one waits for the products of the one before:
         // the next but one comes as far as L2 meanwhile.
-        if (n + 2 < s.nt) {
+        // (Four tiles are far enough ahead by themselves.)
+        if (S < 4 && n + 2 < s.nt) {
           const unsigned box2 = static_cast<unsigned>(n + 2) << sh;
           const int batch = static_cast<int>(box2 >> 5);
           const int ahead = __shfl_sync(0xffffffffu, batch == c ? rows_a : rows_b, (box2 + lane) & 31);
