@@ -4,7 +4,9 @@
 //   mask_i = bit i | mask_parent(i),   depth_i = depth_parent(i) + 1,   position = context + depth.
 // One thread a token and word of its mask walks up the parents, which a block keeps in shared
 // memory; parents lie before their children, so a walk ends after at most i steps.  A batch of 8
-// trees of 60 tokens is bound by the launch and one walk's chain.
+// trees of 60 tokens is bound by the launch and one walk's chain (4.7 us alone and cold; 1.2 us of a
+// step with its attention), one deep tree of 1000 tokens by the walks (37 us; a thread a token that
+// writes all its words in one walk took 43, its stores diverging).
 #include <climits>
 
 #include "ua_device.cuh"
