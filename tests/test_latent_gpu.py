@@ -102,8 +102,10 @@ def test_attention_by_even_shares(lens, h, latent, rope, bs, dtype):
 ])
 @pytest.mark.parametrize("masked", [False, True])
 def test_attention_by_parts(lens, h, latent, masked):
-    t = make(lens, h, latent, bs=16)
-    mask = masks(lens) if masked else None
+    t = make(lens, h, latent, bs=16, pad=7)
+    mask = None
+    if masked:
+        mask = torch.nn.functional.pad(masks(lens), (0, 0, 0, 7), value=-1)
     q, cache, cu, sl, bt = (x.cuda() for x in t)
     for far, whole in ((None, True), (FAR, False)):
         size = sizes(t[2], t[3])
@@ -111,8 +113,10 @@ def test_attention_by_parts(lens, h, latent, masked):
             q, cache, cu, sl, bt, scale=0.08, max_seqlen_q=size["max_seqlen_q"],
             max_seqlen_k=far or size["max_seqlen_k"])
         assert (ua.latent_workspace_bytes(step) == 0) == whole
-    compare(t, mask=mask)
     compare(t, mask=mask, out_dtype=F32)
+    out = torch.full((q.shape[0], h, latent), 7.0, dtype=BF, device="cuda")
+    compare(t, mask=mask, out=out)
+    assert torch.all(out[-7:] == 7)     # rows behind the last sequence
 
 
 def masks(lens, seed=0):

@@ -77,6 +77,9 @@ def test_prefill_by_parts(lens, h, nope, rope, value, dtype):
     t = make(lens, h, nope, rope, value, dtype, pad_q=3, pad_k=5)
     compare(t, max_seqlen_k=(1 << 31) - 1)
     compare(t, out_dtype=F32, scale=0.2, max_seqlen_k=(1 << 31) - 1)
+    out = torch.full((t[0].shape[0], h, value), 7.0, dtype=dtype, device="cuda")
+    compare(t, out=out, max_seqlen_k=(1 << 31) - 1)
+    assert torch.all(out[-3:] == 7)
 
 
 def test_steep_scores():
