@@ -144,7 +144,10 @@ def test_results_are_the_same_every_time():
 
 
 def captured(run):
-    stream = torch.cuda.Stream(priority=-1)
+    return captured_on(torch.cuda.Stream(priority=-1), run)
+
+
+def captured_on(stream, run):
     with torch.cuda.stream(stream):
         run(stream)
         graph = torch.cuda.CUDAGraph()
@@ -179,8 +182,14 @@ def test_a_captured_step_follows_the_lengths():
     assert ua.device_status() == 0
 
 
-def test_two_graphs_of_one_stream_run_side_by_side():
-    steps = [step_of([(1, 6000), (1, 3000)], seed=s) for s in (0, 10)]
+BOTH = pytest.mark.parametrize("lens", [    # even shares with scratch; a cluster a row tile
+    [(1, 6000), (2, 3000)], [(1, 700), (2, 300), (1, 64)]])
+
+
+@BOTH
+def test_two_graphs_of_one_stream_run_side_by_side(lens):
+    steps = [step_of(lens, seed=s) for s in (0, 10)]
+    assert (ua.latent_workspace_bytes(steps[0][0]) == 0) == (lens[0][1] == 700)
     want = [s[0]().clone() for s in steps]
     stream = torch.cuda.Stream(priority=-1)
     graphs = []
@@ -204,8 +213,9 @@ def test_two_graphs_of_one_stream_run_side_by_side():
         assert torch.equal(s._last("out"), w)
 
 
-def test_two_streams_at_once():
-    steps = [step_of([(1, 6000), (2, 3000)], seed=s) for s in (0, 10)]
+@BOTH
+def test_two_streams_at_once(lens):
+    steps = [step_of(lens, seed=s) for s in (0, 10)]
     want = [s[0]().clone() for s in steps]
     sides = [torch.cuda.Stream(priority=-1), torch.cuda.Stream(priority=-1)]
     torch.cuda.synchronize()
@@ -215,6 +225,33 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for (s, _), w in zip(steps, want):
         assert torch.equal(s._last("out"), w)
+
+
+@pytest.mark.parametrize("q_len,k_len,h", [(64, 2000, 16), (700, 700, 8), (900, 900, 40)])
+def test_captured_prefills_on_two_streams(q_len, k_len, h):
+    """Four CTAs a q-block's keys, two or four, and one; both graphs at once, again and again."""
+    cu = torch.tensor([0, q_len], dtype=torch.int32, device="cuda")
+    cu_k = torch.tensor([0, k_len], dtype=torch.int32, device="cuda")
+    sides, calls = [torch.cuda.Stream(priority=-1) for _ in range(2)], []
+    for seed, side in enumerate(sides):
+        q, kv = rand(q_len, h, N + R, seed=seed), rand(k_len, h, N + V, seed=seed + 5)
+        args = (q, kv[..., :N], rand(k_len, R, seed=seed + 9), kv[..., N:], cu, cu_k)
+        out = torch.zeros((q_len, h, V), dtype=BF, device="cuda")
+        calls.append((args, out, captured_on(side, lambda s: ua.latent_prefill(
+            *args, max_seqlen_q=q_len, max_seqlen_k=k_len, out=out, stream=s))))
+    torch.cuda.synchronize()
+    for _, out, _ in calls:
+        out.zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for (_, _, graph), side in zip(calls, sides):
+            with torch.cuda.stream(side):
+                graph.replay()
+    torch.cuda.synchronize()
+    for args, out, _ in calls:
+        want, _, tol, _ = ref.prefill(*(x.cpu() for x in args), (N + R) ** -0.5)
+        ref.check(out, want, tol, BF)
+    assert ua.device_status() == 0
 
 
 def test_a_workspace_of_the_caller():
