@@ -71,6 +71,8 @@ CASES = [
     ([(130, 260)], 2, 512, 64, 128, F16),
     ([(1, 4000), (1, 10), (1, 2500), (1, 1)], 16, 512, 64, 64, BF),
     ([(1, 37)] * 70, 16, 512, 64, 16, BF),
+    ([(1, 9000)], 16, 512, 64, 64, BF), ([(2, 6000), (1, 40), (1, 5000)], 20, 256, 32, 32, F16),
+    ([(1, 8000)], 128, 512, 64, 64, BF), ([(3, 7000)], 9, 128, 64, 16, BF),
 ]
 
 

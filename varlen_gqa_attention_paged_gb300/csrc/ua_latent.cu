@@ -11,13 +11,26 @@
 
 namespace ua {
 
+// Four neighbouring elements of the output.
+__device__ __forceinline__ void store_four(void* out, size_t at, float4 v, int dtype) {
+  if (dtype == UA_DT_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
+  } else {
+    const bool bf = dtype == UA_DT_BF16;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
+        make_uint2(bf ? pack_bf16(v.x, v.y) : pack_f16(v.x, v.y),
+                   bf ? pack_bf16(v.z, v.w) : pack_f16(v.z, v.w));
+  }
+}
+
 // One output row from its partial rows: with m_k, l_k and acc_k of part k
 //   M = max m_k,  L = sum l_k 2^(m_k - M),  out = sum acc_k 2^(m_k - M) / L
 // Blocks (x, y) share the rows of the tile that CTA x began: two warps a row, half of its elements
-// each, or, with many parts of few rows (one long sequence: 152 parts of 2 KB a row), a block a
-// row, an eighth of the parts a warp, joined in shared memory (16 heads over 16000 keys: 20.5 us a
-// call, 41 with a warp a row).  Sums run in a fixed order.
+// each, or, with many parts of few rows (152 parts of 2 KB a row), a block a row, an eighth of the parts
+// a warp, joined in shared memory.  About 3.5 us of a call of 64 sequences of up to 8191 keys, latency
+// of its loads.  Sums run in a fixed order.
 constexpr int kMergeMany = 16;
+constexpr int kMergeFewBlocks = 1024;
 
 template <int L>
 __global__ void __launch_bounds__(256) ua_latent_merge_kernel(
@@ -39,15 +52,7 @@ __global__ void __launch_bounds__(256) ua_latent_merge_kernel(
     return static_cast<size_t>(slot) * kLatRows + r;
   };
   auto store = [&](int r, int v4, float4 v) {
-    const size_t e = (static_cast<size_t>(meta.x) + r) * L + 4 * v4;
-    if (p.out_dtype == UA_DT_F32) {
-      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + e) = v;
-    } else {
-      const bool bf = p.out_dtype == UA_DT_BF16;
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + e) =
-          make_uint2(bf ? pack_bf16(v.x, v.y) : pack_f16(v.x, v.y),
-                     bf ? pack_bf16(v.z, v.w) : pack_f16(v.z, v.w));
-    }
+    store_four(p.out, (static_cast<size_t>(meta.x) + r) * L + 4 * v4, v, p.out_dtype);
   };
   // max over the row's parts; the lane's first part with it
   auto top_of = [&](int r, float& m0, float& l0) -> float {
@@ -166,10 +171,102 @@ __global__ void __launch_bounds__(256) ua_latent_merge_kernel(
   }
 }
 
+// The same for few row tiles of many parts (one long sequence): x counts the tiles that have parts, a
+// block takes 128 elements of a row, an eighth of the parts a warp, joined in shared memory.  (A kernel
+// of its own: in the one above its code cost every other call 0.5 us.)
+template <int L>
+__global__ void __launch_bounds__(256) ua_latent_merge_few_kernel(
+    const __grid_constant__ LatentMergeParams p) {
+  constexpr int kPieces = L / 128;
+  __shared__ float4 s_acc[8][32];
+  __shared__ float s_sum[8];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int cta = -1, seen = 0;  // the CTA that began the tile
+#pragma unroll 4
+  for (int base = 0; base < p.ctas; base += 32) {
+    const bool begun = base + lane < p.ctas && p.ws_meta[base + lane].z > 0;
+    const unsigned m = __ballot_sync(0xffffffffu, begun);
+    const unsigned mine = __ballot_sync(
+        0xffffffffu,
+        begun && seen + __popc(m & ((1u << lane) - 1u)) == static_cast<int>(blockIdx.x));
+    if (mine != 0u) cta = base + __ffs(mine) - 1;
+    seen += __popc(m);
+  }
+  if (cta < 0) return;
+  const int4 meta = p.ws_meta[cta];
+  const int parts = min(meta.z, p.ctas / p.cl - cta / p.cl);
+  const int rows = static_cast<int>(
+      min(static_cast<long long>(min(meta.y, kLatRows)), p.rows - meta.x));
+  if (parts <= 0 || meta.x < 0) return;
+  for (int e = blockIdx.y; e < rows * kPieces; e += gridDim.y) {
+    const int r = e / kPieces, v4 = e % kPieces * 32 + lane;
+    auto at = [&](int k) -> size_t {  // part k of the row
+      const int slot = k == 0 ? 2 * cta + 1 : 2 * (cta + k * p.cl);
+      return static_cast<size_t>(slot) * kLatRows + r;
+    };
+    float M = -INFINITY;
+    for (int k = lane; k < parts; k += 32) M = fmaxf(M, p.ws_m[at(k)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int k0 = warp; k0 < parts; k0 += 64) {
+      float l[8], m[8];
+      float4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {  // eight parts' loads in flight
+        const int k = min(k0 + 8 * u, parts - 1);
+        l[u] = p.ws_l[at(k)];
+        m[u] = p.ws_m[at(k)];
+        v[u] = reinterpret_cast<const float4*>(p.ws_acc + at(k) * L)[v4];
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        // (a part that saw no key has no elements)
+        if (k0 + 8 * u >= parts || l[u] == 0.f) continue;
+        const float f = fast_exp2(m[u] - M);
+        sum += l[u] * f;
+        acc.x += v[u].x * f;
+        acc.y += v[u].y * f;
+        acc.z += v[u].z * f;
+        acc.w += v[u].w * f;
+      }
+    }
+    s_acc[warp][lane] = acc;
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      sum = 0.f;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float4 v = s_acc[w][lane];
+        sum += s_sum[w];
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      store_four(p.out, (static_cast<size_t>(meta.x) + r) * L + 4 * v4,
+                 make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv), p.out_dtype);
+      if (p.lse != nullptr && lane == 0 && e % kPieces == 0)
+        p.lse[meta.x + r] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+    }
+    __syncthreads();
+  }
+}
+
 cudaError_t launch_latent_merge(const LatentMergeParams& p, int latent, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(p.ctas), static_cast<unsigned>(p.grid_rows));
-  const auto kern = latent == 512   ? ua_latent_merge_kernel<512>
-                    : latent == 256 ? ua_latent_merge_kernel<256>
+  const dim3 grid(static_cast<unsigned>(p.few ? p.few : p.ctas),
+                  static_cast<unsigned>(p.grid_rows));
+  const auto kern = latent == 512   ? p.few ? ua_latent_merge_few_kernel<512>
+                                            : ua_latent_merge_kernel<512>
+                    : latent == 256 ? p.few ? ua_latent_merge_few_kernel<256>
+                                            : ua_latent_merge_kernel<256>
+                    : p.few         ? ua_latent_merge_few_kernel<128>
                                     : ua_latent_merge_kernel<128>;
   return launch_pdl(kern, grid, dim3(256), 0, s, 1, p);
 }
@@ -334,9 +431,19 @@ int attend(const ua_latent_t& a, cudaStream_t st) {
   m.ctas = ctas;
   m.cl = p.cl;
   m.out_dtype = a.out_dtype;
-  // blocks of a tile: one for each row, sixteen at most (they walk the others)
-  m.grid_rows = static_cast<int>(std::max(
-      1LL, std::min(16LL, static_cast<long long>(a.max_seqlen_q) * a.num_heads)));
+  const long long rows = std::max(
+      1LL, std::min<long long>(ua::kLatRows, static_cast<long long>(a.max_seqlen_q) * a.num_heads));
+  // (pairs of) row tiles at most; few of them, of many parts: in us, against the other kernel: 16 heads,
+  // one sequence of 2500 keys 12.9 : 13.5, 16000 17.3 : 21.6, 128000 44.2 : 47.1, 4 of 8000 (30 parts)
+  // 21.0 : 22.2, 12 of 8000 (10 parts) 36.4 : 33.7; 128 heads, one of 16000 23.4 : 29.4, 4 of 5000
+  // (4096 blocks) 39.4 : 28.2
+  const long long begun = m.rows / (ua::kLatRows * p.cl) + a.num_seqs;
+  const long long pieces = rows * (a.latent_dim / 128);
+  if (begun * ua::kMergeMany <= p.workers && p.cl * begun * pieces <= ua::kMergeFewBlocks)
+    m.few = static_cast<int>(p.cl * begun);
+  // blocks of a tile: one for each 128 elements; or one for each row, sixteen at most (they walk the
+  // others)
+  m.grid_rows = static_cast<int>(m.few ? pieces : std::min(16LL, rows));
   return ua::launch_latent_merge(m, a.latent_dim, st) == cudaSuccess ? UA_OK : UA_ERR_CUDA;
 }
 

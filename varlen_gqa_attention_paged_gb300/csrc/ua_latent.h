@@ -73,6 +73,7 @@ struct LatentMergeParams {
   const int4* ws_meta;
   long long rows;               // total_q * heads
   int ctas, cl, out_dtype, grid_rows;
+  int few;                      // > 0: row tiles at most, which the grid's x counts
 };
 
 cudaError_t launch_latent_l128(const LatentParams& p, bool bf16, cudaStream_t s);
