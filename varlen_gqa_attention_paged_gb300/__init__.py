@@ -202,8 +202,9 @@ class PreparedAttention:
     Built by :func:`prepare`.  Calling it passes new per-step tensors -- ``q``,
     ``cu_seqlens_q``, ``seq_lens_k``, ``block_table``, ``out`` -- each of the prepared one's
     shape, dtype and device (checked; if one is refused, none is taken); any left out, and
-    ``stream``, keeps what was passed last.  The caches, the score features, the scales and the
-    host sizes (``max_seqlen_q``/``max_seqlen_k``) stay as prepared.  Returns ``out``.
+    ``stream``, keeps what was passed last (no stream yet: the one that was current when the call
+    was prepared).  The caches, the score features, the scales and the host sizes
+    (``max_seqlen_q``/``max_seqlen_k``) stay as prepared.  Returns ``out``.
     """
 
     def __init__(self, lib, call, tensors, stream):
@@ -430,8 +431,9 @@ class PreparedAppend:
     Built by :func:`prepare_append`.  Calling it passes the step's tensors -- ``k``, ``v``,
     ``q``, ``q_out``, ``cu_seqlens_q``, ``seq_lens_k``, ``block_table``, ``positions`` -- each
     of the prepared one's shape, strides, dtype and device (checked; if one is refused, none is
-    taken); any left out, and ``stream``, keeps what was passed last.  The caches, the table and
-    the scales stay as prepared.  Returns ``q_out``.
+    taken); any left out, and ``stream``, keeps what was passed last (no stream yet: the one that
+    was current when the call was prepared).  The caches, the table and the scales stay as
+    prepared.  Returns ``q_out``.
     """
 
     def __init__(self, lib, call, keep, static, stream):

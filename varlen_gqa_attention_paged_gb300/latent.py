@@ -63,9 +63,15 @@ def _out(out, shape, like, out_dtype, stream):
     return out
 
 
+def _handle(stream, index):
+    """The handle of a stream, or of the device's current one (whose object costs 3 us)."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
 class _Prepared:
     """A call with its checks made and its sizes marshalled once; its steps pass new tensors of
-    the prepared ones' shapes, strides, dtypes and device."""
+    the prepared ones' shapes, strides, dtypes and device.  As long as no stream was passed, a step
+    goes to the stream that is current when it is made."""
 
     def __init__(self, what, call, tensors, static, stream):
         self._what = what
@@ -81,7 +87,7 @@ class _Prepared:
         dev = next(t.device for t in tensors.values() if t is not None)
         self._device = dev.index
         self._one_device = torch.cuda.device_count() == 1
-        self._stream = stream if stream is not None else torch.cuda.current_stream(dev)
+        self._stream = stream   # passed last, if one was
 
     def _step(self, passed, stream):
         now = self._now
@@ -107,11 +113,12 @@ class _Prepared:
                     setattr(self._call, name, ptr)
         if stream is not None:
             self._stream = stream
+        handle = _handle(self._stream, self._device)
         if self._one_device or torch.cuda.current_device() == self._device:
-            rc = self._entry(self._ref, self._stream.cuda_stream)
+            rc = self._entry(self._ref, handle)
         else:
             with torch.cuda.device(self._device):
-                rc = self._entry(self._ref, self._stream.cuda_stream)
+                rc = self._entry(self._ref, handle)
         if rc != 0:
             raise UaError(rc, self._what)
 
@@ -124,8 +131,8 @@ class _Prepared:
 class PreparedAppendLatent(_Prepared):
     """``append_latent`` for a loop with fixed shapes, built by :func:`prepare_append_latent`.
     Calling it passes the step's tensors (checked; if one is refused, none is taken); any left
-    out, and ``stream``, keeps what was passed last.  The cache, the norm's weight and the table
-    stay as prepared.  Returns ``q_rope_out``."""
+    out, and ``stream``, keeps what was passed last (no stream yet: the current one).  The cache,
+    the norm's weight and the table stay as prepared.  Returns ``q_rope_out``."""
 
     def __call__(self, latent=None, k_rope=None, q_rope=None, q_rope_out=None, cu_seqlens_q=None,
                  seq_lens_k=None, block_table=None, positions=None, stream=None):
@@ -235,8 +242,9 @@ def prepare_append_latent(latent, k_rope, cache, cu_seqlens_q, seq_lens_k, block
 class PreparedLatentAttention(_Prepared):
     """``latent_attention`` for a loop with fixed shapes, built by
     :func:`prepare_latent_attention`.  Calling it passes the step's tensors (checked; if one is
-    refused, none is taken); any left out, and ``stream``, keeps what was passed last.  The cache,
-    the sizes and the workspace stay as prepared.  Returns ``out``, or ``(out, lse)``."""
+    refused, none is taken); any left out, and ``stream``, keeps what was passed last (no stream
+    yet: the current one).  The cache, the sizes and the workspace stay as prepared.  Returns
+    ``out``, or ``(out, lse)``."""
 
     def __call__(self, q=None, cu_seqlens_q=None, seq_lens_k=None, block_table=None,
                  tree_mask=None, out=None, lse=None, stream=None):
@@ -368,9 +376,7 @@ def tree_mask(parents, cu_seqlens_q, seq_lens_k, *, max_seqlen_q: int, mask=None
                          "parents' device")
     if positions is None:
         positions = _new((total_q,), i32, dev, stream)
-    # (the handle of the current stream without the object: that costs 3 us)
-    handle = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None \
-        else stream.cuda_stream
+    handle = _handle(stream, dev.index)
     call = _lib.UaTree(parents.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens_k.data_ptr(),
                        mask.data_ptr(), positions.data_ptr(), max(step, words), num_seqs, total_q,
                        int(max_seqlen_q), words)
@@ -389,7 +395,8 @@ def tree_mask(parents, cu_seqlens_q, seq_lens_k, *, max_seqlen_q: int, mask=None
 class PreparedLatentPrefill(_Prepared):
     """``latent_prefill`` for a loop with fixed shapes, built by :func:`prepare_latent_prefill`.
     Calling it passes the step's tensors (checked; if one is refused, none is taken); any left
-    out, and ``stream``, keeps what was passed last.  Returns ``out``, or ``(out, lse)``."""
+    out, and ``stream``, keeps what was passed last (no stream yet: the current one).  Returns
+    ``out``, or ``(out, lse)``."""
 
     def __call__(self, q=None, k_nope=None, k_rope=None, v=None, cu_seqlens_q=None,
                  cu_seqlens_k=None, out=None, lse=None, stream=None):
