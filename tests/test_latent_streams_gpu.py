@@ -1,4 +1,7 @@
-"""GPU: the latent calls where the current stream is not the one that they were prepared on."""
+"""GPU: the latent calls where the current stream is not the one that they were prepared on, and
+results that prepared calls write on several streams."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -55,3 +58,63 @@ def test_captured_without_a_stream_given():
     torch.cuda.synchronize()
     check()
     assert ua.device_status() == 0
+
+
+def prepared():
+    """Prepared calls whose result the preparation allocates."""
+    i = dict(dtype=torch.int32, device="cuda")
+    x = torch.randn((3, 2, 64), device="cuda").to(BF)
+    kv = torch.zeros((4, 16, 2, 64), dtype=BF, device="cuda")
+    q, cache = torch.randn((3, 8, 576), device="cuda").to(BF), \
+        torch.zeros((4, 16, 576), dtype=BF, device="cuda")
+    cu, sl = torch.arange(4, **i), torch.tensor([5, 9, 16], **i)
+    bt = torch.tensor([[0], [1], [2]], **i)
+    e, r = torch.randn((3, 8, 256), device="cuda").to(BF), q[:, 0, :64].contiguous()
+    one = dict(max_seqlen_q=1, max_seqlen_k=16)
+    return {
+        "append": lambda **k: ua.prepare_append_latent(
+            q[:, 0, :512], q[:, 0, 512:], cache, cu, sl, bt, q_rope=q[..., 512:], **k),
+        "attention": lambda **k: ua.prepare_latent_attention(
+            q, cache, cu, sl, bt, scale=0.1, return_lse=True, **one, **k),
+        "prefill": lambda **k: ua.prepare_latent_prefill(
+            q[..., :192].contiguous(), e[..., :128], r, e[..., 128:], cu, cu, max_seqlen_q=1,
+            max_seqlen_k=1, **k),
+        "append_kv": lambda **k: ua.prepare_append(x, x, kv, kv.clone(), cu, sl, bt,
+                                                   max_seqlen_q=1, q=x, **k),
+        "unified_attention": lambda **k: ua.prepare(x, kv, kv, cu, sl, bt, **one, **k),
+    }
+
+
+# (append_kv and unified_attention keep the preparation's stream, not the current one)
+@pytest.mark.parametrize("name,how", [(n, h) for n in ("append", "attention", "prefill") for h in (
+    "a step's stream", "a foreign stream", "the current stream")] + [
+    (n, h) for n in ("append_kv", "unified_attention") for h in (
+        "a step's stream", "a foreign stream")])
+def test_a_result_outlives_the_work_of_a_steps_stream(name, how):
+    prepare = prepared()[name]
+    side = torch.cuda.Stream(priority=-1)
+
+    def other(step):
+        if how == "the current stream":
+            with torch.cuda.stream(side):
+                return step()
+        return step(stream=side if how == "a step's stream" else
+                    SimpleNamespace(cuda_stream=side.cuda_stream))
+
+    prepare()()
+    other(prepare())
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    step = prepare()
+    step()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)                    # about a tenth of a second
+    out = other(step)
+    outs = out if isinstance(out, tuple) else (out,)
+    was = [(o.data_ptr(), tuple(o.shape), o.dtype) for o in outs]
+    del out, outs, step
+    held = [torch.empty(shape, dtype=dtype, device="cuda") for _, shape, dtype in was
+            for _ in range(4)]
+    assert not side.query()                               # the step's kernel is still to run
+    assert not {at for at, _, _ in was} & {t.data_ptr() for t in held}
+    torch.cuda.synchronize()

@@ -58,10 +58,16 @@ def _new(shape, dtype, device, stream):
     `stream` is another) not handed out again before that is done with it."""
     t = torch.empty(shape, dtype=dtype, device=device)
     if stream is not None and stream.cuda_stream != torch.cuda.current_stream(device).cuda_stream:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
-        t.record_stream(stream)
+        _hold(t, stream, stream.cuda_stream)
     return t
+
+
+def _hold(t, stream, handle):
+    """Once t is dropped, its memory is not handed out again before `stream` (of this handle) is
+    done with what it was given until then."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, t.device)
+    t.record_stream(stream)
 
 
 def _shape(q, k_cache, block_table, cu_seqlens_q, max_seqlen_q, max_seqlen_k, qq_bias,
@@ -207,7 +213,7 @@ class PreparedAttention:
     (``max_seqlen_q``/``max_seqlen_k``) stay as prepared.  Returns ``out``.
     """
 
-    def __init__(self, lib, call, tensors, stream):
+    def __init__(self, lib, call, tensors, stream, made=None):
         self._lib = lib
         self._call = call
         self._ref = ctypes.byref(call)
@@ -215,6 +221,9 @@ class PreparedAttention:
         self._now = {n: (t, t.data_ptr(), t.shape) for n, t in tensors.items()}
         self._stream = stream
         self.out = tensors["out"]
+        # the result that prepare() allocated, while it is the one in use, and the last stream
+        # that it is held for
+        self._made, self._used = made, stream.cuda_stream
 
     def _take(self, new):
         for name, t in new:
@@ -224,6 +233,8 @@ class PreparedAttention:
         for name, t in new:
             setattr(self._call, name, t.data_ptr())
             self._now[name] = (t, t.data_ptr(), t.shape)
+            if name == self._made:
+                self._made = None
 
     def __call__(self, q=None, cu_seqlens_q=None, seq_lens_k=None, block_table=None, out=None,
                  stream=None):
@@ -241,7 +252,12 @@ class PreparedAttention:
             self._take(new)
         if stream is not None:
             self._stream = stream
-        rc = self._lib.ua_unified_attention_call(self._ref, self._stream.cuda_stream)
+        handle = self._stream.cuda_stream
+        if handle != self._used:
+            self._used = handle
+            if self._made is not None:
+                _hold(now[self._made][0], self._stream, handle)
+        rc = self._lib.ua_unified_attention_call(self._ref, handle)
         if rc != 0:
             raise UaError(rc, "ua_unified_attention")
         return now["out"][0]
@@ -262,6 +278,7 @@ def prepare(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *, max_s
     _, block_size, hkv, _ = k_cache.shape
     if scale is None:
         scale = 1.0 / math.sqrt(d)
+    made = "out" if out is None else None
     if out is None:
         out = _new((total_q, hq, d), out_dtype or q.dtype, q.device, stream)
     if stream is None:
@@ -278,7 +295,7 @@ def prepare(q, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *, max_s
         BACKENDS[backend])
     tensors = {"q": q, "cu_seqlens_q": cu_seqlens_q, "seq_lens_k": seq_lens_k,
                "block_table": block_table, "out": out}
-    prep = PreparedAttention(lib, call, tensors, stream)
+    prep = PreparedAttention(lib, call, tensors, stream, made)
     # the caches, score features and scales the prepared call points at stay alive with it
     prep._static = (k_cache, v_cache, alibi_slopes, qq_bias, sinks, kv_scale, k_scale_tok,
                     v_scale_tok, k_scale_blk, v_scale_blk, workspace)
@@ -436,7 +453,7 @@ class PreparedAppend:
     prepared.  Returns ``q_out``.
     """
 
-    def __init__(self, lib, call, keep, static, stream):
+    def __init__(self, lib, call, keep, static, stream, made=None):
         self._lib = lib
         self._call = call
         self._ref = ctypes.byref(call)
@@ -449,6 +466,9 @@ class PreparedAppend:
         self._device = keep["k"].device.index
         self._one_device = torch.cuda.device_count() == 1
         self._stream = stream
+        # the result that prepare_append() allocated, while it is the one in use, and the last
+        # stream that it is held for
+        self._made, self._used = made, stream.cuda_stream
 
     def _take(self, new):
         for name, t in new:
@@ -458,6 +478,8 @@ class PreparedAppend:
         for name, t in new:
             setattr(self._call, name, t.data_ptr())
             self._now[name] = (t, t.data_ptr(), t.shape, t.stride())
+            if name == self._made:
+                self._made = None
 
     def __call__(self, k=None, v=None, q=None, q_out=None, cu_seqlens_q=None, seq_lens_k=None,
                  block_table=None, positions=None, stream=None):
@@ -477,6 +499,10 @@ class PreparedAppend:
         if stream is not None:
             self._stream = stream
         handle = self._stream.cuda_stream
+        if handle != self._used:
+            self._used = handle
+            if self._made is not None:
+                _hold(now[self._made][0], self._stream, handle)
         if self._one_device or torch.cuda.current_device() == self._device:
             rc = self._lib.ua_append_kv(self._ref, handle)
         else:
@@ -501,7 +527,8 @@ def prepare_append(k, v, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table
         k_scale_blk, v_scale_blk, stream)
     if stream is None:
         stream = torch.cuda.current_stream(k.device)
-    return PreparedAppend(lib, call, keep, static, stream)
+    made = "q_out" if q is not None and q_out is None else None
+    return PreparedAppend(lib, call, keep, static, stream, made)
 
 
 def append_kv(k, v, k_cache, v_cache, cu_seqlens_q, seq_lens_k, block_table, *,

@@ -7,7 +7,7 @@ import math
 
 import torch
 
-from . import UaError, _dtype_code, _lib, _new
+from . import UaError, _dtype_code, _hold, _lib, _new
 
 
 def _strides(t, n):
@@ -73,7 +73,7 @@ class _Prepared:
     the prepared ones' shapes, strides, dtypes and device.  As long as no stream was passed, a step
     goes to the stream that is current when it is made."""
 
-    def __init__(self, what, call, tensors, static, stream):
+    def __init__(self, what, call, tensors, static, stream, made=()):
         self._what = what
         self._entry = getattr(_lib.load(), what)
         self._call = call
@@ -88,6 +88,10 @@ class _Prepared:
         self._device = dev.index
         self._one_device = torch.cuda.device_count() == 1
         self._stream = stream   # passed last, if one was
+        # the results that the preparation allocated, while they are the ones in use, and the last
+        # stream that they are held for
+        self._made = {n: tensors[n] for n in made if tensors[n] is not None}
+        self._used = _handle(stream, self._device)
 
     def _step(self, passed, stream):
         now = self._now
@@ -109,11 +113,16 @@ class _Prepared:
         if new:  # (none is taken if one was refused)
             for name, t, ptr, at in new:
                 now[name] = (t, ptr)
+                self._made.pop(name, None)
                 if ptr != at:
                     setattr(self._call, name, ptr)
         if stream is not None:
             self._stream = stream
         handle = _handle(self._stream, self._device)
+        if handle != self._used:
+            self._used = handle
+            for t in self._made.values():
+                _hold(t, self._stream, handle)
         if self._one_device or torch.cuda.current_device() == self._device:
             rc = self._entry(self._ref, handle)
         else:
@@ -234,7 +243,8 @@ def prepare_append_latent(latent, k_rope, cache, cu_seqlens_q, seq_lens_k, block
     call, tensors, static = _append_call(
         latent, k_rope, cache, cu_seqlens_q, seq_lens_k, block_table, norm_weight, norm_eps,
         q_rope, q_rope_out, cos_sin, positions, interleaved, stream)
-    return PreparedAppendLatent("ua_append_latent", call, tensors, static, stream)
+    made = ("q_rope_out",) if q_rope_out is None else ()
+    return PreparedAppendLatent("ua_append_latent", call, tensors, static, stream, made)
 
 
 # ------------------------------------------------------------------ absorbed attention
@@ -328,7 +338,8 @@ def prepare_latent_attention(q, cache, cu_seqlens_q, seq_lens_k, block_table, *,
     call, tensors, static = _attention_call(
         q, cache, cu_seqlens_q, seq_lens_k, block_table, rope_dim, scale, max_seqlen_q,
         max_seqlen_k, tree_mask, out, out_dtype, return_lse, workspace, stream)
-    return PreparedLatentAttention("ua_latent_attention", call, tensors, static, stream)
+    made = ("out", "lse") if out is None else ("lse",)
+    return PreparedLatentAttention("ua_latent_attention", call, tensors, static, stream, made)
 
 
 def latent_workspace_bytes(prepared: PreparedLatentAttention) -> int:
@@ -474,4 +485,5 @@ def prepare_latent_prefill(q, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, *,
     call, tensors, static = _prefill_call(
         q, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, out,
         out_dtype, return_lse, stream)
-    return PreparedLatentPrefill("ua_latent_prefill", call, tensors, static, stream)
+    made = ("out", "lse") if out is None else ("lse",)
+    return PreparedLatentPrefill("ua_latent_prefill", call, tensors, static, stream, made)
