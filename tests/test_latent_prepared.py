@@ -116,3 +116,18 @@ def test_results_of_the_older_calls_are_held_too(world):
         assert world.held == [(made.data_ptr(), 12)]
         step(**{name: torch.zeros_like(made)}, stream=GIVEN)
         assert len(world.held) == 1
+
+
+def test_nothing_is_taken_that_the_library_refuses(world):
+    """(It sees what the binding does not: a misaligned tensor.)"""
+    step, t = attention(GIVEN)
+    world.code = 1
+    with pytest.raises(ua.UaError):
+        step(q=torch.ones_like(t["q"]), out=torch.ones_like(t["out"]), stream=OTHER)
+    world.code = 0
+    assert step() is t["out"]
+    call, stream = world.calls[-1]
+    assert (call["q"], call["out"], stream) == (t["q"].data_ptr(), t["out"].data_ptr(), 11)
+    q = torch.ones_like(t["q"])
+    step(q=q)
+    assert world.calls[-1][0]["q"] == q.data_ptr()

@@ -110,26 +110,31 @@ class _Prepared:
             if t is not kept or ptr != at:
                 new = new or []
                 new.append((name, t, ptr, at))
-        if new:  # (none is taken if one was refused)
-            for name, t, ptr, at in new:
-                now[name] = (t, ptr)
-                self._made.pop(name, None)
+        if stream is None:
+            stream = self._stream
+        handle = _handle(stream, self._device)
+        if new:
+            for name, _, ptr, at in new:
                 if ptr != at:
                     setattr(self._call, name, ptr)
-        if stream is not None:
-            self._stream = stream
-        handle = _handle(self._stream, self._device)
-        if handle != self._used:
-            self._used = handle
-            for t in self._made.values():
-                _hold(t, self._stream, handle)
         if self._one_device or torch.cuda.current_device() == self._device:
             rc = self._entry(self._ref, handle)
         else:
             with torch.cuda.device(self._device):
                 rc = self._entry(self._ref, handle)
-        if rc != 0:
+        if rc != 0:     # (none is taken if one was refused, here or above)
+            for name, _, _, at in new or ():
+                setattr(self._call, name, at)
             raise UaError(rc, self._what)
+        if new:
+            for name, t, ptr, _ in new:
+                now[name] = (t, ptr)
+                self._made.pop(name, None)
+        self._stream = stream
+        if handle != self._used:
+            self._used = handle
+            for t in self._made.values():
+                _hold(t, stream, handle)
 
     def _last(self, name):
         return self._now[name][0]
