@@ -388,7 +388,8 @@ typedef struct {
   const float* cos_sin;         /* [max_position, rope_dim]: a row's rope_dim / 2 cosines, then its
                                    sines; 16-byte aligned; NULL: no rotation */
   const int32_t* positions;     /* [total_q], or NULL: a token's place in the cache */
-  int64_t latent_stride;        /* token strides and q_rope's head strides: multiples of 8 */
+  int64_t latent_stride;        /* token strides and q_rope's head strides: multiples of 8 (any
+                                   where there is one token, or one head) */
   int64_t k_rope_stride;
   int64_t q_rope_stride[2];     /* token, head */
   int64_t q_rope_out_stride[2];

@@ -198,7 +198,8 @@ __global__ void __launch_bounds__(128, 6)
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-bool stride8(int64_t s) { return s >= 0 && s % 8 == 0; }
+// A stride between n rows that are read in 16-byte chunks (one row has none).
+bool stride8(int64_t s, int64_t n) { return n <= 1 || (s >= 0 && s % 8 == 0); }
 
 int append(const ua_append_latent_t& a, cudaStream_t st) {
   if (a.num_seqs < 0 || a.total_q < 0 || a.max_blocks_per_seq < 0 || a.num_blocks < 0 ||
@@ -221,11 +222,14 @@ int append(const ua_append_latent_t& a, cudaStream_t st) {
                         static_cast<const void*>(a.cache)})
     if (!aligned(x, 16)) return UA_ERR_INVALID_ARG;
   if (!aligned(a.positions, 4)) return UA_ERR_INVALID_ARG;
-  if (!stride8(a.latent_stride) || !stride8(a.k_rope_stride)) return UA_ERR_INVALID_ARG;
+  if (!stride8(a.latent_stride, a.total_q) || !stride8(a.k_rope_stride, a.total_q))
+    return UA_ERR_INVALID_ARG;
   if (a.q_rope) {
-    for (int i = 0; i < 2; ++i)
-      if (!stride8(a.q_rope_stride[i]) || !stride8(a.q_rope_out_stride[i]))
+    for (int i = 0; i < 2; ++i) {
+      const int64_t n = i == 0 ? a.total_q : a.num_heads;
+      if (!stride8(a.q_rope_stride[i], n) || !stride8(a.q_rope_out_stride[i], n))
         return UA_ERR_INVALID_ARG;
+    }
     // what is written may not overlap itself
     const bool head_in = a.q_rope_out_stride[1] <= a.q_rope_out_stride[0];
     const int64_t inner = a.q_rope_out_stride[head_in ? 1 : 0];
