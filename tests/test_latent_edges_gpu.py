@@ -58,3 +58,24 @@ def test_a_step_with_a_misaligned_tensor_leaves_the_call_as_it_was():
     assert e.value.code == 1
     step._last("out").zero_()
     assert torch.equal(step(), want)
+
+
+def test_a_step_in_place_with_other_strides_is_refused():
+    """Prepared apart, where the strides may differ, and then given one memory for both."""
+    args = batch([3, 2], [40, 90])
+    down, cache = rand(5, L + R), torch.zeros((8, 64, L + R), dtype=BF, device="cuda")
+    table = ua.rope_table(100, R)
+    whole = rand(5, 16, 128 + R, seed=1)
+    q = whole[..., 128:]
+    step = ua.prepare_append_latent(down[:, :L], down[:, L:], cache, *args, q_rope=q, cos_sin=table)
+    want = step().clone()
+    before = whole.clone()
+    room = whole.flatten()[128:128 + want.numel()].view(want.shape)     # q's address, its own strides
+    assert room.data_ptr() == q.data_ptr()
+    with pytest.raises(ua.UaError):
+        step(q_rope_out=room)
+    assert torch.equal(whole, before)
+    same = ua.prepare_append_latent(down[:, :L], down[:, L:], cache, *args, q_rope=q,
+                                    q_rope_out=torch.zeros_like(whole)[..., 128:], cos_sin=table)
+    assert torch.equal(same(q_rope_out=q), want)
+    assert torch.equal(whole[..., :128], before[..., :128])

@@ -229,6 +229,9 @@ int append(const ua_append_latent_t& a, cudaStream_t st) {
       const int64_t n = i == 0 ? a.total_q : a.num_heads;
       if (!stride8(a.q_rope_stride[i], n) || !stride8(a.q_rope_out_stride[i], n))
         return UA_ERR_INVALID_ARG;
+      // in place, a row is read and written by the same lanes
+      if (a.q_rope_out == a.q_rope && n > 1 && a.q_rope_out_stride[i] != a.q_rope_stride[i])
+        return UA_ERR_INVALID_ARG;
     }
     // what is written may not overlap itself
     const bool head_in = a.q_rope_out_stride[1] <= a.q_rope_out_stride[0];

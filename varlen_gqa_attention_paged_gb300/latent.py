@@ -179,7 +179,8 @@ def _append_call(latent, k_rope, cache, cu_seqlens_q, seq_lens_k, block_table, n
         if q_rope_out is None:
             q_rope_out = _new(shape, dt, dev, stream)
         _rows("q_rope_out", q_rope_out, shape, dt, dev)
-        if q_rope_out.data_ptr() == q_rope.data_ptr() and q_rope_out.stride() != q_rope.stride():
+        if q_rope_out.data_ptr() == q_rope.data_ptr() and any(
+                n > 1 and x != y for n, x, y in zip(shape, q_rope.stride(), q_rope_out.stride())):
             raise ValueError("q_rope_out in q_rope's place must have its strides")
         a.q_rope, a.q_rope_out = q_rope.data_ptr(), q_rope_out.data_ptr()
         a.q_rope_stride, a.q_rope_out_stride = _strides(q_rope, 2), _strides(q_rope_out, 2)
