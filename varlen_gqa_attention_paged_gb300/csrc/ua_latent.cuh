@@ -276,7 +276,7 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
-// ln of a row's sum: m its running max in log2 units, l the sum of 2^(x - m).
+// ln of a row's sum: m its reference in log2 units, l the sum of 2^(x - m).
 __device__ __forceinline__ float latent_lse(float m, float l) {
   return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
@@ -617,6 +617,7 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
     const uint32_t lane_off = (32u * quad) << 16;
     const uint32_t tO = tmem + C::kTmemO + lane_off;
     const float c = p.scale * kLog2e;
+    constexpr float kDown = latent_down(BF16), kRoom = 8.f + kDown;
     // (of O's 32-column pieces, the warps of a lane quarter take every other 128-element block, or,
     // with one block, a piece each)
     auto mine = [&](int piece) { return (C::kMB > 1 ? piece >> 1 & 1 : piece & 1) == half; };
@@ -672,9 +673,9 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
             }
           }
         }
-        // The running max moves only by more than 8 in log2 units (P stays <= 256, inside f16's
-        // range and fp32 sums'), or to a row's first key.  That is rare, so the exponentials are
-        // taken with the old max while the column halves hear from each other whether it moves.
+        // The reference m (the running max, in f16 kDown below it) moves only when the max is more
+        // than kRoom above it, or at a row's first key.  That is rare, so the exponentials are
+        // taken with the old one while the column halves hear from each other whether it moves.
         float top[2];
         bool grow = false;
 #pragma unroll
@@ -685,7 +686,7 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
             t = fmax3(t, __uint_as_float(x[4 * g + 2 * k]), __uint_as_float(x[4 * g + 2 * k + 1]));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
           top[k] = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2)) * c;
-          grow = grow || (rv[k] && (top[k] > m[k] + 8.f || (m[k] == -INFINITY && top[k] > -INFINITY)));
+          grow = grow || (rv[k] && (top[k] > m[k] + kRoom || (m[k] == -INFINITY && top[k] > -INFINITY)));
         }
         float* const tops = sT + (it & 1) * 2 * kLatRows;
         if (cq == 0) {
@@ -696,8 +697,8 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
           reinterpret_cast<int*>(s_grow[it & 1])[warp] = it + 1;
         __syncwarp();
         if (lane == 0) mbar_arrive(grown);
-        // P rounded to 16 bits for the MMA (half a step of 2^-8 or 2^-11 of each weight); the sum
-        // is of the unrounded weights
+        // P rounded to 16 bits for the MMA (half a step of 2^-8 or 2^-11 of each weight, in f16 at
+        // least 2^-32 of the largest); the sum is of the unrounded weights
         uint32_t pk[8];  // [row][g]
         float add[2];
         auto weights = [&]() {
@@ -730,9 +731,9 @@ __global__ void __launch_bounds__(LatentCfg<L>::kThreads, 1)
           for (int k = 0; k < 2; ++k) {
             const float t = fmaxf(top[k], tops[(half ^ 1) * kLatRows + ra + 8 * k]);
             float alpha = 1.f;
-            if (rv[k] && (t > m[k] + 8.f || (m[k] == -INFINITY && t > -INFINITY))) {
-              alpha = m[k] == -INFINITY ? 0.f : fast_exp2(m[k] - t);
-              m[k] = t;
+            if (rv[k] && (t > m[k] + kRoom || (m[k] == -INFINITY && t > -INFINITY))) {
+              alpha = m[k] == -INFINITY ? 0.f : fast_exp2(m[k] - (t - kDown));
+              m[k] = t - kDown;
             }
             l[k] *= alpha;
             if (half == 0 && cq == 0) f[ra + 8 * k] = alpha;

@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
     const int see = min(k_len, ctx + i_q + 1);  // keys that the row sees
     const int clear = min(k_len, ctx + t_first + qt * BM + 32 * quad + 1);  // and all of the warp's
     const float c = p.scale * kLog2e;
+    constexpr float kDown = latent_down(BF16), kRoom = 8.f + kDown;
     const uint32_t tS = tmem + qt * C::kTmemStride + ((32u * quad) << 16);
     const uint32_t tO = tS + BN;
     const bool hands_on = quad == 0 && qt == (n1 > 0 ? 1 : 0);
@@ -427,13 +428,13 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
           mx[g] = fmax3(mx[g], __uint_as_float(s[g][e]), __uint_as_float(s[g][e + 1]));
       }
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-      // The running max moves only by more than 8 in log2 units (P stays <= 256, inside f16's
-      // range and fp32 sums'), or to a row's first key.
+      // The reference m (the running max, in f16 kDown below it) moves only when the max is more
+      // than kRoom above it, or at a row's first key.
       float alpha = 1.f;
-      const bool grow = top > m + 8.f || (m == -INFINITY && top > -INFINITY);
+      const bool grow = top > m + kRoom || (m == -INFINITY && top > -INFINITY);
       if (grow) {
-        alpha = m == -INFINITY ? 0.f : fast_exp2(m - top);
-        m = top;
+        alpha = m == -INFINITY ? 0.f : fast_exp2(m - (top - kDown));
+        m = top - kDown;
       }
       // (O holds P.V up to the tile before: the commit of this tile's S covered it)
       if (n > 0 && __any_sync(0xffffffffu, grow)) {
@@ -450,8 +451,8 @@ __global__ void __launch_bounds__(LatentPrefillCfg<N, V>::kThreads, 1)
       const float mu = m == -INFINITY ? 0.f : m;
       const float2 cc = make_float2(c, c), mm = make_float2(-mu, -mu);
       float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-      // P rounded to 16 bits for the MMA (half a step of 2^-8 or 2^-11 of each weight); the sum is
-      // of the unrounded weights
+      // P rounded to 16 bits for the MMA (half a step of 2^-8 or 2^-11 of each weight, in f16 at
+      // least 2^-32 of the largest); the sum is of the unrounded weights
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         uint32_t pk[16];

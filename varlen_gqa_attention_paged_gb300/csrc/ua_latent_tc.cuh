@@ -29,6 +29,13 @@ __device__ __forceinline__ void umma_f16_ss_at(uint32_t d_tmem, uint32_t a16, ui
       : "memory");
 }
 
+// How far below a row's running max its weights' reference m is, in log2 units.  Weights are
+// 2^(x - m), and m moves when the max is more than 8 above where it was, so they reach 2^8 in bf16 and
+// 2^15 in f16 (inside its range, and fp32 sums').  In f16 the largest weight is 2^7 at least then, and
+// the smallest steps, 2^-24, are 2^-31 of that.  (With m at the max itself they were 2^-24 of it: tens
+// of thousands of keys below 2^-25 counted in the sum and not in the output.)
+__host__ __device__ constexpr float latent_down(bool bf16) { return bf16 ? 0.f : 7.f; }
+
 // A shared-memory address as descriptors have it, in 16-byte units.  (In a CTA of a cluster the bits
 // above the window's 18 hold its rank, which would land in the leading byte offset.)
 __device__ __forceinline__ uint32_t smem_units(const void* at) {
