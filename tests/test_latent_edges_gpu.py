@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import varlen_gqa_attention_paged_gb300 as ua
+from tests import test_append_latent_gpu as appended
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +80,9 @@ def test_a_step_in_place_with_other_strides_is_refused():
                                     q_rope_out=torch.zeros_like(whole)[..., 128:], cos_sin=table)
     assert torch.equal(same(q_rope_out=q), want)
     assert torch.equal(whole[..., :128], before[..., :128])
+
+
+@pytest.mark.parametrize("tokens", [404, 408, 480, 540, 544])
+def test_appends_where_a_warp_takes_one_pass_and_where_four(tokens):
+    """About as many warps as 152 SMs hold, with a pass of query heads each."""
+    appended.compare(appended.make([(tokens, tokens + 5), (1, 70)], 64), True)

@@ -39,15 +39,17 @@ struct AppendLatentParams {
   float eps;
 };
 
+constexpr int kWarps = 4, kBlocks = 6;  // warps of a block, blocks of an SM
+
 template <int L, bool BF>
-__global__ void __launch_bounds__(128, 6)
+__global__ void __launch_bounds__(32 * kWarps, kBlocks)
     ua_append_latent_kernel(const __grid_constant__ AppendLatentParams p) {
   constexpr int kPer = (L + 255) / 256;  // 16-byte chunks of the latent that a lane takes
   constexpr int U = 4;                   // passes whose loads are in flight together
   ua::grid_dependency_wait();
   ua::grid_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const long long task = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const long long task = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int t = static_cast<int>(task / p.warps_per_token);
   const int part = static_cast<int>(task % p.warps_per_token);
   if (t >= p.total_q) return;
@@ -279,13 +281,15 @@ int append(const ua_append_latent_t& a, cudaStream_t st) {
   p.lanes = a.rope_dim / 16;
   p.heads_per_pass = 32 / p.lanes;
   const int passes = (p.heads + p.heads_per_pass - 1) / p.heads_per_pass;
-  // a warp a pass while they fit the device at once, else four
-  const long long resident = 32LL * sms;
+  // A pass a warp while all warps fit the device at once, else four: in us, 64 heads (9 warps a token
+  // if one pass each), 400 tokens (23.7 warps an SM) 3.3 with one; 416 (24.6) 3.1 with four, 4.2 with
+  // one; 480 (28.4) 3.1, 4.5; 536 (31.7) 3.2, 4.7.
+  const long long resident = static_cast<long long>(kWarps) * kBlocks * sms;
   p.pass_group = static_cast<long long>(a.total_q) * (1 + passes) <= resident ? 1 : 4;
   p.warps_per_token = 1 + (passes + p.pass_group - 1) / p.pass_group;
-  const long long grid = (static_cast<long long>(a.total_q) * p.warps_per_token + 3) / 4;
+  const long long grid = (static_cast<long long>(a.total_q) * p.warps_per_token + kWarps - 1) / kWarps;
   if (grid > INT_MAX) return UA_ERR_INVALID_ARG;
-  const dim3 g(static_cast<unsigned>(grid)), t(128);
+  const dim3 g(static_cast<unsigned>(grid)), t(32 * kWarps);
   const bool bf = a.dtype == UA_DT_BF16;
   decltype(&ua_append_latent_kernel<512, true>) kern;
   switch (a.latent_dim) {
