@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import varlen_gqa_attention_paged_gb300 as ua
+from tests import _latent_ref as ref
 from tests import test_append_latent_gpu as appended
 
 pytestmark = pytest.mark.gpu
@@ -86,3 +87,33 @@ def test_a_step_in_place_with_other_strides_is_refused():
 def test_appends_where_a_warp_takes_one_pass_and_where_four(tokens):
     """About as many warps as 152 SMs hold, with a pass of query heads each."""
     appended.compare(appended.make([(tokens, tokens + 5), (1, 70)], 64), True)
+
+
+@pytest.mark.parametrize("most", [0, 1 << 20])
+def test_prefill_of_no_keys_at_all(most):
+    cu = torch.tensor([0, 3, 3, 200], dtype=torch.int32, device="cuda")
+    q, kv = rand(200, 4, 128 + R), rand(0, 4, 256)
+    out, lse = ua.latent_prefill(q, kv[..., :128], rand(0, R), kv[..., 128:], cu, torch.zeros_like(cu),
+                                 max_seqlen_q=197, max_seqlen_k=most, return_lse=True,
+                                 out=torch.full((200, 4, 128), 7.0, dtype=BF, device="cuda"))
+    assert torch.all(out == 0) and torch.all(lse == -float("inf"))
+    assert ua.device_status() == 0
+
+
+def test_sequences_that_share_blocks_and_slots_of_the_batch_that_are_empty():
+    """A prefix in the tables of three sequences; sequences without tokens whose lengths are left over
+    from before; both ways of cutting the keys."""
+    lens = [(1, 300), (3, 290), (1, 256), (0, 999), (0, 70), (0, 1)]
+    cu = torch.tensor([0, 1, 4, 5, 5, 5, 5]).int()
+    sl = torch.tensor([k for _, k in lens]).int()
+    bt = torch.tensor([[2, 0, 5, 1, 7], [2, 0, 5, 1, 3], [2, 0, 5, 1, -1]] + [[-1] * 5] * 3).int()
+    q, cache = rand(9, 16, L + R), rand(8, 64, L + R, seed=1)
+    want, wlse, tol, ltol = ref.attend(q.cpu(), cache.cpu(), cu[:4], sl[:3], bt[:3], L, 0.08)
+    for most in (300, (1 << 31) - 1):
+        out = torch.full((9, 16, L), 7.0, dtype=BF, device="cuda")
+        out, lse = ua.latent_attention(q, cache, cu.cuda(), sl.cuda(), bt.cuda(), scale=0.08,
+                                       max_seqlen_q=3, max_seqlen_k=most, out=out, return_lse=True)
+        ref.check(out[:5], want[:5], tol[:5], BF)
+        ref.check(lse[:5], wlse[:5], ltol[:5], torch.float32)
+        assert torch.all(out[5:] == 7)
+    assert ua.device_status() == 0
