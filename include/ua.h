@@ -384,7 +384,9 @@ typedef struct {
   const int32_t* cu_seqlens_q;  /* [num_seqs + 1] */
   const int32_t* seq_lens_k;    /* [num_seqs]: lengths with the new tokens */
   const int32_t* block_table;   /* [num_seqs, max_blocks_per_seq] */
-  const void* norm_weight;      /* [latent_dim] of norm_dtype, or NULL: latents are stored as they are */
+  const void* norm_weight;      /* [latent_dim] of norm_dtype, 16-byte aligned (as latent, k_rope,
+                                   q_rope, q_rope_out and cache), or NULL: latents are stored as
+                                   they are */
   const float* cos_sin;         /* [max_position, rope_dim]: a row's rope_dim / 2 cosines, then its
                                    sines; 16-byte aligned; NULL: no rotation */
   const int32_t* positions;     /* [total_q], or NULL: a token's place in the cache */
@@ -444,7 +446,10 @@ typedef struct {
  */
 int ua_tree_mask(const ua_tree_t* call, void* stream);
 
-/* One ua_latent_attention call.  Tensors are contiguous. */
+/*
+ * One ua_latent_attention call.  Tensors are contiguous; q, cache, out and workspace are 16-byte
+ * aligned; out and lse overlap none of the others.
+ */
 typedef struct {
   const void* q;                /* [total_q, num_heads, latent_dim + rope_dim] of `dtype` */
   const void* cache;            /* [num_blocks, block_size, latent_dim + rope_dim] of `dtype` */
@@ -492,7 +497,11 @@ int ua_latent_attention(const ua_latent_t* call, void* stream);
 /* Bytes of scratch that the call needs on the current device (0: none, or an invalid argument). */
 size_t ua_latent_workspace_bytes(const ua_latent_t* call);
 
-/* One ua_latent_prefill call.  Strides are in elements: multiples of 8 (the last dim has stride 1). */
+/*
+ * One ua_latent_prefill call.  Strides are in elements: multiples of 8, not 0 (the last dim has stride
+ * 1; a dim of one element may have any).  q, k_nope, k_rope, v and out are 16-byte aligned; out and lse
+ * overlap none of the others.
+ */
 typedef struct {
   const void* q;                /* [total_q, num_heads, nope_dim + rope_dim] of `dtype` */
   const void* k_nope;           /* [total_k, num_heads, nope_dim] */
@@ -526,6 +535,7 @@ typedef struct {
  * keys.  For row i of a sequence of q_len queries and k_len keys, at position p = k_len - q_len + i:
  *   s_j = scale * (q_nope . k_nope_j + q_rope . k_rope_j),  j <= p,   out = softmax(s) v
  * A row that sees no key is written as 0.  Rows past cu_seqlens_q[num_seqs] stay as they are.
+ * Returns UA_ERR_UNSUPPORTED where total_q / 256 + num_seqs passes 65535.
  */
 int ua_latent_prefill(const ua_latent_prefill_t* call, void* stream);
 

@@ -8,8 +8,8 @@
 // latent and rope key, or some of its query heads: rope_dim / 16 lanes a head, each with both
 // 16-byte chunks of its eight pairs, 32 / (rope_dim / 16) heads a pass.
 //
-// Measured (one GB300): 4 prompts of 2048 tokens, L 512, R 64, 64 query heads, bf16: 29.0 us for 153
-// MB, 5.3 TB/s (0.78 of a copy; six blocks of four warps an SM, of 80 registers; seven 29.2, eight,
+// Measured (one GB300): 4 prompts of 2048 tokens, L 512, R 64, 64 query heads, bf16: 29.4 us for 153
+// MB, 5.2 TB/s (0.77 of a copy; six blocks of four warps an SM, of 80 registers; seven 29.2, eight,
 // which spill, 35.4); one token of each of 32 sequences 2.4 us in a captured graph.
 #include <algorithm>
 #include <climits>

@@ -1,5 +1,5 @@
-// ua_latent.cu -- latent attention, absorbed form: argument checks and launches, the merge of
-// row tiles that several workers shared, and the masks of drafted trees.
+// ua_latent.cu -- latent attention, absorbed form: argument checks and launches, and the merge of
+// row tiles that several workers shared.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -299,7 +299,11 @@ int check(const ua_latent_t& a) {
 }
 
 // CTAs of a worker and workers of a call on `sms` SMs, from the host's sizes (a bound of the work:
-// the kernel takes its shares from the lengths themselves).
+// the kernel takes its shares from the lengths themselves).  Workers of two CTAs are one choice for the
+// batch, made by its longest sequence of new tokens: a sequence of an odd number of row tiles leaves
+// the second CTA of a pair without rows on its walk, single tokens among chunks above all (a chunk of
+// 64 tokens behind 2,496 and 63 single tokens over 4,000 keys, 16 heads: 114.8 us, where the two as
+// calls of their own take 22.2 and 64.2; a chunk of 512: 163.0, 75.3 and 64.5).
 constexpr int kMinShare = 2;
 // Few row tiles over few keys take a cluster of up to kSpread CTAs each instead (`spread` CTAs; 0: even
 // shares), with an even part of the keys a CTA: that saves the merge kernel and the second row tile

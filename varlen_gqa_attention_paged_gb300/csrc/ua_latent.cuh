@@ -23,9 +23,9 @@
 //
 // Measured (one GB300, bf16, L 512, R 64): 64 sequences of up to 8191 keys, 16 heads, 75 us with the
 // merge, 4.9 TB/s (0.72 of a copy; start, last share and merge are 12 us of it); 32 x 6000 keys, 128
-// heads, 84.6 us, 632 TFLOP/s (0.34 of cuBLAS: the tensor cores are busy 45 % of the time, a tile takes
+// heads, 85.7 us, 624 TFLOP/s (0.33 of cuBLAS: the tensor cores are busy 45 % of the time, a tile takes
 // 3060 cycles of which its products need 1940; two tiles in shared memory leave the chain of copy
-// (1400), Q K^T, softmax (1400) and P.V bare); 16 heads, one token, 700 keys 10.7 us (launch and one
+// (1400), Q K^T, softmax (1400) and P.V bare); 16 heads, one token, 700 keys 10.1 us (launch and one
 // chain).
 #pragma once
 

@@ -104,7 +104,9 @@ int prefill(const ua_latent_prefill_t& a, cudaStream_t st) {
   p.slots = static_cast<int>(slots);
   p.scale = a.scale;
   p.parts = parts(a, slots, sms);
-  // (where all start at once, or all are short, the order is nothing: it costs 500 cycles)
+  // (where all start at once, or all are short, the order is nothing: it costs 500 cycles.  A lane ranks
+  // two slots; past 64 they start in reverse order of the batch: 118 slots of 4 heads, prompts of 3,000
+  // and 2,000 tokens and 70 of 100, take 52.6 us with the long ones last in it and 64.7 with them first)
   p.by_length = slots <= 64 && slots * a.num_heads > sms && a.max_seqlen_k > 2 * kBlockTokens;
   const auto launch =
       a.nope_dim == 64 ? ua::launch_latent_prefill_n64 : ua::launch_latent_prefill_n128;

@@ -18,10 +18,11 @@
 // Where q-blocks are few, a cluster of two or four CTAs shares the keys of each (SPLIT), and their rows
 // meet through distributed shared memory.
 //
-// Measured (one GB300, N = V = 128, R = 64): two prompts of 8192, 16 heads, bf16 450 us, 1530 TFLOP/s
-// (0.81 of cuBLAS; tensor cores busy 66 % of the time); five chunks of up to 1901 behind prefixes, 8
-// heads, f16 56 us (0.45: 200 CTAs on 152 SMs, the longest alone takes 45 of the mean SM's 34.5 steps);
-// 64 tokens behind 3936, 16 heads 19.1 us (one CTA a q-block 54.4).
+// Measured (one GB300, N = V = 128, R = 64): two prompts of 8192, 16 heads, bf16 479 to 486 us in turn
+// with other work, 1413 to 1436 TFLOP/s (0.75 of cuBLAS; alone, at a higher clock, 448 us; tensor cores
+// busy 66 % of the time); five chunks of up to 1901 behind prefixes, 8 heads, f16 58 us (0.44: 216 CTAs
+// with work on 152 SMs, the longest alone takes 45 of the mean SM's 34.5 steps); 64 tokens behind 3936,
+// 16 heads 20.5 us (one CTA a q-block 54.4).
 #pragma once
 
 #include <atomic>
