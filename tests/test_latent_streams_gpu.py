@@ -118,3 +118,29 @@ def test_a_result_outlives_the_work_of_a_steps_stream(name, how):
     assert not side.query()                               # the step's kernel is still to run
     assert not {at for at, _, _ in was} & {t.data_ptr() for t in held}
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("name", ["append", "attention", "prefill"])
+def test_results_of_the_preparation_in_a_capture(name):
+    """Made outside the capture, written by its stream, read after replays, dropped in its time."""
+    step = prepared()[name]()
+
+    def outs():
+        out = step()
+        return out if isinstance(out, tuple) else (out,)
+
+    want = [o.clone() for o in outs()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = outs()
+    for o in got:
+        o.zero_()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del graph, got, step
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    assert ua.device_status() == 0
